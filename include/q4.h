@@ -59,7 +59,8 @@ enum {
     Q4_ERR_ALIGN = 3,     /* a device pointer is not 16-byte aligned           */
     Q4_ERR_WORKSPACE = 4, /* workspace missing or smaller than required        */
     Q4_ERR_HIP = 5,       /* a HIP call failed; see q4_last_hip_error()        */
-    Q4_ERR_FORMAT = 6,    /* a GGUF file is malformed or uses an unknown form  */
+    Q4_ERR_FORMAT = 6,    /* a GGUF file is malformed or uses an unknown form;
+                             an element type an operator does not take       */
     Q4_ERR_IO = 7,        /* a file could not be opened or read                */
     Q4_ERR_NOT_FOUND = 8  /* no such tensor / metadata key / index             */
 };
@@ -307,6 +308,64 @@ const char* q4_matvec_route(int64_t N, int64_t K, int32_t argmax);
  */
 q4_status q4_quantize(const float* w, void* w_q4, int64_t N, int64_t K,
                       int32_t* flag, void* stream);
+
+/*
+ * Operators that adapt a frozen Q4_0 model (section "Architecture": the
+ * quantised projections and their widths): the projections and the head stay
+ * in Q4_0, low-rank adapters beside them are served and trained.
+ *
+ * Element types: activations (x, dy, r, y, dx) share one type, Q4_TYPE_F32,
+ * Q4_TYPE_F16 or Q4_TYPE_BF16; the adapters' type is that one, or
+ * Q4_TYPE_F32, or, with float32 activations, any of the three
+ * (Q4_ERR_FORMAT otherwise).  Sums are float32 whatever the types, and each
+ * output is rounded once.
+ */
+enum { Q4_TYPE_F32 = 0, Q4_TYPE_F16 = 1, Q4_TYPE_BF16 = 30 };
+
+/*
+ * q4_lora -- low-rank adapters of many requests at once beside a shared
+ * projection: y[m] = r[m] + s_a B_a (A_a x[m]) with a = ids[m].  With y as
+ * the r of q4_matmul_residual (in place) the projection itself is added.
+ *   x     : [M, K].   r : [M, N], y itself (in place) or a buffer that does
+ *           not overlap it; NULL: zeros.   y : [M, N].
+ *   a, b  : A [adapters, R, K] and B [adapters, N, R].
+ *   scale : adapters float32 factors s_a, or NULL (ones).
+ *   ids   : M int32 (device).  A row whose id is outside [0, adapters) has
+ *           no adapter: y = r there, and its x is not used.
+ *   1 <= M <= 65535*128, 1 <= N <= 4194304, K a positive multiple of 32 up to
+ *   4194304, R a multiple of 8 from 8 to 128, 1 <= adapters <= 65535.
+ *   workspace : q4_lora_workspace_bytes(M, N, K, R) bytes of device scratch;
+ *           its contents do not matter.  Calls that share it must be ordered.
+ * Two launches; A_a x is kept in float32.  Deterministic, and a row's result
+ * does not depend on the other rows of its call.
+ */
+size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
+q4_status q4_lora(const void* x, const void* a, const void* b, const float* scale,
+                  const int32_t* ids, const void* r, void* y, int32_t type, int32_t atype,
+                  int64_t M, int64_t N, int64_t K, int64_t R, int64_t adapters,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * q4_lora_grad -- the gradient of q4_lora for dy, the gradient of its y:
+ *   g[m] = s_a B_a^T dy[m],   dx[m] = r[m] + A_a^T g[m],
+ *   da[a] = sum g[m] x[m]^T,  db[a] = sum s_a dy[m] (A_a x[m])^T, the sums
+ * over the rows m with ids[m] == a.
+ *   x, dy : [M, K], [M, N].   dx : [M, K] or NULL.   r : [M, K] (the gradient
+ *           that reaches x otherwise, as q4_matmul_dx gives it), dx itself,
+ *           or NULL: zeros.
+ *   da, db: [adapters, R, K] and [adapters, N, R] float32, written (not
+ *           accumulated; zeros for an adapter without rows), or NULL.  At
+ *           least one of dx, da, db is given.
+ *   Rows without an adapter: dx = r, nothing to da and db.  s_a is a constant.
+ *   Ranges as for q4_lora, and adapters * (ceil(K/64) + ceil(N/64)) <= 2^21.
+ * Two launches.  Deterministic.
+ */
+size_t q4_lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
+q4_status q4_lora_grad(const void* x, const void* dy, const void* a, const void* b,
+                       const float* scale, const int32_t* ids, const void* r, void* dx,
+                       float* da, float* db, int32_t type, int32_t atype, int64_t M, int64_t N,
+                       int64_t K, int64_t R, int64_t adapters, void* workspace, size_t ws_bytes,
+                       void* stream);
 
 /*
  * GGUF reader (host code, no GPU) -- the container of the pages' quantised

@@ -12,6 +12,8 @@ Entry points (same names as the C ABI, minus the ``q4_`` prefix):
     embed_rows(table_q4, ids, out=None)          rows of deq(T)
     lmhead_argmax(w_q4, x, workspace=None, ...)  argmax_n (deq(T) x)_n
     quantize(w, out=None, check=True)            float32 -> Q4_0 bytes
+    lora(x, a, b, ids, scale=None, r=None, ...)  y = r + s_a B_a (A_a x), a = ids[row]
+    lora_grad(x, dy, a, b, ids, ...)             its gradient: dx, da, db
 
 Q4_0 tensors are ``torch.uint8`` of shape [N, 18*K/32] (rows of 32-weight
 blocks: binary16 scale + 16 bytes of nibbles, as stored in GGUF).
@@ -68,6 +70,10 @@ _SIGS = {
     "q4_decode_chain": ([_P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "q4_matmul_route": ([_I64, _I64, _I64, _SZ, _P], ctypes.c_char_p),
     "q4_matvec_route": ([_I64, _I64, ctypes.c_int32], ctypes.c_char_p),
+    "q4_lora_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
+    "q4_lora": ([_P] * 7 + [ctypes.c_int32] * 2 + [_I64] * 5 + [_P, _SZ, _P], ctypes.c_int),
+    "q4_lora_grad_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
+    "q4_lora_grad": ([_P] * 10 + [ctypes.c_int32] * 2 + [_I64] * 5 + [_P, _SZ, _P], ctypes.c_int),
     "q4_gguf_open": ([_P, _I64, _P], ctypes.c_int),
     "q4_gguf_close": ([_P], None),
     "q4_gguf_version": ([_P], ctypes.c_uint32),
@@ -392,6 +398,113 @@ def quantize(w: torch.Tensor, out: torch.Tensor | None = None, check: bool = Tru
     if bad:
         raise ValueError("q4_quantize: non-finite input or a scale overflowing binary16")
     return out
+
+
+# Element types of the operators that adapt a frozen model (Q4_TYPE_* of the ABI).
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}
+
+
+def _addr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dtype=None) -> None:
+    """A contiguous tensor of `shape` with `dtype` (any activation type if None)."""
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    if (t.dtype != dtype) if dtype is not None else (t.dtype not in _TYPES):
+        raise ValueError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+
+
+def _same_gpu(*ts) -> None:
+    """Every tensor on the current GPU (the library launches on the current device)."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.get_device() == cur):
+            raise ValueError("tensors must live on the current GPU")
+
+
+def _scratch(workspace, nbytes: int, device):
+    """The caller's uint8 workspace, or one of `nbytes` from the current stream's pool."""
+    if workspace is None or workspace is True:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def _adapters(x, a, b, ids, scale):
+    """(M, N, K, R, adapters) of a low-rank adapter call."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [M, K], a [adapters, R, K] and b [adapters, N, R]")
+    m, k = x.shape
+    na, r = a.shape[:2]
+    n = b.shape[1]
+    _matrix(x, "x", (m, k))
+    _matrix(a, "a", (na, r, k))
+    _matrix(b, "b", (na, n, r), a.dtype)
+    _matrix(ids, "ids", (m,), torch.int32)
+    if scale is not None:
+        _matrix(scale, "scale", (na,), torch.float32)
+    return m, n, k, r, na
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
+         scale: torch.Tensor | None = None, r: torch.Tensor | None = None,
+         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """y[m] = r[m] + scale[i] B_i (A_i x[m]) with i = ids[m]: low-rank adapters of many
+    requests at once.  x is [M, K] (float32, float16 or bfloat16), a [adapters, R, K] and
+    b [adapters, N, R] (x's type, or float32; with a float32 x any of the three), ids int32
+    [M]; an id outside [0, adapters) leaves y = r.  r (zeros if None) may be ``out``.
+    With ``matmul_residual(w, x, y, out=y)`` after it, y is the adapted projection."""
+    m, n, k, rank, na = _adapters(x, a, b, ids, scale)
+    if r is not None:
+        _matrix(r, "r", (m, n), x.dtype)
+    if out is not None:
+        _matrix(out, "out", (m, n), x.dtype)
+    _same_gpu(x, a, b, ids, scale, r, out, workspace if workspace is not True else None)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        ws = _scratch(workspace, lib().q4_lora_workspace_bytes(m, n, k, rank), x.device)
+        _check(lib().q4_lora(_addr(x), _addr(a), _addr(b), _addr(scale), _addr(ids), _addr(r),
+                             _addr(out), _TYPES[x.dtype], _TYPES[a.dtype], m, n, k, rank, na,
+                             _addr(ws), ws.numel(), _stream(stream)), "q4_lora")
+    return out
+
+
+def lora_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+              ids: torch.Tensor, scale: torch.Tensor | None = None, r: torch.Tensor | None = None,
+              dx: torch.Tensor | None = None, da: torch.Tensor | None = None,
+              db: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dx, da, db): the gradient of ``lora`` for dy [M, N], the gradient of its y.
+    dx = r + scale A^T B^T dy row by row (x's type; r zeros if None, or the gradient
+    through the projection itself, may be ``dx``); da and db are float32, summed over
+    the rows of each adapter, zeros for one without rows."""
+    m, n, k, rank, na = _adapters(x, a, b, ids, scale)
+    _matrix(dy, "dy", (m, n), x.dtype)
+    if r is not None:
+        _matrix(r, "r", (m, k), x.dtype)
+    if dx is not None:
+        _matrix(dx, "dx", (m, k), x.dtype)
+    if da is not None:
+        _matrix(da, "da", (na, rank, k), torch.float32)
+    if db is not None:
+        _matrix(db, "db", (na, n, rank), torch.float32)
+    _same_gpu(x, dy, a, b, ids, scale, r, dx, da, db, workspace if workspace is not True else None)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+        if da is None:
+            da = torch.empty((na, rank, k), dtype=torch.float32, device=x.device)
+        if db is None:
+            db = torch.empty((na, n, rank), dtype=torch.float32, device=x.device)
+        ws = _scratch(workspace, lib().q4_lora_grad_workspace_bytes(m, n, k, rank), x.device)
+        _check(lib().q4_lora_grad(_addr(x), _addr(dy), _addr(a), _addr(b), _addr(scale),
+                                  _addr(ids), _addr(r), _addr(dx), _addr(da), _addr(db),
+                                  _TYPES[x.dtype], _TYPES[a.dtype], m, n, k, rank, na, _addr(ws),
+                                  ws.numel(), _stream(stream)), "q4_lora_grad")
+    return dx, da, db
 
 
 GGUF_F32, GGUF_F16, GGUF_Q4_0, GGUF_Q8_0, GGUF_BF16 = 0, 1, 2, 8, 30

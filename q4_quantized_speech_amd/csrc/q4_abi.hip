@@ -20,12 +20,6 @@ std::atomic<int> g_cu_count[kMaxDevices];
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-q4_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return Q4_OK;
-  g_last_hip_error = static_cast<int>(e);
-  return Q4_ERR_HIP;
-}
-
 bool k_ok(int64_t K) { return K > 0 && K % 32 == 0 && K <= (int64_t(1) << 30); }
 
 bool matmul_shape_ok(int64_t M, int64_t N, int64_t K) {
@@ -34,6 +28,12 @@ bool matmul_shape_ok(int64_t M, int64_t N, int64_t K) {
          M * N < (int64_t(1) << 40);
 }
 }  // namespace
+
+int hip_status(hipError_t e) {
+  if (e == hipSuccess) return Q4_OK;
+  g_last_hip_error = static_cast<int>(e);
+  return Q4_ERR_HIP;
+}
 
 DeviceInfo device_info() {
   int dev = 0;
@@ -63,7 +63,7 @@ const char* q4_status_string(q4_status status) {
     case Q4_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
     case Q4_ERR_WORKSPACE: return "workspace missing or too small";
     case Q4_ERR_HIP: return "a HIP call failed (see q4_last_hip_error)";
-    case Q4_ERR_FORMAT: return "malformed or unsupported GGUF content";
+    case Q4_ERR_FORMAT: return "malformed or unsupported GGUF content, or an unsupported element type";
     case Q4_ERR_IO: return "a file could not be opened or read";
     case Q4_ERR_NOT_FOUND: return "no such tensor, metadata key or index";
     default: return "unknown status";

@@ -11,6 +11,8 @@ struct DeviceInfo {
   int cu_count;
 };
 DeviceInfo device_info();
+// The q4_status of a HIP call; a failure is kept for q4_last_hip_error().
+int hip_status(hipError_t e);
 
 hipError_t launch_matvec(const uint8_t* w, const float* x, float* y, int64_t M, int64_t N,
                          int64_t K, hipStream_t s);
@@ -57,5 +59,24 @@ hipError_t launch_embed(const uint8_t* table, const int32_t* ids, float* out, in
 
 hipError_t launch_quantize(const float* w, uint8_t* out, int64_t N, int64_t K, int32_t* flag,
                            hipStream_t s);
+
+// Low-rank adapters (arguments as in q4_lora and q4_lora_grad; y is dx and n
+// the output width in both).
+struct LoraArgs {
+  const void *x, *dy, *a, *b, *r;
+  const float* scale;
+  const int32_t* ids;
+  void* y;
+  float *da, *db;
+  int type, atype;
+  bool grad;
+  int64_t M, N, K, R, adapters;
+  void* ws;
+  hipStream_t stream;
+};
+bool lora_types_ok(int type, int atype);
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int cus);
+size_t lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int cus);
+hipError_t launch_lora(const LoraArgs& p, int cus);
 
 }  // namespace q4
