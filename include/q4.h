@@ -323,6 +323,58 @@ q4_status q4_quantize(const float* w, void* w_q4, int64_t N, int64_t K,
 enum { Q4_TYPE_F32 = 0, Q4_TYPE_F16 = 1, Q4_TYPE_BF16 = 30 };
 
 /*
+ * q4_matmul_dx -- the gradient of a Q4_0 projection with respect to its
+ * input: dx[m, k] = sum_n dy[m, n] deq(W)[n, k].
+ *   w_q4 : N rows of Q4_0.   dy : [M, N].   dx : [M, K] (written).
+ *   1 <= M <= 2^20, 1 <= N <= 4194304, K a positive multiple of 32 up to
+ *   4194304, M*N, M*K and N*K below 2^34.
+ *   workspace : q4_matmul_dx_workspace_bytes(type, M, N, K) bytes of device
+ *           scratch; its contents do not matter.  Calls that share it must be
+ *           ordered.
+ * On the matrix cores with float32 sums.  Each row of dy is scaled by a power
+ * of two into binary16 (float32 rows as two parts), so gradients of any
+ * magnitude keep their precision: per element the error of an operand is at
+ * most 2^-22 of it or 2^-40 of its row's largest magnitude.  Weights are exact
+ * (two parts) for float32 and float16, and rounded to binary16 for bfloat16,
+ * whose own rounding is eight times coarser.  |deq(W)| must stay below 65504.
+ * Deterministic; a row that holds an infinity or NaN gives non-finite values
+ * in that row only.
+ */
+size_t q4_matmul_dx_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);
+q4_status q4_matmul_dx(const void* w_q4, const void* dy, void* dx, int32_t type, int64_t M,
+                       int64_t N, int64_t K, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * q4_lmhead_xent -- softmax cross entropy of the Q4_0 LM head and its
+ * gradient, in pieces of the vocabulary (section "Solutions techniques pour
+ * l'exécution dans le navigateur", item 3: the 131072-row table in Q4).  With
+ * l[n] = sum_k deq(T)[n, k] x[m, k] and t = targets[m]:
+ *   lse[m] = log sum_n exp l[n],   loss[m] = lse[m] - l[t],
+ *   dx[m]  = dloss[m] * sum_n (softmax(l)[n] - [n == t]) deq(T)[n, :].
+ *   w_q4    : N rows of Q4_0.   x : [M, K].   targets : M int32 (device).
+ *   loss, lse : M float32 (written).
+ *   dloss   : M float32, the gradient of the loss of each row, or NULL (ones).
+ *   dx      : [M, K] of x's type (written), or NULL: no gradient.
+ *   A row whose target is outside [0, N) (padding) has loss 0 and dx 0.
+ *   1 <= M <= 65536, 1 <= N < 2^31, K a positive multiple of 32 up to
+ *   4194304, M*K and N*K below 2^34.
+ *   workspace : q4_lmhead_xent_workspace_bytes(type, dx != NULL, M, N, K)
+ *           bytes of device scratch; its contents do not matter.  Calls that
+ *           share it must be ordered.
+ * Logits, maxima and sums are float32 over exact weights.  1 - softmax at the
+ * target is taken as the sum of the others, so small losses and gradients
+ * keep their relative precision.  For float16 and bfloat16 the gradient's
+ * probabilities and weights are rounded to binary16 (float32 keeps two parts
+ * of each).  Deterministic.
+ */
+size_t q4_lmhead_xent_workspace_bytes(int32_t type, int32_t grad, int64_t M, int64_t N,
+                                      int64_t K);
+q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets,
+                         const float* dloss, float* loss, float* lse, void* dx, int32_t type,
+                         int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
  * q4_lora -- low-rank adapters of many requests at once beside a shared
  * projection: y[m] = r[m] + s_a B_a (A_a x[m]) with a = ids[m].  With y as
  * the r of q4_matmul_residual (in place) the projection itself is added.

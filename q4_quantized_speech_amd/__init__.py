@@ -12,6 +12,8 @@ Entry points (same names as the C ABI, minus the ``q4_`` prefix):
     embed_rows(table_q4, ids, out=None)          rows of deq(T)
     lmhead_argmax(w_q4, x, workspace=None, ...)  argmax_n (deq(T) x)_n
     quantize(w, out=None, check=True)            float32 -> Q4_0 bytes
+    matmul_dx(w_q4, dy, out=None, ...)           dX = dY deq(W): the gradient through a projection
+    lmhead_xent(w_q4, x, targets, grad=False)    cross entropy of the head, and its gradient
     lora(x, a, b, ids, scale=None, r=None, ...)  y = r + s_a B_a (A_a x), a = ids[row]
     lora_grad(x, dy, a, b, ids, ...)             its gradient: dx, da, db
 
@@ -70,6 +72,10 @@ _SIGS = {
     "q4_decode_chain": ([_P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "q4_matmul_route": ([_I64, _I64, _I64, _SZ, _P], ctypes.c_char_p),
     "q4_matvec_route": ([_I64, _I64, ctypes.c_int32], ctypes.c_char_p),
+    "q4_matmul_dx_workspace_bytes": ([ctypes.c_int32, _I64, _I64, _I64], _SZ),
+    "q4_matmul_dx": ([_P] * 3 + [ctypes.c_int32] + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
+    "q4_lmhead_xent_workspace_bytes": ([ctypes.c_int32] * 2 + [_I64] * 3, _SZ),
+    "q4_lmhead_xent": ([_P] * 7 + [ctypes.c_int32] + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
     "q4_lora_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
     "q4_lora": ([_P] * 7 + [ctypes.c_int32] * 2 + [_I64] * 5 + [_P, _SZ, _P], ctypes.c_int),
     "q4_lora_grad_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
@@ -431,6 +437,65 @@ def _scratch(workspace, nbytes: int, device):
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return workspace
+
+
+def matmul_dx(w_q4: torch.Tensor, dy: torch.Tensor, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None):
+    """dX = dY deq(W), the gradient of ``matmul`` with respect to x: dy is [M, N] of float32,
+    float16 or bfloat16, the result [M, K] of its type.  Without ``workspace`` one is
+    allocated (several times the decoded weights' size for float32)."""
+    n, k = q4_shape(w_q4)
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be [M, {n}]")
+    m = dy.shape[0]
+    _matrix(dy, "dy", (m, n))
+    if out is not None:
+        _matrix(out, "out", (m, k), dy.dtype)
+    _same_gpu(w_q4, dy, out, workspace if workspace is not True else None)
+    t = _TYPES[dy.dtype]
+    with _on(stream):
+        if out is None:
+            out = torch.empty((m, k), dtype=dy.dtype, device=dy.device)
+        ws = _scratch(workspace, lib().q4_matmul_dx_workspace_bytes(t, m, n, k), dy.device)
+        _check(lib().q4_matmul_dx(_addr(w_q4), _addr(dy), _addr(out), t, m, n, k, _addr(ws),
+                                  ws.numel(), _stream(stream)), "q4_matmul_dx")
+    return out
+
+
+def lmhead_xent(w_q4: torch.Tensor, x: torch.Tensor, targets: torch.Tensor, grad: bool = False,
+                dloss: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """(loss, lse, dx): per row of x, lse = logsumexp(deq(T) x), loss = lse - the target's
+    logit (float32), and with ``grad`` (or a ``dx`` to write) the gradient of
+    sum(dloss * loss) with respect to x, in x's type; dx is None otherwise.  Rows whose
+    target is outside [0, N) have loss 0 and dx 0.  The logits are never kept whole."""
+    n, k = q4_shape(w_q4)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, {k}]")
+    m = x.shape[0]
+    _matrix(x, "x", (m, k))
+    _matrix(targets, "targets", (m,), torch.int32)
+    for t, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
+        if t is not None:
+            _matrix(t, name, (m,), torch.float32)
+    if dx is not None:
+        _matrix(dx, "dx", (m, k), x.dtype)
+        grad = True
+    _same_gpu(w_q4, x, targets, dloss, loss, lse, dx, workspace if workspace is not True else None)
+    t = _TYPES[x.dtype]
+    with _on(stream):
+        if loss is None:
+            loss = torch.empty(m, dtype=torch.float32, device=x.device)
+        if lse is None:
+            lse = torch.empty(m, dtype=torch.float32, device=x.device)
+        if grad and dx is None:
+            dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+        ws = _scratch(workspace, lib().q4_lmhead_xent_workspace_bytes(t, int(grad), m, n, k), x.device)
+        _check(lib().q4_lmhead_xent(_addr(w_q4), _addr(x), _addr(targets), _addr(dloss),
+                                    _addr(loss), _addr(lse), _addr(dx), t, m, n, k, _addr(ws),
+                                    ws.numel(), _stream(stream)), "q4_lmhead_xent")
+    return loss, lse, dx
 
 
 def _adapters(x, a, b, ids, scale):

@@ -30,9 +30,63 @@ bool lora_grad_shape_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t adap
          adapters * ((K + 63) / 64 + (N + 63) / 64) <= (int64_t(1) << 21);
 }
 
+bool dx_shape_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t most = int64_t(1) << 34;
+  return M >= 1 && M <= (int64_t(1) << 20) && N >= 1 && N <= MAX_NK && K >= 32 && K <= MAX_NK &&
+         K % 32 == 0 && M * N < most && M * K < most && N * K < most;
+}
+
+bool xent_shape_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t most = int64_t(1) << 34;
+  return M >= 1 && M <= 65536 && N >= 1 && N < (int64_t(1) << 31) && K >= 32 && K <= MAX_NK &&
+         K % 32 == 0 && M * K < most && N * K < most;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t q4_matmul_dx_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K) {
+  if (!type_ok(type) || !dx_shape_ok(M, N, K)) return 0;
+  return matmul_dx_workspace_bytes(type, M, N, K, device_info().cu_count);
+}
+
+q4_status q4_matmul_dx(const void* w_q4, const void* dy, void* dx, int32_t type, int64_t M,
+                       int64_t N, int64_t K, void* workspace, size_t ws_bytes, void* stream) {
+  if (!w_q4 || !dy || !dx) return Q4_ERR_NULL;
+  if (!type_ok(type)) return Q4_ERR_FORMAT;
+  if (!dx_shape_ok(M, N, K)) return Q4_ERR_SHAPE;
+  if (!aligned16(w_q4) || !aligned16(dy) || !aligned16(dx) || !aligned16(workspace))
+    return Q4_ERR_ALIGN;
+  const int cus = device_info().cu_count;
+  if (!workspace || ws_bytes < matmul_dx_workspace_bytes(type, M, N, K, cus))
+    return Q4_ERR_WORKSPACE;
+  return hip_status(launch_matmul_dx(static_cast<const uint8_t*>(w_q4), dy, dx, type, M, N, K,
+                                     workspace, cus, static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_lmhead_xent_workspace_bytes(int32_t type, int32_t grad, int64_t M, int64_t N,
+                                      int64_t K) {
+  if (!type_ok(type) || !xent_shape_ok(M, N, K)) return 0;
+  return xent_workspace_bytes(type, grad != 0, M, N, K, device_info().cu_count);
+}
+
+q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets,
+                         const float* dloss, float* loss, float* lse, void* dx, int32_t type,
+                         int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  if (!w_q4 || !x || !targets || !loss || !lse) return Q4_ERR_NULL;
+  if (!type_ok(type)) return Q4_ERR_FORMAT;
+  if (!xent_shape_ok(M, N, K)) return Q4_ERR_SHAPE;
+  if (!aligned16(w_q4) || !aligned16(x) || !aligned16(targets) || !aligned16(dloss) ||
+      !aligned16(loss) || !aligned16(lse) || !aligned16(dx) || !aligned16(workspace))
+    return Q4_ERR_ALIGN;
+  const int cus = device_info().cu_count;
+  if (!workspace || ws_bytes < xent_workspace_bytes(type, dx != nullptr, M, N, K, cus))
+    return Q4_ERR_WORKSPACE;
+  return hip_status(launch_xent(static_cast<const uint8_t*>(w_q4), x, targets, dloss, loss, lse, dx,
+                                type, M, N, K, workspace, cus, static_cast<hipStream_t>(stream)));
+}
 
 size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
   if (!lora_shape_ok(M, N, K, R, 1)) return 0;

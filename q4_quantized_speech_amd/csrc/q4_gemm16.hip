@@ -1,0 +1,705 @@
+// Prepared binary16 products on the CDNA4 matrix cores (see q4_gemm16.h for
+// the operand layout), and the gradient of a Q4_0 projection built on them:
+// dX[m, k] = sum_n dY[m, n] deq(W)[n, k] (section "Architecture" of
+// "Implémentation en Rust du modèle Voxtral Mini 4B Realtime de Mistral pour
+// l'exécuter dans le navigateur": the quantised projections).
+
+#include <algorithm>
+
+#include "q4_gemm16.h"
+#include "q4_kernels.h"
+
+namespace q4 {
+namespace {
+
+constexpr int XCDS = 8;
+
+// The hardware deals workgroups to the XCDs round-robin; give XCD x a
+// contiguous range of tiles, so tiles that share operands share an L2.
+__device__ __forceinline__ unsigned xcd_order(unsigned bid, unsigned n) {
+  const unsigned per = n / XCDS, rem = n % XCDS, x = bid % XCDS, i = bid / XCDS;
+  return (x < rem ? x * (per + 1) : rem * (per + 1) + (x - rem) * per) + i;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// Power of two that brings `top` (a row's largest magnitude) to [2^14, 2^15);
+// 1 for rows of zeros or with a magnitude that is not finite.
+__device__ __forceinline__ float row_scale(float top) {
+  if (!(top > 0.f) || !(top < __builtin_inff())) return 1.f;
+  int e;
+  frexpf(top, &e);  // top in [2^(e-1), 2^e)
+  return ldexpf(1.f, min(15 - e, 126));
+}
+
+// ---------------------------------------------------------------------------
+// Operand preparation
+// ---------------------------------------------------------------------------
+
+// One wave per row, 16 rows per workgroup.
+template <typename T, bool NIB, int PARTS, bool VEC>
+__global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X,
+                                                         f16x8* __restrict__ out,
+                                                         float* __restrict__ inv, int64_t M,
+                                                         int64_t C, int64_t CB) {
+  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + i;
+  const bool live = m < M;
+  const T* row = X + (live ? m : 0) * C;
+  auto load4 = [&](int64_t c, float (&v)[4]) {
+    if constexpr (VEC) {
+      if (live && c < C) {
+        load_f32<4>(row + c, v);
+        return;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = 0.f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = live && c + e < C ? to_f32(row[c + e]) : 0.f;
+    }
+  };
+  float top = 0.f;
+  for (int64_t c = 4 * lane; c < C; c += 256) {
+    float v[4];
+    load4(c, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[e]));
+  }
+  top = wave_max(top);
+  const float s = row_scale(top);
+  if (live && lane == 0) inv[m] = 1.f / s;
+  const int64_t part = static_cast<int64_t>(gridDim.x) * CB * 64;
+  for (int64_t q = lane; q < CB * 4; q += 64) {  // slot: block q / 4, group q % 4
+    const int64_t blk = q >> 2;
+    const int g = static_cast<int>(q & 3);
+    float a[4], b[4];
+    load4(32 * blk + (NIB ? 4 * g : 8 * g), a);
+    load4(32 * blk + (NIB ? 16 + 4 * g : 8 * g + 4), b);
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = (e < 4 ? a[e & 3] : b[e & 3]) * s;
+      hi[e] = static_cast<_Float16>(v);
+      if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(v - static_cast<float>(hi[e]));
+    }
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * CB + blk) * 64 + i + 16 * g;
+    out[at] = hi;
+    if constexpr (PARTS == 2) out[part + at] = lo;
+  }
+}
+
+template <typename T>
+void prep_rows_t(const T* x, Order order, int parts, f16x8* frag, float* inv, int64_t M, int64_t C,
+                 hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((M + 15) / 16)), block(1024);
+  const int64_t CB = blocks32(C);
+  const bool vec = C % 4 == 0;
+  auto go = [&](auto nib, auto p, auto v) {
+    hipLaunchKernelGGL((prep_rows_kernel<T, decltype(nib)::value, decltype(p)::value, decltype(v)::value>),
+                       grid, block, 0, s, x, frag, inv, M, C, CB);
+  };
+  using std::integral_constant;
+  const integral_constant<int, 1> p1;
+  const integral_constant<int, 2> p2;
+  const std::true_type yes;
+  const std::false_type no;
+  if (order == Order::NIBBLE) {  // K is a multiple of 32
+    if (parts == 2) go(yes, p2, yes); else go(yes, p1, yes);
+  } else if (parts == 2) {
+    if (vec) go(no, p2, yes); else go(no, p2, no);
+  } else {
+    if (vec) go(no, p1, yes); else go(no, p1, no);
+  }
+}
+
+// (q - 8) of the eight codes of a dword, binary16, NIBBLE order.
+__device__ __forceinline__ f16x8 codes8(uint32_t qs) {
+  const uint32_t lo = qs & 0x0F0F0F0Fu, hi = (qs >> 4) & 0x0F0F0F0Fu;
+  const uint32_t magic = 0x64646464u;  // 0x64xx: the binary16 value 1024 + q
+  const f16x2 off = {static_cast<_Float16>(-1032.0f), static_cast<_Float16>(-1032.0f)};
+  const f16x2 h0 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(magic, lo, 0x04010400u)) + off;
+  const f16x2 h1 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(magic, lo, 0x04030402u)) + off;
+  const f16x2 h2 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(magic, hi, 0x04010400u)) + off;
+  const f16x2 h3 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(magic, hi, 0x04030402u)) + off;
+  return f16x8{h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
+}
+
+// One thread per block of 32 weights: 16 rows x 16 blocks per workgroup.
+__global__ __launch_bounds__(256) void prep_codes_kernel(const uint8_t* __restrict__ W, int64_t n0,
+                                                         int64_t N, int64_t kblocks, int64_t KB,
+                                                         f16x8* __restrict__ qfrag,
+                                                         float* __restrict__ scale) {
+  const int i = threadIdx.x & 15;
+  const int64_t kb = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
+  if (kb >= KB) return;
+  const int64_t rt = blockIdx.x, n = n0 + rt * 16 + i;
+  uint32_t d = 0, qs[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
+  if (n < N && kb < kblocks) load_block_any(W, n * kblocks + kb, d, qs);
+  const int64_t f = rt * KB + kb;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) qfrag[f * 64 + i + 16 * g] = codes8(qs[g]);
+  scale[f * 16 + i] = half_bits_to_float(d);
+}
+
+// One thread per (32-row block, group of 8 rows, block of 32 weights, code
+// dword): eight rows' dwords hold eight columns, whose operands are written
+// with the eight rows as the reduction.
+template <int PARTS>
+__global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __restrict__ W,
+                                                             int64_t n0, int64_t N, int64_t kblocks,
+                                                             int64_t NB, f16x8* __restrict__ tfrag) {
+  const int j = threadIdx.x & 3, g = (threadIdx.x >> 2) & 3;
+  const int64_t kb = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
+  if (kb >= kblocks) return;
+  const int64_t nb = blockIdx.x;
+  uint32_t qs[8];
+  float d[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int64_t n = n0 + nb * 32 + 8 * g + r;
+    qs[r] = 0;
+    d[r] = 0.f;
+    if (n < N) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(W + (n * kblocks + kb) * BLOCK_BYTES);
+      d[r] = half_bits_to_float(p[0]);
+      qs[r] = p[1 + 2 * j] | (static_cast<uint32_t>(p[2 + 2 * j]) << 16);
+    }
+  }
+  const int64_t part = kblocks * 2 * NB * 64;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {  // codes 0-3: low nibbles, columns 4 j + c; 4-7: high, 16 + ...
+    f16x8 hi, lo;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const uint32_t q = (qs[r] >> (8 * (c & 3) + 4 * (c >> 2))) & 15u;
+      const float w = (static_cast<float>(q) - 8.f) * d[r];
+      hi[r] = static_cast<_Float16>(w);
+      // w has at most 15 significant bits and is a multiple of 2^-24 like
+      // its scale, so the rest fits binary16 exactly
+      if constexpr (PARTS == 2) lo[r] = static_cast<_Float16>(w - static_cast<float>(hi[r]));
+    }
+    const int64_t at = ((2 * kb + (c >> 2)) * NB + nb) * 64 + 4 * j + (c & 3) + 16 * g;
+    tfrag[at] = hi;
+    if constexpr (PARTS == 2) tfrag[part + at] = lo;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The product.  WM x WN waves, each FM x FN fragments of 16 x 16 outputs; a
+// stage is KS blocks of 32 reduction indices of every fragment row of the
+// tile, loaded straight to LDS while the previous stage is multiplied.
+// ---------------------------------------------------------------------------
+template <int WM_, int WN_, int FM_, int FN_>
+struct Shape {
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
+  static constexpr int THREADS = 64 * WM * WN, M = 16 * WM * FM, N = 16 * WN * FN;
+};
+using S256 = Shape<2, 4, 8, 4>;
+using S128 = Shape<2, 2, 4, 4>;
+using S32 = Shape<1, 4, 2, 4>;
+
+// Memory to LDS without registers: lane l's `SIZE` bytes at g land at
+// l + SIZE * lane.  Asynchronous: arrived() before the barrier that publishes.
+template <int SIZE>
+__device__ __forceinline__ void to_lds(const void* g, void* l) {
+  static_assert(SIZE == 16 || SIZE == 4, "bytes per lane");
+  const auto gp = (const __attribute__((address_space(1))) void*)g;
+  const auto lp = (__attribute__((address_space(3))) void*)l;
+  if constexpr (SIZE == 16)
+    __builtin_amdgcn_global_load_lds(gp, lp, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds(gp, lp, 4, 0, 0);
+}
+// The loads to LDS before this point are issued before the work after it (they
+// touch other arrays, so the compiler would be free to start them late).
+__device__ __forceinline__ void issued() { asm volatile("" ::: "memory"); }
+// This wave's loads to LDS are complete, and no LDS access moves across.
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <typename S, int PA, int PB, int KS>
+struct Stage {
+  static constexpr int WAVES = S::WM * S::WN;
+  static constexpr int FA = S::WM * S::FM * PA * KS, FB = S::WN * S::FN * PB * KS;
+  static constexpr int NF = FA + FB, PER = (NF + WAVES - 1) / WAVES;
+
+  const f16x8* at[PER];  // this wave's fragments of block 0
+
+  // Fragments of a stage: A's first, [part][row tile][block].  Row tiles past
+  // the matrix repeat its last one (their results are dropped).
+  __device__ __forceinline__ Stage(const f16x8* __restrict__ A, const f16x8* __restrict__ B,
+                                   int64_t ma, int64_t rta, int64_t mb, int64_t rtb, int64_t CB,
+                                   int wave) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int f = wave * PER + u;
+      const bool isa = f < FA;
+      const int h = isa ? f : f - FA;
+      const int rows = (isa ? S::WM * S::FM : S::WN * S::FN);
+      const int part = h / (rows * KS), row = h / KS % rows, k = h % KS;
+      const int64_t rt = isa ? min(ma + row, rta - 1) : min(mb + row, rtb - 1);
+      const int64_t all = isa ? rta : rtb;
+      at[u] = (isa ? A : B) + ((part * all + rt) * CB + k) * 64;
+    }
+  }
+  // Starts the loads of blocks c .. c + KS - 1.
+  __device__ __forceinline__ void issue(f16x8 (*buf)[64], int64_t c, int wave, int lane) const {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      if (NF % WAVES != 0 && wave * PER + u >= NF) break;  // wave-uniform
+      to_lds<16>(at[u] + c * 64 + lane, &buf[wave * PER + u][0]);
+    }
+    issued();
+  }
+};
+
+template <typename S, int PA, int PB, int KS>
+__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gemm_plain_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B, int64_t M,
+                       int64_t N, int64_t CB, int tiles_m, int tiles, int64_t span,
+                       float* __restrict__ out, int64_t ld, const float* __restrict__ alpha) {
+  using St = Stage<S, PA, PB, KS>;
+  // two arrays rather than one of two: the compiler then knows that reading
+  // one does not have to wait for loads into the other
+  __shared__ f16x8 buf0[St::NF][64], buf1[St::NF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = xcd_order(blockIdx.x, gridDim.x);
+  const int split = item / tiles, tile = item % tiles;
+  const int tm = tile % tiles_m, tn = tile / tiles_m;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int64_t ma = static_cast<int64_t>(tm) * (S::M / 16), mb = static_cast<int64_t>(tn) * (S::N / 16);
+  const int64_t rta = (M + 15) / 16, rtb = (N + 15) / 16;
+  const int64_t c0 = split * span, c1 = min(CB, c0 + span);
+
+  f32x4 acc[S::FM][S::FN];
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const St st(A, B, ma, rta, mb, rtb, CB, wave);
+  auto compute = [&](const f16x8 (*buf)[64]) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      f16x8 b[PB][S::FN];
+#pragma unroll
+      for (int p = 0; p < PB; ++p)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j)
+          b[p][j] = buf[St::FA + (p * S::WN * S::FN + wn * S::FN + j) * KS + k][lane];
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        f16x8 a[PA];
+#pragma unroll
+        for (int p = 0; p < PA; ++p) a[p] = buf[(p * S::WM * S::FM + wm * S::FM + i) * KS + k][lane];
+        // D rows are B's (the columns of out), D columns A's (its rows)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0][j], a[0], acc[i][j], 0, 0, 0);
+          if constexpr (PB == 2)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[1][j], a[0], acc[i][j], 0, 0, 0);
+          if constexpr (PA == 2)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0][j], a[1], acc[i][j], 0, 0, 0);
+        }
+      }
+    }
+  };
+  if (c0 < c1) {  // a slice of a short reduction may be empty: its sum is zero
+    st.issue(buf0, c0, wave, lane);
+    arrived();
+  }
+  __syncthreads();
+  int64_t c = c0;
+  for (; c + 2 * KS <= c1; c += 2 * KS) {
+    st.issue(buf1, c + KS, wave, lane);
+    compute(buf0);
+    arrived();
+    __syncthreads();
+    if (c + 2 * KS < c1) st.issue(buf0, c + 2 * KS, wave, lane);
+    compute(buf1);
+    arrived();
+    __syncthreads();
+  }
+  if (c < c1) compute(buf0);
+  // lane (i, g): row i of a fragment row, columns 4 g .. 4 g + 3 (N % 16 == 0)
+  float* o = out + static_cast<int64_t>(split) * M * ld;
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) {
+    const int64_t m = (ma + wm * S::FM + i) * 16 + (lane & 15);
+    if (m >= M) continue;
+    const float al = alpha ? alpha[m] : 0.f;
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) {
+      const int64_t n = (mb + wn * S::FN + j) * 16 + 4 * (lane >> 4);
+      if (n >= N) continue;
+      f32x4* p = reinterpret_cast<f32x4*>(o + m * ld + n);
+      f32x4 v = acc[i][j];
+      if (alpha) {
+        const f32x4 q = *p;
+        v.x = __builtin_fmaf(al, q.x, v.x);
+        v.y = __builtin_fmaf(al, q.y, v.y);
+        v.z = __builtin_fmaf(al, q.z, v.z);
+        v.w = __builtin_fmaf(al, q.w, v.w);
+      }
+      *p = v;
+    }
+  }
+}
+
+// Maximum over the 16 lanes of a DPP row, in all of them.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, dpp_f32<0xB1>(v));
+  v = fmaxf(v, dpp_f32<0x4E>(v));
+  v = fmaxf(v, dpp_f32<0x141>(v));
+  v = fmaxf(v, dpp_f32<0x140>(v));
+  return v;
+}
+
+template <typename S, int PA, int KS, bool STATS>
+__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
+                        const float* __restrict__ scale, const float* __restrict__ inv, int64_t M,
+                        int64_t cols, int64_t CB, int tiles_m, int64_t n0, int64_t N,
+                        const int32_t* __restrict__ targets, float* __restrict__ logits,
+                        float* __restrict__ tmax, float* __restrict__ tsum,
+                        float* __restrict__ tlogit, int64_t ld, int64_t tld) {
+  static_assert(S::FN == 4, "a wave's columns are one entry of tmax");
+  using St = Stage<S, PA, 1, KS>;
+  constexpr int SC = S::N * KS;  // block scales of a stage, [row tile][block][16]
+  constexpr int SU = (SC / 64 + St::WAVES - 1) / St::WAVES;  // loads of 64 scales per wave
+  __shared__ f16x8 buf0[St::NF][64], buf1[St::NF][64];
+  __shared__ float sc0[SC], sc1[SC];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = xcd_order(blockIdx.x, gridDim.x);
+  const int tm = item % tiles_m, tn = item / tiles_m;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int64_t ma = static_cast<int64_t>(tm) * (S::M / 16), mb = static_cast<int64_t>(tn) * (S::N / 16);
+  const int64_t rta = (M + 15) / 16, rtb = cols / 16;
+
+  f32x4 acc[S::FM][S::FN];
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const St st(A, Q, ma, rta, mb, rtb, CB, wave);
+  auto issue = [&](f16x8 (*buf)[64], float* sc, int64_t c) {
+    st.issue(buf, c, wave, lane);
+#pragma unroll
+    for (int u = 0; u < SU; ++u) {
+      const int first = (wave * SU + u) * 64;
+      if (SC / 64 % St::WAVES != 0 && first >= SC) break;
+      const int e = first + lane;
+      const int64_t rt = min(mb + e / (16 * KS), rtb - 1);
+      to_lds<4>(scale + (rt * CB + c) * 16 + e % (16 * KS), sc + first);
+    }
+    issued();
+  };
+  auto compute = [&](const f16x8 (*buf)[64], const float* sc) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      f16x8 b[S::FN];
+      float d[S::FN];
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        b[j] = buf[St::FA + (wn * S::FN + j) * KS + k][lane];
+        d[j] = sc[((wn * S::FN + j) * KS + k) * 16 + (lane & 15)];
+      }
+      // Row i + 1's products are started before row i's scaled sums are taken,
+      // so the matrix cores and the vector unit overlap within the wave.  The
+      // empty volatile asm keeps that order (pure arithmetic would otherwise
+      // be regrouped, all products first, whose temporaries then spill).
+      f32x4 t[2][S::FN];
+      auto products = [&](int i) {
+        f16x8 a[PA];
+#pragma unroll
+        for (int p = 0; p < PA; ++p) a[p] = buf[(p * S::WM * S::FM + wm * S::FM + i) * KS + k][lane];
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[j], f32x4{0.f, 0.f, 0.f, 0.f},
+                                                               0, 0, 0);
+          if constexpr (PA == 2)
+            t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], b[j], t[i & 1][j], 0, 0, 0);
+        }
+        asm volatile("" : "+v"(t[i & 1][0]), "+v"(t[i & 1][1]), "+v"(t[i & 1][2]), "+v"(t[i & 1][3]));
+      };
+      products(0);
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        if (i + 1 < S::FM) products(i + 1);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          acc[i][j].x = __builtin_fmaf(d[j], t[i & 1][j].x, acc[i][j].x);
+          acc[i][j].y = __builtin_fmaf(d[j], t[i & 1][j].y, acc[i][j].y);
+          acc[i][j].z = __builtin_fmaf(d[j], t[i & 1][j].z, acc[i][j].z);
+          acc[i][j].w = __builtin_fmaf(d[j], t[i & 1][j].w, acc[i][j].w);
+        }
+        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+      }
+    }
+  };
+  issue(buf0, sc0, 0);
+  arrived();
+  __syncthreads();
+  int64_t c = 0;
+  for (; c + 2 * KS <= CB; c += 2 * KS) {
+    issue(buf1, sc1, c + KS);
+    compute(buf0, sc0);
+    arrived();
+    __syncthreads();
+    if (c + 2 * KS < CB) issue(buf0, sc0, c + 2 * KS);
+    compute(buf1, sc1);
+    arrived();
+    __syncthreads();
+  }
+  if (c < CB) compute(buf0, sc0);
+
+  // lane: column lane % 16 of a fragment, rows 4 g + v
+  const int64_t nl = (mb + wn * S::FN) * 16 + (lane & 15);  // local column of fragment 0
+  const int64_t entry = (mb + wn * S::FN) / 4;
+  if (mb + wn * S::FN >= rtb) return;
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t m = (ma + wm * S::FM + i) * 16 + 4 * (lane >> 4) + v;
+      const bool live = m < M;
+      const float is = live ? inv[m] : 0.f;
+      float l[S::FN], top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        l[j] = n0 + nl + 16 * j < N ? acc[i][j][v] * is : -__builtin_inff();
+        top = fmaxf(top, l[j]);
+      }
+      top = row16_max(top);
+      if constexpr (STATS) {
+        const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 - nl : -1;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          const bool is_target = t == 16 * j && n0 + nl + 16 * j < N;
+          if (is_target) tlogit[m] = l[j];
+          if (!is_target && l[j] != -__builtin_inff()) s += expf(l[j] - top);
+        }
+        s = row16_sum(s);
+        if (live && (lane & 15) == 0) {
+          tmax[m * tld + entry] = top;
+          tsum[m * tld + entry] = s;
+        }
+      } else if (live) {
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j)
+          if (nl + 16 * j < cols) logits[m * ld + nl + 16 * j] = l[j];
+        if ((lane & 15) == 0) tmax[m * tld + entry] = top;
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ part, int splits,
+                                                   const float* __restrict__ inv,
+                                                   T* __restrict__ out, int64_t M, int64_t K) {
+  const int64_t quads = K / 4, total = M * quads;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total;
+       e += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t m = e / quads;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < splits; ++t)
+      s += *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(t) * M * K + 4 * e);
+    const float f = inv[m];
+    const float v[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
+    store_f32<4>(out + 4 * e, v);
+  }
+}
+
+template <typename F>
+hipError_t with_tile(Tile t, F f) {
+  switch (t) {
+    case Tile::T256x256: f(S256{}); break;
+    case Tile::T128x128: f(S128{}); break;
+    default: f(S32{}); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t prep_rows(const void* x, int type, Order order, int parts, f16x8* frag, float* inv,
+                     int64_t M, int64_t C, hipStream_t s) {
+  if (type == TYPE_F32)
+    prep_rows_t(static_cast<const float*>(x), order, parts, frag, inv, M, C, s);
+  else if (type == TYPE_F16)
+    prep_rows_t(static_cast<const _Float16*>(x), order, parts, frag, inv, M, C, s);
+  else
+    prep_rows_t(static_cast<const __bf16*>(x), order, parts, frag, inv, M, C, s);
+  return hipGetLastError();
+}
+
+hipError_t prep_weights(const uint8_t* w, int64_t n0, int64_t rows, int64_t N, int64_t K,
+                        f16x8* qfrag, float* scale, f16x8* tfrag, int parts, hipStream_t s) {
+  const int64_t kblocks = K / 32, KB = blocks32(K);
+  const unsigned gy = static_cast<unsigned>((KB + 15) / 16);
+  if (qfrag)
+    hipLaunchKernelGGL(prep_codes_kernel, dim3(static_cast<unsigned>(rows / 16), gy), dim3(256), 0,
+                       s, w, n0, N, kblocks, KB, qfrag, scale);
+  if (tfrag) {
+    const dim3 grid(static_cast<unsigned>(rows / 32), gy);
+    if (parts == 2)
+      hipLaunchKernelGGL(prep_transpose_kernel<2>, grid, dim3(256), 0, s, w, n0, N, kblocks,
+                         rows / 32, tfrag);
+    else
+      hipLaunchKernelGGL(prep_transpose_kernel<1>, grid, dim3(256), 0, s, w, n0, N, kblocks,
+                         rows / 32, tfrag);
+  }
+  return hipGetLastError();
+}
+
+TileDim tile_dim(Tile t) {
+  return t == Tile::T256x256 ? TileDim{256, 256} : t == Tile::T128x128 ? TileDim{128, 128} : TileDim{32, 256};
+}
+
+double tile_time_us(Tile t, int64_t M, int64_t N, int64_t C, int units, int splits, int cus) {
+  const TileDim d = tile_dim(t);
+  const int64_t items = ((M + d.m - 1) / d.m) * ((N + d.n - 1) / d.n) * splits;
+  const int per_cu = t == Tile::T256x256 ? 1 : 2;
+  const double eff = t == Tile::T256x256 ? 0.45 : t == Tile::T128x128 ? 0.30 : 0.12;
+  const double cu_rate = 2.5e9 / 256 * eff;  // flops per microsecond of one CU
+  const double rounds = static_cast<double>((items + per_cu * cus - 1) / (static_cast<int64_t>(per_cu) * cus));
+  const double gemm = rounds * per_cu * 2.0 * d.m * d.n * (static_cast<double>(C) / splits) * units / cu_rate;
+  return gemm + 2.0 * splits * M * N * 4.0 / 4e6;  // slices written and read at 4 TB/s
+}
+
+hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s) {
+  const TileDim d = tile_dim(t);
+  const int tm = static_cast<int>((p.M + d.m - 1) / d.m), tn = static_cast<int>((p.N + d.n - 1) / d.n);
+  const int64_t span = ((p.CB / 2 + p.splits - 1) / p.splits) * 2;
+  return with_tile(t, [&](auto shape) {
+    using S = decltype(shape);
+    auto go = [&](auto pa, auto pb, auto ks) {
+      hipLaunchKernelGGL((gemm_plain_kernel<S, decltype(pa)::value, decltype(pb)::value, decltype(ks)::value>),
+                         dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.splits)),
+                         dim3(S::THREADS), 0, s, p.a, p.b, p.M, p.N, p.CB, tm, tm * tn, span, p.out,
+                         p.ld, p.alpha);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    if (p.pa == 1 && p.pb == 1) go(one, one, two);
+    else if (p.pa == 1) go(one, two, one);
+    else go(two, two, one);
+  });
+}
+
+hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
+  const TileDim d = tile_dim(t);
+  const int tm = static_cast<int>((p.M + d.m - 1) / d.m), tn = static_cast<int>((p.cols + d.n - 1) / d.n);
+  return with_tile(t, [&](auto shape) {
+    using S = decltype(shape);
+    auto go = [&](auto pa, auto ks, auto stats) {
+      hipLaunchKernelGGL((gemm_logits_kernel<S, decltype(pa)::value, decltype(ks)::value, decltype(stats)::value>),
+                         dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn)), dim3(S::THREADS), 0, s,
+                         p.a, p.q, p.scale, p.inv, p.M, p.cols, p.CB, tm, p.n0, p.N, p.targets, p.logits,
+                         p.tmax, p.tsum, p.tlogit, p.ld, p.tld);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const std::true_type yes;
+    const std::false_type no;
+    if (p.logits) {
+      if (p.pa == 1) go(one, two, no); else go(two, one, no);
+    } else {
+      if (p.pa == 1) go(one, two, yes); else go(two, one, yes);
+    }
+  });
+}
+
+hipError_t launch_fold(const float* part, int splits, const float* inv, void* out, int type,
+                       int64_t M, int64_t K, hipStream_t s) {
+  const int64_t total = M * (K / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 8192));
+  if (type == TYPE_F32)
+    hipLaunchKernelGGL(fold_kernel<float>, dim3(grid), dim3(256), 0, s, part, splits, inv,
+                       static_cast<float*>(out), M, K);
+  else if (type == TYPE_F16)
+    hipLaunchKernelGGL(fold_kernel<_Float16>, dim3(grid), dim3(256), 0, s, part, splits, inv,
+                       static_cast<_Float16*>(out), M, K);
+  else
+    hipLaunchKernelGGL(fold_kernel<__bf16>, dim3(grid), dim3(256), 0, s, part, splits, inv,
+                       static_cast<__bf16*>(out), M, K);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// dX = dY deq(W)
+// ---------------------------------------------------------------------------
+namespace {
+
+struct DxPlan {
+  Tile tile;
+  int pa, pb, splits;
+  int64_t rows;  // weight rows, padded
+  size_t dy, inv, w, part, total;
+};
+
+DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
+  DxPlan p;
+  p.pa = type == TYPE_F32 ? 2 : 1;
+  // bfloat16: the weight's rounding to binary16 (2^-11) is well below the
+  // result's (2^-8); float16 and float32 results keep the weight exact
+  p.pb = type == TYPE_BF16 ? 1 : 2;
+  const int units = p.pa + p.pb - 1;
+  p.rows = (N + 63) / 64 * 64;
+  double best = 1e30;
+  for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
+    for (int s = 1; s <= 16 && (s == 1 || p.rows / s >= 128); ++s) {
+      const double us = tile_time_us(t, M, K, p.rows, units, s, cus);
+      if (us < best) {
+        best = us;
+        p.tile = t;
+        p.splits = s;
+      }
+    }
+  }
+  p.splits = even_splits(p.rows / 32, p.splits);
+  Carver c;
+  p.dy = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * p.pa);
+  p.inv = c.take(static_cast<size_t>(M) * 4);
+  p.w = c.take(static_cast<size_t>(K) * p.rows * 2 * p.pb);
+  p.part = c.take(static_cast<size_t>(p.splits) * M * K * 4);
+  p.total = c.at;
+  return p;
+}
+
+}  // namespace
+
+size_t matmul_dx_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus) {
+  return dx_plan(type, M, N, K, cus).total;
+}
+
+hipError_t launch_matmul_dx(const uint8_t* w, const void* dy, void* dx, int type, int64_t M,
+                            int64_t N, int64_t K, void* ws, int cus, hipStream_t s) {
+  const DxPlan p = dx_plan(type, M, N, K, cus);
+  char* base = static_cast<char*>(ws);
+  f16x8* fa = reinterpret_cast<f16x8*>(base + p.dy);
+  float* inv = reinterpret_cast<float*>(base + p.inv);
+  f16x8* fb = reinterpret_cast<f16x8*>(base + p.w);
+  float* part = reinterpret_cast<float*>(base + p.part);
+  hipError_t e = prep_rows(dy, type, Order::NATURAL, p.pa, fa, inv, M, N, s);
+  if (e == hipSuccess) e = prep_weights(w, 0, p.rows, N, K, nullptr, nullptr, fb, p.pb, s);
+  if (e == hipSuccess) {
+    const PlainGemm g = {fa, fb, p.pa, p.pb, M, K, p.rows / 32, p.splits, part, K, nullptr};
+    e = launch_gemm_plain(p.tile, g, s);
+  }
+  if (e == hipSuccess) e = launch_fold(part, p.splits, inv, dx, type, M, K, s);
+  return e;
+}
+
+}  // namespace q4

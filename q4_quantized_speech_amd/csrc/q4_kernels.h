@@ -79,4 +79,15 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int cus);
 size_t lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int cus);
 hipError_t launch_lora(const LoraArgs& p, int cus);
 
+// dX = dY deq(W) (type: element type of dY and dX).
+size_t matmul_dx_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_matmul_dx(const uint8_t* w, const void* dy, void* dx, int type, int64_t M,
+                            int64_t N, int64_t K, void* ws, int cus, hipStream_t s);
+
+// Cross entropy of the head; dx null: the loss alone.
+size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, const float* dloss,
+                       float* loss, float* lse, void* dx, int type, int64_t M, int64_t N, int64_t K,
+                       void* ws, int cus, hipStream_t s);
+
 }  // namespace q4

@@ -1,0 +1,461 @@
+// Softmax cross entropy of the Q4_0 LM head, in pieces of the vocabulary, and
+// its gradient (section "Solutions techniques pour l'exécution dans le
+// navigateur", item 3, of "Implémentation en Rust du modèle Voxtral Mini 4B
+// Realtime de Mistral pour l'exécuter dans le navigateur": the 131072-row
+// table kept in Q4).  With l[m, n] = x[m] . deq(T)[n] and t the row's target:
+//
+//   lse_m = log sum_n exp l[m, n]       loss_m = lse_m - l[m, t]
+//   dx[m] = g_m (sum_{n != t} p_n T_n - (1 - p_t) T_t),  p_n = exp(l - lse)
+//
+// The logits of one piece exist at a time.  Per piece: the codes are unpacked
+// into matrix-core operands (q4_gemm16.h), the logits computed with the exact
+// codes, the running maximum and sum of the softmax updated, and, for the
+// gradient, the piece's probabilities multiplied by the transposed piece into
+// a float32 accumulator that is rescaled when the maximum grows.  1 - p_t is
+// the sum of the other probabilities, so a row the model is sure of keeps its
+// small gradient and loss.
+//
+// A few rows without a gradient go through the matvec-accuracy kernels four
+// rows at a time instead: they read the table at its Q4_0 size.
+
+#include <algorithm>
+
+#include "q4_gemm16.h"
+#include "q4_kernels.h"
+
+namespace q4 {
+namespace {
+
+constexpr float P_SCALE = 0x1p14f;  // probabilities relative to the row's maximum, scaled into binary16
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+// exp(a - b) for a <= b; 1 where both are the same infinity.
+__device__ __forceinline__ float exp_below(float a, float b) { return a == b ? 1.f : expf(a - b); }
+
+// Per row, one wave each.  GRAD: the new running maximum, alpha = the factor
+// that moves sums and gradients to it, and the running sum with the previous
+// piece's partial sums (psum [chunks][M]).  Else: the piece's own (tmax,
+// tsum) entries folded into the running pair.
+template <bool GRAD>
+__global__ __launch_bounds__(256) void xent_rows_kernel(const float* __restrict__ tmax,
+                                                        const float* __restrict__ tsum,
+                                                        int64_t entries, int64_t tld,
+                                                        const float* __restrict__ psum, int chunks,
+                                                        float* __restrict__ run_max,
+                                                        float* __restrict__ run_sum,
+                                                        float* __restrict__ alpha, int64_t M,
+                                                        bool first) {
+  const int lane = threadIdx.x & 63;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (m >= M) return;
+  float top = -__builtin_inff();
+  for (int64_t e = lane; e < entries; e += 64) top = fmaxf(top, tmax[m * tld + e]);
+  top = wave_max(top);
+  const float old = first ? -__builtin_inff() : run_max[m];
+  top = fmaxf(top, old);
+  const float al = first ? 0.f : exp_below(old, top);
+  float s = 0.f;
+  if constexpr (GRAD) {
+    if (!first)
+      for (int c = lane; c < chunks; c += 64) s += psum[static_cast<int64_t>(c) * M + m];
+    s = wave_sum(s);
+    if (lane == 0) {
+      run_sum[m] = first ? 0.f : (run_sum[m] + s) * al;
+      alpha[m] = al;
+      run_max[m] = top;
+    }
+  } else {
+    for (int64_t e = lane; e < entries; e += 64) {
+      const float t = tsum[m * tld + e];
+      if (t != 0.f) s += t * exp_below(tmax[m * tld + e], top);
+    }
+    s = wave_sum(s);
+    if (lane == 0) {
+      run_sum[m] = (first ? 0.f : run_sum[m] * al) + s;
+      run_max[m] = top;
+    }
+  }
+}
+
+// Probabilities of a piece relative to the running maximum, as operand
+// fragments (NATURAL over the columns), 16 rows x `chunk` columns per
+// workgroup; the target's is left out.  psum[chunk][m] their float32 sums.
+constexpr int PC_CHUNK = 2048;
+template <int PARTS>
+__global__ __launch_bounds__(256) void xent_prob_kernel(const float* __restrict__ logits,
+                                                        const float* __restrict__ run_max,
+                                                        const int32_t* __restrict__ targets,
+                                                        f16x8* __restrict__ out,
+                                                        float* __restrict__ psum,
+                                                        float* __restrict__ tlogit, int64_t M,
+                                                        int64_t cols, int64_t ld, int64_t n0,
+                                                        int64_t N) {
+  __shared__ float red[4][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t rt = blockIdx.x, m = rt * 16 + i, CB = cols / 32;
+  const bool live = m < M;
+  const float top = live ? run_max[m] : 0.f;
+  const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 : -1;
+  const int64_t b1 = min(CB, static_cast<int64_t>(blockIdx.y + 1) * (PC_CHUNK / 32));
+  const int64_t part = static_cast<int64_t>(gridDim.x) * CB * 64;
+  float sum = 0.f;
+  for (int64_t b = static_cast<int64_t>(blockIdx.y) * (PC_CHUNK / 32) + wave; b < b1; b += 4) {
+    const int64_t n = b * 32 + 8 * g;
+    f16x8 hi = {}, lo = {};
+    if (live) {
+      float l[8];
+      const f32x4 a = *reinterpret_cast<const f32x4*>(logits + m * ld + n);
+      const f32x4 c = *reinterpret_cast<const f32x4*>(logits + m * ld + n + 4);
+      l[0] = a.x; l[1] = a.y; l[2] = a.z; l[3] = a.w;
+      l[4] = c.x; l[5] = c.y; l[6] = c.z; l[7] = c.w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float p = 0.f;
+        if (n0 + n + e < N) {
+          if (t == n + e) {
+            tlogit[m] = l[e];
+          } else {
+            p = exp_below(l[e], top);
+          }
+        }
+        sum += p;
+        p *= P_SCALE;
+        hi[e] = static_cast<_Float16>(p);
+        if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(p - static_cast<float>(hi[e]));
+      }
+    }
+    const int64_t at = (rt * CB + b) * 64 + lane;
+    out[at] = hi;
+    if constexpr (PARTS == 2) out[part + at] = lo;
+  }
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (lane < 16) red[wave][lane] = sum;
+  __syncthreads();
+  if (threadIdx.x < 16 && rt * 16 + threadIdx.x < M) {
+    const int r = threadIdx.x;
+    psum[static_cast<int64_t>(blockIdx.y) * M + rt * 16 + r] =
+        ((red[0][r] + red[1][r]) + red[2][r]) + red[3][r];
+  }
+}
+
+// loss, lse and (dx not null) the gradient: one workgroup per row.
+template <typename T>
+__global__ __launch_bounds__(256) void xent_final_kernel(
+    const float* __restrict__ run_max, const float* __restrict__ run_sum,
+    const float* __restrict__ psum, int chunks, const float* __restrict__ tlogit,
+    const int32_t* __restrict__ targets, const float* __restrict__ dloss,
+    const float* __restrict__ part, int splits, const uint8_t* __restrict__ W,
+    float* __restrict__ loss, float* __restrict__ lse, T* __restrict__ dx, int64_t M, int64_t N,
+    int64_t K) {
+  const int64_t m = blockIdx.x;
+  const int64_t t = targets[m];
+  const bool valid = t >= 0 && t < N;
+  float rest = run_sum[m];  // exp sum without the target, relative to the maximum
+  for (int c = 0; c < chunks; ++c) rest += psum[static_cast<int64_t>(c) * M + m];
+  const float top = run_max[m];
+  const float et = valid ? exp_below(tlogit[m], top) : 0.f;
+  if (threadIdx.x == 0) {
+    lse[m] = top + logf(rest + et);
+    loss[m] = !valid ? 0.f
+              : et >= rest ? log1pf(rest / et)
+                           : logf(rest + et) + (top - tlogit[m]);
+  }
+  if (!dx) return;
+  const float g = valid ? (dloss ? dloss[m] : 1.f) : 0.f;
+  const float f = 1.f / (rest + et);
+  T* o = dx + m * K;
+  for (int64_t k = 4 * threadIdx.x; k < K; k += 1024) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (valid) {
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < splits; ++p)
+        s += *reinterpret_cast<const f32x4*>(part + (static_cast<int64_t>(p) * M + m) * K + k);
+      const uint8_t* blk = W + (t * (K / 32) + k / 32) * BLOCK_BYTES;
+      const float d = half_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
+      const int j = static_cast<int>(k & 31);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t b = blk[2 + ((j + e) & 15)];
+        const float w = (static_cast<float>(j < 16 ? b & 15u : b >> 4) - 8.f) * d;
+        v[e] = g * (f * (s[e] * (1.f / P_SCALE) - rest * w));
+      }
+    }
+    store_f32<4>(o + k, v);
+  }
+}
+
+// Maximum and sum (without the target) of a chunk of a row's logits.
+constexpr int FEW_CHUNK = 4096;
+__global__ __launch_bounds__(256) void xent_chunk_kernel(const float* __restrict__ logits,
+                                                         const int32_t* __restrict__ targets,
+                                                         float* __restrict__ tmax,
+                                                         float* __restrict__ tsum,
+                                                         float* __restrict__ tlogit, int64_t N) {
+  __shared__ float red[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = blockIdx.y;
+  const float* l = logits + m * N;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * FEW_CHUNK, t = targets[m];
+  float v[FEW_CHUNK / 256], top = -__builtin_inff();
+#pragma unroll
+  for (int u = 0; u < FEW_CHUNK / 256; ++u) {
+    const int64_t n = n0 + u * 256 + threadIdx.x;
+    v[u] = n < N ? l[n] : -__builtin_inff();
+    top = fmaxf(top, v[u]);
+  }
+  top = wave_max(top);
+  if (lane == 0) red[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int u = 0; u < FEW_CHUNK / 256; ++u) {
+    const int64_t n = n0 + u * 256 + threadIdx.x;
+    if (n < N) {
+      if (n == t)
+        tlogit[m] = v[u];
+      else
+        s += exp_below(v[u], top);
+    }
+  }
+  s = wave_sum(s);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    tmax[m * gridDim.x + blockIdx.x] = top;
+    tsum[m * gridDim.x + blockIdx.x] = ((red[0] + red[1]) + red[2]) + red[3];
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, float* __restrict__ out,
+                                                    int64_t quads) {
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < quads;
+       e += static_cast<int64_t>(gridDim.x) * 256) {
+    float v[4];
+    load_f32<4>(x + 4 * e, v);
+    store_f32<4>(out + 4 * e, v);
+  }
+}
+
+// Rows whose loss alone goes through the matvec-accuracy kernels.
+constexpr int64_t FEW_ROWS = 16;
+
+struct XentPlan {
+  bool few;
+  int pa, pp, pb, splits;      // parts of x, of the probabilities and of the transposed weights
+  Tile t1, t2;
+  int64_t piece, entries, chunks;
+  size_t x, inv, run_max, run_sum, tlogit, alpha, tmax, tsum, psum, logits, codes, scale, wt, prob,
+      part, total;
+};
+
+XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus) {
+  XentPlan p = {};
+  Carver c;
+  p.few = !grad && M <= FEW_ROWS;
+  p.run_max = c.take(M * 4);
+  p.run_sum = c.take(M * 4);
+  p.tlogit = c.take(M * 4);
+  if (p.few) {
+    p.entries = (N + FEW_CHUNK - 1) / FEW_CHUNK;
+    if (type != TYPE_F32) p.x = c.take(static_cast<size_t>(M) * K * 4);
+    p.logits = c.take(static_cast<size_t>(M) * N * 4);
+    p.tmax = c.take(static_cast<size_t>(M) * p.entries * 4);
+    p.tsum = c.take(static_cast<size_t>(M) * p.entries * 4);
+    p.total = c.at;
+    return p;
+  }
+  p.pa = type == TYPE_F32 ? 2 : 1;
+  p.pp = p.pa;  // probabilities and weights: binary16's 11 bits below a 16-bit result's rounding
+  p.pb = p.pa;
+  // pieces of equal size, their logits up to 256 MiB
+  const int64_t cap = std::max<int64_t>(2048, std::min<int64_t>(32768, (int64_t(1) << 26) / M / 256 * 256));
+  const int64_t pieces = (N + cap - 1) / cap;
+  p.piece = ((N + pieces - 1) / pieces + 255) / 256 * 256;
+  p.piece = std::min<int64_t>(p.piece, (N + 63) / 64 * 64);
+  p.entries = p.piece / 64;
+  p.chunks = (p.piece + PC_CHUNK - 1) / PC_CHUNK;
+  double best1 = 1e30, best2 = 1e30;
+  for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
+    const double us = tile_time_us(t, M, p.piece, K, p.pa, 1, cus);
+    if (us < best1) {
+      best1 = us;
+      p.t1 = t;
+    }
+    for (int s = 1; s <= 16 && (s == 1 || p.piece / s >= 128); ++s) {
+      const double u2 = tile_time_us(t, M, K, p.piece, p.pp + p.pb - 1, s, cus);
+      if (u2 < best2) {
+        best2 = u2;
+        p.t2 = t;
+        p.splits = s;
+      }
+    }
+  }
+  p.splits = even_splits(p.piece / 32, p.splits);
+  p.x = c.take(static_cast<size_t>(frag_elems(M, K)) * 16 * p.pa);
+  p.inv = c.take(M * 4);
+  p.alpha = c.take(M * 4);
+  p.tmax = c.take(static_cast<size_t>(M) * p.entries * 4);
+  p.codes = c.take(static_cast<size_t>(frag_elems(p.piece, K)) * 16);
+  p.scale = c.take(static_cast<size_t>(p.piece) * blocks32(K) * 4);
+  if (grad) {
+    p.psum = c.take(static_cast<size_t>(p.chunks) * M * 4);
+    p.logits = c.take(static_cast<size_t>(M) * p.piece * 4);
+    p.wt = c.take(static_cast<size_t>(K) * p.piece * 2 * p.pb);
+    p.prob = c.take(static_cast<size_t>(frag_elems(M, p.piece)) * 16 * p.pp);
+    p.part = c.take(static_cast<size_t>(p.splits) * M * K * 4);
+  } else {
+    p.tsum = c.take(static_cast<size_t>(M) * p.entries * 4);
+  }
+  p.total = c.at;
+  return p;
+}
+
+#define Q4_TRY(expr)                          \
+  do {                                        \
+    const hipError_t e_ = (expr);             \
+    if (e_ != hipSuccess) return e_;          \
+  } while (0)
+
+}  // namespace
+
+size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus) {
+  return xent_plan(type, grad, M, N, K, cus).total;
+}
+
+hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, const float* dloss,
+                       float* loss, float* lse, void* dx, int type, int64_t M, int64_t N, int64_t K,
+                       void* ws, int cus, hipStream_t s) {
+  const bool grad = dx != nullptr;
+  const XentPlan p = xent_plan(type, grad, M, N, K, cus);
+  char* base = static_cast<char*>(ws);
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+  float *run_max = f32(p.run_max), *run_sum = f32(p.run_sum), *tlogit = f32(p.tlogit);
+  const dim3 rows4(static_cast<unsigned>((M + 3) / 4));
+  const float* psum = nullptr;
+  int chunks = 0;
+  const float* part = nullptr;
+
+  if (p.few) {
+    const float* xf = static_cast<const float*>(x);
+    if (type != TYPE_F32) {
+      const int64_t quads = M * K / 4;
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 1024));
+      if (type == TYPE_F16)
+        hipLaunchKernelGGL(widen_kernel<_Float16>, dim3(grid), dim3(256), 0, s,
+                           static_cast<const _Float16*>(x), f32(p.x), quads);
+      else
+        hipLaunchKernelGGL(widen_kernel<__bf16>, dim3(grid), dim3(256), 0, s,
+                           static_cast<const __bf16*>(x), f32(p.x), quads);
+      Q4_TRY(hipGetLastError());
+      xf = f32(p.x);
+    }
+    for (int64_t m = 0; m < M; m += 4)
+      Q4_TRY(launch_matmul(w, xf + m * K, f32(p.logits) + m * N, nullptr, std::min<int64_t>(4, M - m),
+                           N, K, nullptr, 0, cus, s));
+    hipLaunchKernelGGL(xent_chunk_kernel,
+                       dim3(static_cast<unsigned>(p.entries), static_cast<unsigned>(M)), dim3(256), 0,
+                       s, f32(p.logits), targets, f32(p.tmax), f32(p.tsum), tlogit, N);
+    hipLaunchKernelGGL(xent_rows_kernel<false>, rows4, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
+                       p.entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, true);
+    Q4_TRY(hipGetLastError());
+  } else {
+    f16x8* xa = reinterpret_cast<f16x8*>(base + p.x);
+    f16x8* codes = reinterpret_cast<f16x8*>(base + p.codes);
+    f16x8* wt = grad ? reinterpret_cast<f16x8*>(base + p.wt) : nullptr;
+    f16x8* prob = reinterpret_cast<f16x8*>(base + p.prob);
+    Q4_TRY(prep_rows(x, type, Order::NIBBLE, p.pa, xa, f32(p.inv), M, K, s));
+    for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
+      const bool first = n0 == 0;
+      const int64_t cols = std::min<int64_t>(p.piece, (N - n0 + 63) / 64 * 64);
+      Q4_TRY(prep_weights(w, n0, cols, N, K, codes, f32(p.scale), wt, p.pb, s));
+      LogitGemm lg = {};
+      lg.a = xa;
+      lg.q = codes;
+      lg.pa = p.pa;
+      lg.scale = f32(p.scale);
+      lg.inv = f32(p.inv);
+      lg.M = M;
+      lg.cols = cols;
+      lg.CB = blocks32(K);
+      lg.n0 = n0;
+      lg.N = N;
+      lg.targets = targets;
+      lg.logits = grad ? f32(p.logits) : nullptr;
+      lg.tmax = f32(p.tmax);
+      lg.tsum = grad ? nullptr : f32(p.tsum);
+      lg.tlogit = tlogit;
+      lg.ld = p.piece;
+      lg.tld = p.entries;
+      Q4_TRY(launch_gemm_logits(p.t1, lg, s));
+      const int64_t entries = cols / 64;
+      if (!grad) {
+        hipLaunchKernelGGL(xent_rows_kernel<false>, rows4, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
+                           entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, first);
+        Q4_TRY(hipGetLastError());
+        continue;
+      }
+      // `chunks` still is the previous piece's count
+      hipLaunchKernelGGL(xent_rows_kernel<true>, rows4, dim3(256), 0, s, f32(p.tmax), nullptr,
+                         entries, p.entries, f32(p.psum), chunks, run_max, run_sum, f32(p.alpha), M,
+                         first);
+      chunks = static_cast<int>((cols + PC_CHUNK - 1) / PC_CHUNK);
+      const dim3 pg(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>(chunks));
+      if (p.pp == 2)
+        hipLaunchKernelGGL(xent_prob_kernel<2>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
+                           prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
+      else
+        hipLaunchKernelGGL(xent_prob_kernel<1>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
+                           prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
+      Q4_TRY(hipGetLastError());
+      // a shorter last piece may fill fewer slices: the others keep their sums
+      // but still have to move to the new maximum, so every piece uses p.splits
+      PlainGemm g = {};
+      g.a = prob;
+      g.b = wt;
+      g.pa = p.pp;
+      g.pb = p.pb;
+      g.M = M;
+      g.N = K;
+      g.CB = cols / 32;
+      g.splits = p.splits;
+      g.out = f32(p.part);
+      g.ld = K;
+      g.alpha = first ? nullptr : f32(p.alpha);
+      Q4_TRY(launch_gemm_plain(p.t2, g, s));
+    }
+    if (grad) {
+      psum = f32(p.psum);
+      part = f32(p.part);
+    }
+  }
+  const dim3 grid(static_cast<unsigned>(M));
+  const int splits = grad ? p.splits : 0;
+  if (type == TYPE_F32)
+    hipLaunchKernelGGL(xent_final_kernel<float>, grid, dim3(256), 0, s, run_max, run_sum, psum,
+                       chunks, tlogit, targets, dloss, part, splits, w, loss, lse,
+                       static_cast<float*>(dx), M, N, K);
+  else if (type == TYPE_F16)
+    hipLaunchKernelGGL(xent_final_kernel<_Float16>, grid, dim3(256), 0, s, run_max, run_sum, psum,
+                       chunks, tlogit, targets, dloss, part, splits, w, loss, lse,
+                       static_cast<_Float16*>(dx), M, N, K);
+  else
+    hipLaunchKernelGGL(xent_final_kernel<__bf16>, grid, dim3(256), 0, s, run_max, run_sum, psum,
+                       chunks, tlogit, targets, dloss, part, splits, w, loss, lse,
+                       static_cast<__bf16*>(dx), M, N, K);
+  return hipGetLastError();
+}
+
+}  // namespace q4

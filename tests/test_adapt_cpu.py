@@ -70,3 +70,54 @@ def test_lora_binding_refusals():
                 dict(da=torch.zeros(2, 8, 64).half()), dict(db=torch.zeros(2, 8, 32)), {}):
         with pytest.raises(ValueError):
             q4.lora_grad(**{**dict(x=x, dy=dy, a=a, b=b, ids=ids), **bad})
+
+
+DX = dict(w=A, dy=A, dx=A, type=0, M=4, N=64, K=64, ws=A, ws_bytes=BIG, stream=None)
+XENT = dict(w=A, x=A, targets=A, dloss=A, loss=A, lse=A, dx=A, type=0, M=4, N=64, K=64, ws=A,
+            ws_bytes=BIG, stream=None)
+
+
+def _need(fn, type=0, **change):
+    a = dict(type=type, M=4, N=64, K=64, **({"grad": 1} if "xent" in fn else {}))
+    a.update(change)
+    order = (["type", "grad"] if "xent" in fn else ["type"]) + ["M", "N", "K"]
+    return int(getattr(q4.lib(), fn + "_workspace_bytes")(*[a[k] for k in order]))
+
+
+@pytest.mark.parametrize("fn,base,required,optional,shapes", [
+    ("q4_matmul_dx", DX, ("w", "dy", "dx"), (),
+     (dict(M=0), dict(M=(1 << 20) + 1), dict(N=0), dict(N=(1 << 22) + 1), dict(K=0), dict(K=40),
+      dict(K=1 << 23), dict(M=1 << 20, K=1 << 14), dict(M=1 << 20, N=1 << 14), dict(N=1 << 22, K=1 << 12))),
+    ("q4_lmhead_xent", XENT, ("w", "x", "targets", "loss", "lse"), ("dloss", "dx"),
+     (dict(M=0), dict(M=65537), dict(N=0), dict(N=1 << 31), dict(K=0), dict(K=40), dict(K=1 << 23),
+      dict(N=1 << 30, K=32), dict(M=65536, K=1 << 18)))])
+def test_dx_and_xent_refusals(fn, base, required, optional, shapes):
+    for name in required:
+        assert _call(fn, base, **{name: None}) == q4.Q4_ERR_NULL, name
+    for name in required + optional + ("ws",):
+        assert _call(fn, base, **{name: A + 8}) == q4.Q4_ERR_ALIGN, name
+    for t in (2, 8, -1, 31):
+        assert _call(fn, base, type=t) == q4.Q4_ERR_FORMAT
+        assert _need(fn, t) == 0
+    for bad in shapes:
+        assert _call(fn, base, **bad) == q4.Q4_ERR_SHAPE, bad
+        assert _need(fn, **bad) == 0, bad
+    for t in (0, 1, 30):
+        need = _need(fn, t)
+        assert need > 0
+        assert _call(fn, base, type=t, ws_bytes=need - 1) == q4.Q4_ERR_WORKSPACE
+    assert _call(fn, base, ws=None) == q4.Q4_ERR_WORKSPACE
+
+
+def test_dx_and_xent_binding_refusals():
+    w = torch.zeros((8, 36), dtype=torch.uint8)
+    dy, x, t = torch.zeros(4, 8), torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    for bad in (dict(dy=dy[0]), dict(dy=dy[:, :7]), dict(dy=dy.double()), dict(out=torch.zeros(4, 63)),
+                dict(out=x.half()), dict(w_q4=w[:, ::2]), {}):
+        with pytest.raises(ValueError):
+            q4.matmul_dx(**{**dict(w_q4=w, dy=dy), **bad})
+    for bad in (dict(x=x[0]), dict(x=x[:, :32]), dict(x=x.double()), dict(targets=t.long()),
+                dict(targets=t[:3]), dict(dloss=torch.zeros(3)), dict(loss=torch.zeros(4).half()),
+                dict(dx=x.half()), dict(lse=torch.zeros(4, 1)), {}):
+        with pytest.raises(ValueError):
+            q4.lmhead_xent(**{**dict(w_q4=w, x=x, targets=t), **bad})
