@@ -388,8 +388,8 @@ q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets
  *   4194304, R a multiple of 8 from 8 to 128, 1 <= adapters <= 65535.
  *   workspace : q4_lora_workspace_bytes(M, N, K, R) bytes of device scratch;
  *           its contents do not matter.  Calls that share it must be ordered.
- * Two launches; A_a x is kept in float32.  Deterministic, and a row's result
- * does not depend on the other rows of its call.
+ * Two launches; A_a x is kept in float32.  Deterministic; the order of a row's
+ * float32 sums depends on the sizes and on how many rows share its adapter.
  */
 size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 q4_status q4_lora(const void* x, const void* a, const void* b, const float* scale,
@@ -410,7 +410,7 @@ q4_status q4_lora(const void* x, const void* a, const void* b, const float* scal
  *           least one of dx, da, db is given.
  *   Rows without an adapter: dx = r, nothing to da and db.  s_a is a constant.
  *   Ranges as for q4_lora, and adapters * (ceil(K/64) + ceil(N/64)) <= 2^21.
- * Two launches.  Deterministic.
+ * Three launches.  Deterministic.
  */
 size_t q4_lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 q4_status q4_lora_grad(const void* x, const void* dy, const void* a, const void* b,

@@ -9,16 +9,20 @@
 //
 // The rank is small (8 to 128), so every product streams a long operand (x,
 // dy, A, B, y) past a small one; what bounds them is bytes, and for a decode
-// step the two dependent launches.  All sums are float32 on the matrix cores
-// (v_mfma_f32_16x16x4_f32 takes float32 operands, so values of every type
-// enter exactly), in a fixed order.
+// step the two dependent launches.  Products run on the matrix cores as
+// bfloat16 with float32 sums, in a fixed order: a value enters as one, two or
+// three bfloat16 parts (bfloat16, float16, float32: the leading 8 bits of
+// what is left, exact), and the products of parts below 2^-24 of the whole are
+// dropped.  One v_mfma_f32_16x16x32_bf16 takes the reduction steps of eight
+// float32 MFMAs in a sixteenth of their time, so six of them are still faster.
 //
 // A first launch contracts the long axis ("down": rank vectors h and g),
-// split over workgroups into slices that the second launch adds while it
-// loads them.  Rows are taken 16 at a time; within a tile the rows that share
-// an adapter (not necessarily adjacent) form a group, and the groups of a
-// tile are dealt to gridDim.y workgroups, so a decode batch whose rows all
-// use different adapters reads those adapters in parallel.
+// split over workgroups into slices that the next launch adds.  Rows are
+// taken 64 at a time; within a tile the rows that share an adapter (not
+// necessarily adjacent) form a group, and the groups of a tile are dealt to
+// gridDim.y workgroups, so a decode batch whose rows all use different
+// adapters reads those adapters in parallel, and a prompt reads its adapter
+// once for 64 rows.
 //
 // MFMA operand layout: lane l = i + 16 g (i < 16, g < 4) carries row / column
 // i and one reduction index of group g; any permutation of the reduction axis
@@ -32,47 +36,105 @@
 namespace q4 {
 namespace {
 
-constexpr int LT = 16;          // rows per tile
+constexpr int LT = 64;          // rows per tile
+constexpr int SUB = LT / 16;    // MFMA row blocks of a tile
 constexpr int DOWN_WAVES = 8;   // waves of a "down" workgroup, each its part of the long axis
 constexpr int DOWN_STEP = 32;   // reduction indices per wave and step
+constexpr int FEW = 4;          // groups of up to this many rows take the vector unit
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// The adapter groups of a 16-row tile: calls f(rows, id) for every group that
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight values as sums of NP bfloat16 parts.
+template <int NP>
+struct Parts {
+  bf16x8 p[NP];
+};
+template <typename T>
+constexpr int parts_of = sizeof(T) == 4 ? 3 : (__is_same(T, __bf16) ? 1 : 2);
+
+__device__ __forceinline__ uint32_t pack_high(float a, float b) {  // the high halves of a and b
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
+// Leading 8 significant bits, then the rest's (truncation: exact remainders).
+template <int NP>
+__device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
+  Parts<NP> out;
+  float r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = v[e];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_high(r[2 * e], r[2 * e + 1]);
+    out.p[p] = __builtin_bit_cast(bf16x8, w);
+    if (p + 1 < NP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] -= __uint_as_float(__float_as_uint(r[e]) & 0xFFFF0000u);
+    }
+  }
+  return out;
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma_parts(const Parts<NA>& a, const Parts<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)  // small products first
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], c, 0, 0, 0);
+  return c;
+}
+
+// The adapter groups of a 64-row tile: calls f(rows, id) for every group that
 // falls to this workgroup, rows a mask of the tile's rows.  Uniform over the
 // workgroup (every wave reads the same ids).
 template <typename F>
 __device__ __forceinline__ void for_groups(const int32_t* __restrict__ ids, int64_t m0, int64_t M,
                                            int adapters, int mine, int of, F f) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = m0 + (lane & 15);
+  const int64_t row = m0 + (threadIdx.x & 63);
   const int id = row < M ? ids[row] : -1;
-  unsigned left = static_cast<unsigned>(__ballot(id >= 0 && id < adapters)) & 0xFFFFu;
+  uint64_t left = __ballot(id >= 0 && id < adapters);
   for (int n = 0; left != 0u; ++n) {
-    const int first = __builtin_ctz(left);
-    const int a = __builtin_amdgcn_readlane(id, first);
-    const unsigned same = static_cast<unsigned>(__ballot(id == a)) & left;
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const uint64_t same = __ballot(id == a);
     left &= ~same;
     if (n % of == mine) f(same, a);
   }
 }
 
 // Rows of the tile inside [0, M) that have no adapter.
-__device__ __forceinline__ unsigned rows_without(const int32_t* __restrict__ ids, int64_t m0,
+__device__ __forceinline__ uint64_t rows_without(const int32_t* __restrict__ ids, int64_t m0,
                                                  int64_t M, int adapters) {
-  const int64_t row = m0 + (threadIdx.x & 15);
+  const int64_t row = m0 + (threadIdx.x & 63);
   const int id = row < M ? ids[row] : 0;
-  return static_cast<unsigned>(__ballot(row < M && (id < 0 || id >= adapters))) & 0xFFFFu;
+  return __ballot(row < M && (id < 0 || id >= adapters));
+}
+
+// Which 16-row blocks of the tile hold rows of the mask.
+__device__ __forceinline__ unsigned blocks_of(uint64_t rows) {
+  unsigned b = 0;
+#pragma unroll
+  for (int s = 0; s < SUB; ++s) b |= ((rows >> (16 * s)) & 0xFFFFu) != 0u ? 1u << s : 0u;
+  return b;
 }
 
 // Eight consecutive elements c .. c + 7 of a row of C elements (zeros past
-// its end); VEC: C % 8 == 0 and the row is 16-byte aligned.
+// its end, or where `live` is false); VEC: C % 8 == 0 and the row is 16-byte
+// aligned.
 template <bool VEC, typename T>
-__device__ __forceinline__ void row8(const T* __restrict__ row, int64_t c, int64_t C, float (&v)[8]) {
+__device__ __forceinline__ void row8(const T* __restrict__ row, int64_t c, int64_t C, bool live,
+                                     float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
   if constexpr (VEC) {
-    if (c < C) {
+    if (live && c < C) {
       if constexpr (sizeof(T) == 4) {
         float lo[4], hi[4];
         load_f32<4>(row + c, lo);
@@ -82,13 +144,60 @@ __device__ __forceinline__ void row8(const T* __restrict__ row, int64_t c, int64
       } else {
         load_f32<8>(row + c, v);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < C ? to_f32(row[c + e]) : 0.f;
+    for (int e = 0; e < 8; ++e)
+      if (live && c + e < C) v[e] = to_f32(row[c + e]);
+  }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ Parts<parts_of<T>> load_parts(const T* __restrict__ row, int64_t c,
+                                                         int64_t C, bool live) {
+  if constexpr (VEC && __is_same(T, __bf16)) {
+    Parts<1> out = {};
+    if (live && c < C) out.p[0] = *reinterpret_cast<const bf16x8*>(row + c);
+    return out;
+  } else {
+    float v[8];
+    row8<VEC>(row, c, C, live, v);
+    return split8<parts_of<T>>(v);
+  }
+}
+
+// Part of the sum over c of Z[m, c] F_a[j, c] for NS blocks of 16 rows (row
+// block s starts at zrow[s]): this wave's steps of [c0, c1).
+template <typename T, typename TA, bool FT, bool VEC, int RT, int NS>
+__device__ __forceinline__ void down_steps(const T* const (&zrow)[NS], const bool (&live)[NS],
+                                           const TA* __restrict__ f, int64_t c0, int64_t c1,
+                                           int64_t C, int R, int i, int g, f32x4 (&acc)[NS][RT]) {
+#pragma unroll 1
+  for (int64_t cs = c0; cs < c1; cs += DOWN_WAVES * DOWN_STEP) {
+    const int64_t c = cs + 8 * g;  // this lane's reduction indices c .. c + 7
+    Parts<parts_of<T>> z[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) z[s] = load_parts<VEC>(zrow[s], c, C, live[s]);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int j = 16 * t + i;
+      Parts<parts_of<TA>> w;
+      if constexpr (FT && __is_same(TA, __bf16)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w.p[0][e] = (j < R && c + e < C) ? f[(c + e) * R + j] : static_cast<__bf16>(0.f);
+      } else if constexpr (FT) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = (j < R && c + e < C) ? to_f32(f[(c + e) * R + j]) : 0.f;
+        w = split8<parts_of<TA>>(v);
+      } else {
+        w = load_parts<true>(f + static_cast<int64_t>(j) * C, c, C, j < R);
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) acc[s][t] = mfma_parts(z[s], w, acc[s][t]);
+    }
   }
 }
 
@@ -100,69 +209,77 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
                                           const int32_t* __restrict__ ids, float* __restrict__ P,
                                           int64_t M, int64_t C, int R, int adapters, int64_t tile,
                                           int split, int64_t span, int mine, int of,
-                                          f32x4 (*red)[64]) {
+                                          f32x4 (*red)[4][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int64_t m0 = tile * LT;
-  const T* zrow = Z + min(m0 + i, M - 1) * C;
-  const int64_t c0 = split * span, c1 = min(C, c0 + span);
-  for_groups(ids, m0, M, adapters, mine, of, [&](unsigned rows, int a) {
+  const int64_t c0 = split * span + wave * DOWN_STEP, c1 = min(C, (split + 1) * span);
+  for_groups(ids, m0, M, adapters, mine, of, [&](uint64_t rows, int a) {
     const TA* f = F + static_cast<int64_t>(a) * R * C;
-    f32x4 acc[RT];
+    // the waves' parts of the 16 x 16 results of blocks s0, s0 + 1, ..., four at
+    // a time, added in wave order
+    auto finish = [&](auto& acc, int s0) {
+      constexpr int NB = sizeof(acc) / sizeof(f32x4);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t cs = c0 + wave * DOWN_STEP; cs < c1; cs += DOWN_WAVES * DOWN_STEP) {
-      const int64_t c = cs + 8 * g;  // this lane's reduction indices c .. c + 7
-      float z[8], w[RT][8];
-      row8<VEC>(zrow, c, C, z);
+      for (int q = 0; q < NB; q += 4) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int j = 16 * t + i;
-        if constexpr (FT) {
+        for (int u = 0; u < 4 && q + u < NB; ++u) red[wave][u][lane] = acc[(q + u) / RT][(q + u) % RT];
+        __syncthreads();
+        const int mine = q + wave;
+        if (wave < 4 && mine < NB) {
+          f32x4 sum = red[0][wave][lane];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[t][e] = (j < R && c + e < C) ? to_f32(f[(c + e) * R + j]) : 0.f;
-        } else {
-          if (j < R) {
-            row8<true>(f + static_cast<int64_t>(j) * C, c, C, w[t]);
-          } else {
+          for (int w = 1; w < DOWN_WAVES; ++w) sum += red[w][wave][lane];
+          const int j = 16 * (mine % RT) + i;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[t][e] = 0.f;
+          for (int v = 0; v < 4; ++v) {
+            const int row = 16 * (s0 + mine / RT) + 4 * g + v;
+            if (((rows >> row) & 1u) && j < R)
+              P[(static_cast<int64_t>(split) * M + m0 + row) * R + j] = sum[v];
           }
         }
+        __syncthreads();
       }
+    };
+    const unsigned blocks = blocks_of(rows);
+    if ((blocks & (blocks - 1)) == 0u) {
+      // rows of one block of 16 (a decode batch)
+      const int s = __builtin_ctz(blocks);
+      const T* const zrow[1] = {Z + min(m0 + 16 * s + i, M - 1) * C};
+      const bool live[1] = {((rows >> (16 * s + i)) & 1u) != 0u};
+      f32x4 acc[1][RT];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int t = 0; t < RT; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      down_steps<T, TA, FT, VEC, RT, 1>(zrow, live, f, c0, c1, C, R, i, g, acc);
+      finish(acc, s);
+    } else {
+      // as many blocks at once as the registers hold beside the factor
+      constexpr int NS = RT <= 2 ? SUB : SUB / 2;
+#pragma unroll 1
+      for (int s0 = 0; s0 < SUB; s0 += NS) {
+        if (((blocks >> s0) & ((1u << NS) - 1)) == 0u) continue;
+        const T* zrow[NS];
+        bool live[NS];
+        f32x4 acc[NS][RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = mfma_f32(z[e], w[t][e], acc[t]);
-    }
-    // the waves' parts, added in wave order
+        for (int s = 0; s < NS; ++s) {
+          zrow[s] = Z + min(m0 + 16 * (s0 + s) + i, M - 1) * C;
+          live[s] = ((rows >> (16 * (s0 + s) + i)) & 1u) != 0u;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      red[wave][lane] = acc[t];
-      __syncthreads();
-      if (wave == 0) {
-        f32x4 s = red[0][lane];
-#pragma unroll
-        for (int w = 1; w < DOWN_WAVES; ++w) s += red[w][lane];
-        const int j = 16 * t + i;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int row = 4 * g + v;
-          if (((rows >> row) & 1u) && j < R)
-            P[(static_cast<int64_t>(split) * M + m0 + row) * R + j] = s[v];
+          for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+        down_steps<T, TA, FT, VEC, RT, NS>(zrow, live, f, c0, c1, C, R, i, g, acc);
+        finish(acc, s0);
       }
-      __syncthreads();
     }
   });
 }
 
 template <typename T, typename TA, int RT>
-__global__ __launch_bounds__(64 * DOWN_WAVES) void lora_down_kernel(
+__global__ __launch_bounds__(64 * DOWN_WAVES, RT == 1 && sizeof(T) == 2 ? 4 : 2) void lora_down_kernel(
     const T* __restrict__ X, const TA* __restrict__ A, const int32_t* __restrict__ ids,
     float* __restrict__ P, int64_t M, int64_t K, int R, int adapters, int splits, int64_t span) {
-  __shared__ f32x4 red[DOWN_WAVES][64];
+  __shared__ f32x4 red[DOWN_WAVES][4][64];
   const int64_t tile = blockIdx.x / splits;
   const int split = static_cast<int>(blockIdx.x - tile * splits);
   down_body<T, TA, false, true, RT>(X, A, ids, P, M, K, R, adapters, tile, split, span, blockIdx.y,
@@ -172,12 +289,12 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_down_kernel(
 // Both rank vectors of the backward pass: workgroups below `hblocks` h (from
 // x), the rest g (from dy).
 template <typename T, typename TA, int RT, bool VEC>
-__global__ __launch_bounds__(64 * DOWN_WAVES) void lora_down2_kernel(
+__global__ __launch_bounds__(64 * DOWN_WAVES, RT == 1 && sizeof(T) == 2 ? 4 : 2) void lora_down2_kernel(
     const T* __restrict__ X, const T* __restrict__ DY, const TA* __restrict__ A,
     const TA* __restrict__ B, const int32_t* __restrict__ ids, float* __restrict__ PH,
     float* __restrict__ PG, int64_t M, int64_t N, int64_t K, int R, int adapters, int hsplits,
     int64_t hspan, int gsplits, int64_t gspan, unsigned hblocks) {
-  __shared__ f32x4 red[DOWN_WAVES][64];
+  __shared__ f32x4 red[DOWN_WAVES][4][64];
   if (blockIdx.x < hblocks) {
     const int64_t tile = blockIdx.x / hsplits;
     const int split = static_cast<int>(blockIdx.x - tile * hsplits);
@@ -192,130 +309,258 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_down2_kernel(
   }
 }
 
-// hs[row][j] = s_a * (the slices' sum), for the rows of a group; zero for the
-// other rows and for j in [R, R rounded up to 16).
-constexpr int HS_LD = 132;  // row stride in floats: 16-byte aligned, rows on different banks
-__device__ __forceinline__ void load_rank(const float* __restrict__ P, int splits, int64_t M, int R,
-                                          int64_t m0, unsigned rows, float scale,
-                                          float (*hs)[HS_LD]) {
-  const int R16 = (R + 15) & ~15;
-  for (int e = threadIdx.x; e < LT * R16; e += blockDim.x) {
-    const int row = e / R16, j = e - row * R16;
-    float s = 0.f;
-    if (((rows >> row) & 1u) && j < R) {
-      const float* p = P + (m0 + row) * R + j;
-      for (int t = 0; t < splits; ++t) s += p[static_cast<int64_t>(t) * M * R];
-      s *= scale;
-    }
-    hs[row][j] = s;
+// The slices' sum of one element, in slice order, eight loads in flight.
+__device__ __forceinline__ float sum_slices(const float* __restrict__ p, int splits, int64_t step) {
+  float s = 0.f;
+  for (int t = 0; t < splits; t += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = t + u < splits ? p[(t + u) * step] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
+  return s;
+}
+
+// The slices of h and g summed and scaled, once for the many workgroups that
+// read them.  H, G: [M][R].  HT, GT (nullable): their three bfloat16 parts,
+// transposed, [3][R][MP] with MP = M rounded up to 32.
+__global__ __launch_bounds__(256) void lora_sum_kernel(
+    const float* __restrict__ PH, const float* __restrict__ PG, const float* __restrict__ scale,
+    const int32_t* __restrict__ ids, float* __restrict__ H, float* __restrict__ G,
+    uint16_t* __restrict__ HT, uint16_t* __restrict__ GT, int64_t M, int R, int adapters,
+    int hsplits, int gsplits, int64_t MP) {
+  const int64_t n = M * R;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n;
+       e += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t m = e / R, j = e - m * R;
+    const int id = ids[m];
+    const bool ok = id >= 0 && id < adapters;
+    const float s = ok && scale ? scale[id] : 1.f;
+    auto put = [&](const float* p, int splits, float* out, uint16_t* t) {
+      float v = ok ? s * sum_slices(p + e, splits, n) : 0.f;
+      out[e] = v;
+      if (!t) return;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const uint32_t bits = __float_as_uint(v);
+        t[(q * R + j) * MP + m] = static_cast<uint16_t>(bits >> 16);
+        v -= __uint_as_float(bits & 0xFFFF0000u);
+      }
+    };
+    if (hsplits) put(PH, hsplits, H, HT);
+    if (gsplits) put(PG, gsplits, G, GT);
   }
 }
 
+// Rank vectors of a group as NP bfloat16 parts in LDS, hs[part][row][ld]: scale
+// * (the slices' sum); zero for the tile's other rows and for j in [R, R
+// rounded up to 32).  ld = that + 8: rows 16-byte aligned, on different banks.
+__device__ __forceinline__ int rank_ld(int R) { return ((R + 31) & ~31) + 8; }
+template <int NP>
+constexpr size_t rank_lds(int64_t R) { return static_cast<size_t>(NP) * LT * (((R + 31) & ~31) + 8) * 2; }
+
+template <int NP>
+__device__ __forceinline__ void load_rank(const float* __restrict__ P, int splits, int64_t M, int R,
+                                          int64_t m0, uint64_t rows, float scale, uint16_t* hs) {
+  const int ld = rank_ld(R), o8 = (ld - 8) / 8;  // groups of eight in a row
+  for (int e = threadIdx.x; e < LT * o8; e += blockDim.x) {
+    const int row = e / o8, j = 8 * (e - row * o8);
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 0.f;
+    if (((rows >> row) & 1u) && j < R) {
+      const float* p = P + (m0 + row) * R + j;
+      for (int t = 0; t < splits; ++t) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(t) * M * R);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(t) * M * R + 4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) { v[u] += a[u]; v[4 + u] += b[u]; }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] *= scale;
+    }
+    const Parts<NP> q = split8<NP>(v);
+#pragma unroll
+    for (int u = 0; u < NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + row) * ld + j) = q.p[u];
+  }
+}
+
+template <int NP>
+__device__ __forceinline__ Parts<NP> rank_parts(const uint16_t* hs, int ld, int row, int j) {
+  Parts<NP> q;
+#pragma unroll
+  for (int u = 0; u < NP; ++u) q.p[u] = *reinterpret_cast<const bf16x8*>(hs + (u * LT + row) * ld + j);
+  return q;
+}
+
+// Parts of a rank vector that a result of type T needs: 16 bits of it are far
+// below a 16-bit result's rounding.
+template <typename T>
+constexpr int rank_np = sizeof(T) == 4 ? 3 : 2;
+
 // y[m, n] = r[m, n] + sum_j hs[m][j] B_a[n, j] for one tile of rows and the
-// columns [n0, n1).  Per wave 64 columns at a time: MFMA row rho of tile t is
-// column n = base + 16 (rho / 4) + 4 t + rho % 4, so a lane's results are 16
-// consecutive columns of one row.
+// columns [n0, n1).
+//  - Groups of up to FEW rows (decode): a lane per column, its row of B read
+//    in full, on the vector unit; loads and stores are contiguous.
+//  - Larger groups: 64 columns per wave on the matrix cores.  MFMA row rho of
+//    block t is column n = base + 16 (rho / 4) + 4 t + rho % 4, so a lane's
+//    results are 16 consecutive columns of one row; B is read once for the
+//    tile's 64 rows.
 template <typename T, typename TA, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(
     const float* __restrict__ P, const TA* __restrict__ B, const float* __restrict__ scale,
     const int32_t* __restrict__ ids, const T* R_, T* Y, int64_t M, int64_t N, int R, int adapters,
     int splits, int chunks, int64_t chunk) {
-  __shared__ float hs[LT][HS_LD];
+  extern __shared__ __attribute__((aligned(16))) uint16_t hs[];  // rank_lds<NP>(R) bytes
+  constexpr int NP = rank_np<T>;
+  const int ld = rank_ld(R);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int64_t tile = blockIdx.x / chunks;
   const int64_t n0 = (blockIdx.x - tile * chunks) * chunk, n1 = min(N, n0 + chunk);
   const int64_t m0 = tile * LT;
-  const bool vec = (N & 3) == 0;  // rows start on a 4-element boundary
+  constexpr int V = 16 / sizeof(T);       // elements of a 16-byte access
+  const bool vec = N % V == 0;            // rows start on a 16-byte boundary
 
+  // 16 consecutive columns of a row, base + 16 g on
   auto write = [&](int64_t base, int row, const f32x4 (&acc)[4]) {
-    const int64_t at = (m0 + row) * N + base + 16 * g;
+    const int64_t n = base + 16 * g, at = (m0 + row) * N + n;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t n = base + 16 * g + 4 * t;
-      float v[4] = {acc[t].x, acc[t].y, acc[t].z, acc[t].w};
+    for (int u = 0; u < 16; u += V) {
+      float v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = acc[(u + e) / 4][(u + e) % 4];
       if (vec) {
-        if (n < n1) {
+        if (n + u < n1) {
           if (R_) {
-            float q[4];
-            load_f32<4>(R_ + at + 4 * t, q);
+            float q[V];
+            load_f32<V>(R_ + at + u, q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += q[e];
+            for (int e = 0; e < V; ++e) v[e] += q[e];
           }
-          store_f32<4>(Y + at + 4 * t, v);
+          store_f32<V>(Y + at + u, v);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < n1)
-            Y[at + 4 * t + e] = from_f32<T>(R_ ? to_f32(R_[at + 4 * t + e]) + v[e] : v[e]);
+        for (int e = 0; e < V; ++e)
+          if (n + u + e < n1)
+            Y[at + u + e] = from_f32<T>(R_ ? to_f32(R_[at + u + e]) + v[e] : v[e]);
       }
     }
   };
 
-  for_groups(ids, m0, M, adapters, blockIdx.y, gridDim.y, [&](unsigned rows, int a) {
+  for_groups(ids, m0, M, adapters, blockIdx.y, gridDim.y, [&](uint64_t rows, int a) {
     __syncthreads();  // the previous group's rank vectors are no longer read
-    load_rank(P, splits, M, R, m0, rows, scale ? scale[a] : 1.f, hs);
-    __syncthreads();
     const TA* b = B + static_cast<int64_t>(a) * N * R;
-    for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES) {
-      f32x4 acc[4];
+    const float sc = scale ? scale[a] : 1.f;
+    const int count = __builtin_popcountll(rows);
+    if (count <= FEW) {
+      int at[FEW];
+      uint64_t left = rows;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < FEW; ++u) {
+        at[u] = left ? __builtin_ctzll(left) : at[0];
+        left &= left - 1;
+      }
+      float* hf = reinterpret_cast<float*>(hs);  // [FEW][R]
+      for (int e = threadIdx.x; e < FEW * R; e += 64 * WAVES) {
+        const int u = e / R, j = e - u * R;
+        const int row = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
+        if (u < count) hf[e] = sc * sum_slices(P + (m0 + row) * R + j, splits, M * R);
+      }
+      __syncthreads();
+      for (int64_t n = n0 + threadIdx.x; n < n1; n += 64 * WAVES) {
+        float acc[FEW] = {0.f, 0.f, 0.f, 0.f}, q[FEW];
+#pragma unroll
+        for (int u = 0; u < FEW; ++u) q[u] = u < count && R_ ? to_f32(R_[(m0 + at[u]) * N + n]) : 0.f;
+        const TA* brow = b + n * R;
+#pragma unroll 2
+        for (int j = 0; j < R; j += 8) {
+          float w[8];
+          row8<true>(brow, j, R, true, w);
+#pragma unroll
+          for (int u = 0; u < FEW; ++u) {
+            if (u < count) {
+              const f32x4 h0 = *reinterpret_cast<const f32x4*>(hf + u * R + j);
+              const f32x4 h1 = *reinterpret_cast<const f32x4*>(hf + u * R + j + 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                acc[u] = __builtin_fmaf(w[e], h0[e], acc[u]);
+                acc[u] = __builtin_fmaf(w[4 + e], h1[e], acc[u]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < FEW; ++u)
+          if (u < count) Y[(m0 + at[u]) * N + n] = from_f32<T>(q[u] + acc[u]);
+      }
+      return;
+    }
+    load_rank<NP>(P, splits, M, R, m0, rows, sc, hs);
+    __syncthreads();
+    const unsigned blocks = blocks_of(rows);
+    for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES) {
+      f32x4 acc[SUB][4];
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
       const TA* brow[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         brow[t] = b + min(base + 16 * (i >> 2) + 4 * t + (i & 3), N - 1) * R;
-      for (int j0 = 0; j0 < R; j0 += 16) {
-        const int j = j0 + 4 * g;
-        const f32x4 h = *reinterpret_cast<const f32x4*>(&hs[i][j]);
-        float w[4][4];
+      for (int j0 = 0; j0 < R; j0 += 32) {
+        Parts<parts_of<TA>> w[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (j < R) {
-            load_f32<4>(brow[t] + j, w[t]);
-          } else {
+        for (int t = 0; t < 4; ++t) w[t] = load_parts<true>(brow[t], j0 + 8 * g, R, true);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[t][e] = 0.f;
-          }
+        for (int s = 0; s < SUB; ++s) {
+          if (!((blocks >> s) & 1u)) continue;
+          const Parts<NP> h = rank_parts<NP>(hs, ld, 16 * s + i, j0 + 8 * g);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts(w[t], h, acc[s][t]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[t] = mfma_f32(w[t][e], h[e], acc[t]);
       }
-      if ((rows >> i) & 1u) write(base, i, acc);
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+        if ((rows >> (16 * s + i)) & 1u) write(base, 16 * s + i, acc[s]);
     }
   });
   // rows without an adapter: y = r
   if (blockIdx.y == 0 && R_ != Y) {
-    const unsigned rows = rows_without(ids, m0, M, adapters);
+    const uint64_t rows = rows_without(ids, m0, M, adapters);
     if (rows != 0u) {
       const f32x4 zero[4] = {};
       for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES)
-        if ((rows >> i) & 1u) write(base, i, zero);
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+          if ((rows >> (16 * s + i)) & 1u) write(base, 16 * s + i, zero);
     }
   }
 }
 
-// dx[m, k] = r[m, k] + sum_j hs[m][j] A_a[j, k], 64 columns per wave at a
-// time: MFMA column i of tile t is k = base + 4 i + t, so a lane's loads and
-// stores are four consecutive elements and a row's 256.
+// dx[m, k] = r[m, k] + sum_j G[m][j] A_a[j, k], 64 columns per wave at a
+// time: MFMA column i of block t is k = base + 4 i + t, so a lane's loads and
+// stores are four consecutive elements and a row's 64.
 template <typename T, typename TA, int WAVES>
-__device__ __forceinline__ void dx_body(const float* __restrict__ PG, const TA* __restrict__ A,
-                                        const float* __restrict__ scale,
+__device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* __restrict__ A,
                                         const int32_t* __restrict__ ids, const T* R_, T* DX,
-                                        int64_t M, int64_t K, int R, int adapters, int splits,
-                                        int64_t tile, int64_t k0, int64_t k1, float (*hs)[HS_LD]) {
+                                        int64_t M, int64_t K, int R, int adapters, int64_t tile,
+                                        int64_t k0, int64_t k1, int mine, int of, uint16_t* hs) {
+  constexpr int NP = rank_np<T>;
+  const int ld = rank_ld(R);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int64_t m0 = tile * LT;
-  auto write = [&](unsigned rows, int64_t base, const f32x4 (&acc)[4]) {
+  // rows 4 g .. 4 g + 3 of block s, four columns each
+  auto write = [&](uint64_t rows, int s, int64_t base, const f32x4 (&acc)[4]) {
     const int64_t k = base + 4 * i;
     if (k >= k1) return;  // K % 32 == 0: four columns are in or out together
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int row = 4 * g + v;
+      const int row = 16 * s + 4 * g + v;
       if (!((rows >> row) & 1u)) continue;
       const int64_t at = (m0 + row) * K + k;
       float o[4] = {acc[0][v], acc[1][v], acc[2][v], acc[3][v]};
@@ -328,49 +573,67 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ PG, const TA* 
       store_f32<4>(DX + at, o);
     }
   };
-  for_groups(ids, m0, M, adapters, 0, 1, [&](unsigned rows, int a) {
+  for_groups(ids, m0, M, adapters, mine, of, [&](uint64_t rows, int a) {
     __syncthreads();
-    load_rank(PG, splits, M, R, m0, rows, scale ? scale[a] : 1.f, hs);
+    load_rank<NP>(G, 1, M, R, m0, rows, 1.f, hs);
     __syncthreads();
     const TA* ad = A + static_cast<int64_t>(a) * R * K;
+    const unsigned blocks = blocks_of(rows);
     for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES) {
-      f32x4 acc[4];
+      f32x4 acc[SUB][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
       const int64_t k = min(base + 4 * i, K - 4);
-      for (int j0 = 0; j0 < R; j0 += 8) {  // R % 8 == 0
-        float w[2][4], h[2];
+      for (int j0 = 0; j0 < R; j0 += 32) {
+        // rows j0 + 8 g .. + 7 of A, four columns each, turned into the
+        // operands of the four columns
+        const int j = j0 + 8 * g;
+        float v[8][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          load_f32<4>(ad + static_cast<int64_t>(j0 + 4 * e + g) * K + k, w[e]);
-          h[e] = hs[i][j0 + 4 * e + g];
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[e][t] = 0.f;
+          if (j < R) load_f32<4>(ad + static_cast<int64_t>(j + e) * K + k, v[e]);  // R % 8 == 0
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int t = 0; t < 4; ++t) {
+          const float col[8] = {v[0][t], v[1][t], v[2][t], v[3][t], v[4][t], v[5][t], v[6][t], v[7][t]};
+          const Parts<parts_of<TA>> w = split8<parts_of<TA>>(col);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) acc[t] = mfma_f32(h[e], w[e][t], acc[t]);
+          for (int s = 0; s < SUB; ++s) {
+            if (!((blocks >> s) & 1u)) continue;
+            acc[s][t] = mfma_parts(rank_parts<NP>(hs, ld, 16 * s + i, j), w, acc[s][t]);
+          }
+        }
       }
-      write(rows, base, acc);
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+        if ((blocks >> s) & 1u) write(rows, s, base, acc[s]);
     }
   });
-  if (R_ != DX) {
-    const unsigned rows = rows_without(ids, m0, M, adapters);
+  if (mine == 0 && R_ != DX) {
+    const uint64_t rows = rows_without(ids, m0, M, adapters);
     if (rows != 0u) {
       const f32x4 zero[4] = {};
-      for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES) write(rows, base, zero);
+      for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES)
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) write(rows, s, base, zero);
     }
   }
 }
 
-// Sum over the rows m of adapter a of l[m][j] Z[m, c], l the scaled rank
+// Sum over the rows m of adapter a of L[m][j] Z[m, c], L the scaled rank
 // vectors: 64 columns c per workgroup, the rows split over its waves.  OT
 // false: out[j][c] (dA), true: out[c][j] (dB).  Rows of other adapters are
 // read as zeros on both sides, so nothing of theirs (infinities, NaN) enters.
 template <typename T, bool OT, int RT, int WAVES, bool VEC>
-__device__ __forceinline__ void outer_body(const float* __restrict__ P, const T* __restrict__ Z,
-                                           float scale, const int32_t* __restrict__ ids,
-                                           float* __restrict__ out, int64_t M, int64_t C, int R,
-                                           int a, int splits, int64_t c0, f32x4 (*red)[4][64]) {
+__device__ __forceinline__ void outer_body(const float* __restrict__ L, const T* __restrict__ Z,
+                                           const int32_t* __restrict__ ids, float* __restrict__ out,
+                                           const uint16_t* __restrict__ LT3, int64_t MP, int64_t M,
+                                           int64_t C, int R, int a, int64_t c0,
+                                           f32x4 (*red)[4][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   f32x4 acc[RT][4];
@@ -382,47 +645,86 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ P, const T*
   for (int64_t r0 = 64 * wave; r0 < M; r0 += 64 * WAVES) {
     const int64_t mine = r0 + lane;
     const uint64_t match = __ballot(mine < M && ids[min(mine, M - 1)] == a);
+    if constexpr (sizeof(T) == 2) {
+      // 32 rows at a time: lane (i, g) has rows 8 g .. 8 g + 7
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {  // 16 rows at a time
-      const unsigned rows = static_cast<unsigned>(match >> (16 * q)) & 0xFFFFu;
-      if (rows == 0u) continue;
-      float l[4][RT], z[4][4];
+      for (int q = 0; q < 2; ++q) {
+        if ((static_cast<uint32_t>(match >> (32 * q))) == 0u) continue;
+        const unsigned ok = static_cast<unsigned>(match >> (32 * q + 8 * g)) & 0xFFu;
+        const int64_t m = r0 + 32 * q + 8 * g;
+        float z[8][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bool ok = (rows >> (4 * s + g)) & 1u;
-        const int64_t m = min(r0 + 16 * q + 4 * s + g, M - 1);
-        const T* zr = Z + m * C;
-        if constexpr (VEC) {
-          if (ok && c < C) {
-            load_f32<4>(zr + c, z[s]);
+        for (int e = 0; e < 8; ++e) {
+          const T* zr = Z + min(m + e, M - 1) * C;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) z[e][u] = 0.f;
+          if constexpr (VEC) {
+            if (((ok >> e) & 1u) && c < C) load_f32<4>(zr + c, z[e]);
           } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) z[s][u] = 0.f;
+            for (int u = 0; u < 4; ++u)
+              if (((ok >> e) & 1u) && c + u < C) z[e][u] = to_f32(zr[c + u]);
           }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) z[s][u] = ok && c + u < C ? to_f32(zr[c + u]) : 0.f;
         }
+        u32x4 keep;  // both halves of a dword: two rows
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          keep[e] = ((ok >> (2 * e)) & 1u ? 0xFFFFu : 0u) | ((ok >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+        Parts<3> l[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const int j = 16 * t + i;
-          float v = 0.f;
-          if (ok && j < R) {
-            for (int p = 0; p < splits; ++p) v += P[(static_cast<int64_t>(p) * M + m) * R + j];
-            v *= scale;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (j < R && ok)  // MP is M rounded up to 32: eight rows are there where one is
+              v = *reinterpret_cast<const u32x4*>(LT3 + (static_cast<int64_t>(p) * R + j) * MP + m);
+            l[t].p[p] = __builtin_bit_cast(bf16x8, v & keep);
           }
-          l[s][t] = v;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float col[8] = {z[0][u], z[1][u], z[2][u], z[3][u], z[4][u], z[5][u], z[6][u], z[7][u]};
+          const Parts<parts_of<T>> w = split8<parts_of<T>>(col);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[t][u] = mfma_parts(l[t], w, acc[t][u]);
         }
       }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // 16 rows at a time
+        const unsigned rows = static_cast<unsigned>(match >> (16 * q)) & 0xFFFFu;
+        if (rows == 0u) continue;
+        float l[4][RT], z[4][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
+          const bool ok = (rows >> (4 * s + g)) & 1u;
+          const int64_t m = min(r0 + 16 * q + 4 * s + g, M - 1);
+          const T* zr = Z + m * C;
+          if constexpr (VEC) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+            for (int u = 0; u < 4; ++u) z[s][u] = 0.f;
+            if (ok && c < C) load_f32<4>(zr + c, z[s]);
+          } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) acc[t][u] = mfma_f32(l[s][t], z[s][u], acc[t][u]);
+            for (int u = 0; u < 4; ++u) z[s][u] = ok && c + u < C ? to_f32(zr[c + u]) : 0.f;
+          }
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const int j = 16 * t + i;
+            l[s][t] = ok && j < R ? L[m * R + j] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[t][u] = mfma_f32(l[s][t], z[s][u], acc[t][u]);
+      }
     }
   }
-  // the waves' sums, added in wave order; then lane (i, g) of tile (t, u)
+  // the waves' sums, added in wave order; then lane (i, g) of block (t, u)
   // holds j = 16 t + 4 g + v, c = c0 + 4 i + u
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
@@ -451,39 +753,40 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ P, const T*
   }
 }
 
-// Second launch of the backward pass: workgroups [0, dxblocks) dx, the next
+// Last launch of the backward pass: workgroups [0, dxblocks) dx, the next
 // adapters * achunks dA, the rest dB.
 constexpr int G_WAVES = 8;
 template <typename T, typename TA, int RT, bool VEC>
 __global__ __launch_bounds__(64 * G_WAVES) void lora_grad_kernel(
-    const float* __restrict__ PH, const float* __restrict__ PG, const T* __restrict__ X,
-    const T* __restrict__ DY, const TA* __restrict__ A, const float* __restrict__ scale,
-    const int32_t* __restrict__ ids, const T* R_, T* DX, float* __restrict__ DA,
-    float* __restrict__ DB, int64_t M, int64_t N, int64_t K, int R, int adapters, int hsplits,
-    int gsplits, int chunks, int64_t chunk, unsigned dxblocks, unsigned ablocks, int achunks,
-    int bchunks) {
-  __shared__ f32x4 red[G_WAVES][4][64];
+    const float* __restrict__ H, const float* __restrict__ G, const uint16_t* __restrict__ HT,
+    const uint16_t* __restrict__ GT, int64_t MP, const T* __restrict__ X,
+    const T* __restrict__ DY, const TA* __restrict__ A, const int32_t* __restrict__ ids,
+    const T* R_, T* DX, float* __restrict__ DA, float* __restrict__ DB, int64_t M, int64_t N,
+    int64_t K, int R, int adapters, int chunks, int64_t chunk, int gy, unsigned dxblocks,
+    unsigned ablocks, int achunks, int bchunks) {
+  __shared__ __attribute__((aligned(16))) union {
+    f32x4 red[G_WAVES][4][64];
+    uint16_t hs[rank_lds<rank_np<T>>(16 * RT) / 2];
+  } sh;
   const unsigned bid = blockIdx.x;
   if (bid < dxblocks) {
-    float(*hs)[HS_LD] = reinterpret_cast<float(*)[HS_LD]>(&red[0][0][0]);
-    const int64_t tile = bid / chunks;
-    const int64_t k0 = (bid - tile * chunks) * chunk;
-    dx_body<T, TA, G_WAVES>(PG, A, scale, ids, R_, DX, M, K, R, adapters, gsplits, tile, k0,
-                            min(K, k0 + chunk), hs);
+    const unsigned b = bid / gy;
+    const int64_t tile = b / chunks;
+    const int64_t k0 = (b - tile * chunks) * chunk;
+    dx_body<T, TA, G_WAVES>(G, A, ids, R_, DX, M, K, R, adapters, tile, k0, min(K, k0 + chunk),
+                            bid % gy, gy, sh.hs);
   } else if (bid < dxblocks + ablocks) {
     const unsigned b = bid - dxblocks;
     const int a = static_cast<int>(b / achunks);
     const int64_t c0 = static_cast<int64_t>(b - static_cast<unsigned>(a) * achunks) * 64;
-    outer_body<T, false, RT, G_WAVES, true>(PG, X, scale ? scale[a] : 1.f, ids,
-                                            DA + static_cast<int64_t>(a) * R * K, M, K, R, a,
-                                            gsplits, c0, red);
+    outer_body<T, false, RT, G_WAVES, true>(G, X, ids, DA + static_cast<int64_t>(a) * R * K, GT, MP,
+                                            M, K, R, a, c0, sh.red);
   } else {
     const unsigned b = bid - dxblocks - ablocks;
     const int a = static_cast<int>(b / bchunks);
     const int64_t c0 = static_cast<int64_t>(b - static_cast<unsigned>(a) * bchunks) * 64;
-    outer_body<T, true, RT, G_WAVES, VEC>(PH, DY, scale ? scale[a] : 1.f, ids,
-                                          DB + static_cast<int64_t>(a) * N * R, M, N, R, a, hsplits,
-                                          c0, red);
+    outer_body<T, true, RT, G_WAVES, VEC>(H, DY, ids, DB + static_cast<int64_t>(a) * N * R, HT, MP, M,
+                                          N, R, a, c0, sh.red);
   }
 }
 
@@ -498,7 +801,7 @@ Split down_split(int64_t M, int64_t C, int cus) {
   constexpr int64_t unit = DOWN_WAVES * DOWN_STEP;
   const int64_t units = (C + unit - 1) / unit;
   int64_t n = std::min<int64_t>(units, std::max<int64_t>(1, 2 * cus / tiles));
-  n = std::min<int64_t>(n, 16);
+  n = std::min<int64_t>(n, 24);
   const int64_t span = (units + n - 1) / n * unit;
   return {static_cast<int>((C + span - 1) / span), span};
 }
@@ -506,30 +809,54 @@ Split down_split(int64_t M, int64_t C, int cus) {
 // Workgroups a tile's adapter groups are dealt to: one per possible group
 // for a decode batch, two for longer inputs (a tile of a prompt holds one
 // request, or the seam of two).
-unsigned group_blocks(int64_t M) { return M <= 256 ? static_cast<unsigned>(std::min<int64_t>(M, LT)) : 2u; }
+unsigned group_blocks(int64_t M, int64_t adapters) {
+  return static_cast<unsigned>(std::min<int64_t>({M, adapters, M <= 256 ? LT : 2}));
+}
+
+// Whether the slices of M rows are summed by a launch of their own.
+bool sum_first(int64_t M, int splits) { return M > 256 && splits > 1; }
 
 template <typename T, typename TA, int RT>
 hipError_t lora_rt(const LoraArgs& p, int cus) {
   const int64_t tiles = (p.M + LT - 1) / LT;
   const Split sp = down_split(p.M, p.K, cus);
   float* P = static_cast<float*>(p.ws);
-  const unsigned gy = group_blocks(p.M);
+  const unsigned gy = group_blocks(p.M, p.adapters);
   hipLaunchKernelGGL((lora_down_kernel<T, TA, RT>), dim3(static_cast<unsigned>(tiles * sp.n), gy),
                      dim3(64 * DOWN_WAVES), 0, p.stream, static_cast<const T*>(p.x),
                      static_cast<const TA*>(p.a), p.ids, P, p.M, p.K, static_cast<int>(p.R),
                      static_cast<int>(p.adapters), sp.n, sp.span);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // a prompt's many workgroups read summed rank vectors; a decode batch adds
+  // the slices itself and saves the launch
+  const float* H = P;
+  const float* scale = p.scale;
+  int slices = sp.n;
+  if (sum_first(p.M, sp.n)) {
+    const int64_t MR = p.M * p.R;
+    float* sum = P + sp.n * MR;
+    hipLaunchKernelGGL(lora_sum_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((MR + 255) / 256, 4096))),
+                       dim3(256), 0, p.stream, P, nullptr, p.scale, p.ids, sum, nullptr, nullptr,
+                       nullptr, p.M, static_cast<int>(p.R), static_cast<int>(p.adapters), sp.n, 0, 0);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    H = sum;
+    scale = nullptr;
+    slices = 1;
+  }
   constexpr int WAVES = 4;
   const int64_t unit = 64 * WAVES, units = (p.N + unit - 1) / unit;
-  const int64_t want = std::max<int64_t>(1, 4 * cus / tiles);
-  const int64_t per = std::max<int64_t>(1, units / want);
+  // all workgroups resident at once (four per CU), so that each pays for its
+  // rank vectors once
+  const int64_t want = std::max<int64_t>(1, 4 * cus / (tiles * (p.M <= 256 ? gy : 1)));
+  const int64_t per = (units + want - 1) / want;
   const int chunks = static_cast<int>((units + per - 1) / per);
   hipLaunchKernelGGL((lora_up_kernel<T, TA, WAVES>),
-                     dim3(static_cast<unsigned>(tiles * chunks), gy), dim3(64 * WAVES), 0, p.stream,
-                     P, static_cast<const TA*>(p.b), p.scale, p.ids, static_cast<const T*>(p.r),
+                     dim3(static_cast<unsigned>(tiles * chunks), gy), dim3(64 * WAVES),
+                     rank_lds<rank_np<T>>(p.R), p.stream, H, static_cast<const TA*>(p.b), scale, p.ids, static_cast<const T*>(p.r),
                      static_cast<T*>(p.y), p.M, p.N, static_cast<int>(p.R),
-                     static_cast<int>(p.adapters), sp.n, chunks, per * unit);
+                     static_cast<int>(p.adapters), slices, chunks, per * unit);
   return hipGetLastError();
 }
 
@@ -537,31 +864,42 @@ template <typename T, typename TA, int RT, bool VEC>
 hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
   const int64_t tiles = (p.M + LT - 1) / LT;
   const Split sh = down_split(p.M, p.K, cus), sg = down_split(p.M, p.N, cus);
-  float* PH = static_cast<float*>(p.ws);
-  float* PG = PH + static_cast<int64_t>(sh.n) * p.M * p.R;
-  const unsigned hb = p.db ? static_cast<unsigned>(tiles * sh.n) : 0u;
-  const unsigned gb = p.y || p.da ? static_cast<unsigned>(tiles * sg.n) : 0u;
-  hipLaunchKernelGGL((lora_down2_kernel<T, TA, RT, VEC>), dim3(hb + gb, group_blocks(p.M)),
-                     dim3(64 * DOWN_WAVES), 0, p.stream, static_cast<const T*>(p.x),
-                     static_cast<const T*>(p.dy), static_cast<const TA*>(p.a),
-                     static_cast<const TA*>(p.b), p.ids, PH, PG, p.M, p.N, p.K,
-                     static_cast<int>(p.R), static_cast<int>(p.adapters), sh.n, sh.span, sg.n,
-                     sg.span, hb);
+  const int64_t MR = p.M * p.R;
+  float* H = static_cast<float*>(p.ws);
+  float* G = H + MR;
+  float* PH = G + MR;
+  float* PG = PH + sh.n * MR;
+  const int64_t MP = (p.M + 31) & ~int64_t(31);
+  uint16_t* HT = sizeof(T) == 2 ? reinterpret_cast<uint16_t*>(PG + sg.n * MR) : nullptr;
+  uint16_t* GT = HT ? HT + 3 * MP * p.R : nullptr;
+  const bool need_h = p.db != nullptr, need_g = p.y || p.da;
+  const unsigned hb = need_h ? static_cast<unsigned>(tiles * sh.n) : 0u;
+  const unsigned gb = need_g ? static_cast<unsigned>(tiles * sg.n) : 0u;
+  const unsigned gy = group_blocks(p.M, p.adapters);
+  const int R = static_cast<int>(p.R), adapters = static_cast<int>(p.adapters);
+  hipLaunchKernelGGL((lora_down2_kernel<T, TA, RT, VEC>), dim3(hb + gb, gy), dim3(64 * DOWN_WAVES),
+                     0, p.stream, static_cast<const T*>(p.x), static_cast<const T*>(p.dy),
+                     static_cast<const TA*>(p.a), static_cast<const TA*>(p.b), p.ids, PH, PG, p.M,
+                     p.N, p.K, R, adapters, sh.n, sh.span, sg.n, sg.span, hb);
   hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(lora_sum_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((MR + 255) / 256, 4096))),
+                     dim3(256), 0, p.stream, PH, PG, p.scale, p.ids, H, G, HT, GT, p.M, R, adapters,
+                     need_h ? sh.n : 0, need_g ? sg.n : 0, MP);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t unit = 64 * G_WAVES, units = (p.K + unit - 1) / unit;
   const int64_t per = std::max<int64_t>(1, units / std::max<int64_t>(1, 2 * cus / tiles));
   const int chunks = static_cast<int>((units + per - 1) / per);
   const int achunks = static_cast<int>((p.K + 63) / 64), bchunks = static_cast<int>((p.N + 63) / 64);
-  const unsigned dxb = p.y ? static_cast<unsigned>(tiles * chunks) : 0u;
+  const unsigned dxb = p.y ? static_cast<unsigned>(tiles * chunks * gy) : 0u;
   const unsigned ab = p.da ? static_cast<unsigned>(p.adapters * achunks) : 0u;
   const unsigned bb = p.db ? static_cast<unsigned>(p.adapters * bchunks) : 0u;
   hipLaunchKernelGGL((lora_grad_kernel<T, TA, RT, VEC>), dim3(dxb + ab + bb), dim3(64 * G_WAVES), 0,
-                     p.stream, PH, PG, static_cast<const T*>(p.x), static_cast<const T*>(p.dy),
-                     static_cast<const TA*>(p.a), p.scale, p.ids, static_cast<const T*>(p.r),
-                     static_cast<T*>(p.y), p.da, p.db, p.M, p.N, p.K, static_cast<int>(p.R),
-                     static_cast<int>(p.adapters), sh.n, sg.n, chunks, per * unit, dxb, ab, achunks,
-                     bchunks);
+                     p.stream, H, G, HT, GT, MP, static_cast<const T*>(p.x), static_cast<const T*>(p.dy),
+                     static_cast<const TA*>(p.a), p.ids, static_cast<const T*>(p.r),
+                     static_cast<T*>(p.y), p.da, p.db, p.M, p.N, p.K, R, adapters, chunks,
+                     per * unit, static_cast<int>(gy), dxb, ab, achunks, bchunks);
   return hipGetLastError();
 }
 
@@ -583,12 +921,15 @@ hipError_t lora_types(const LoraArgs& p, int cus) {
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int cus) {
-  return static_cast<size_t>(down_split(M, K, cus).n) * M * R * sizeof(float);
+  const int n = down_split(M, K, cus).n;
+  return static_cast<size_t>(n + (sum_first(M, n) ? 1 : 0)) * M * R * sizeof(float);
 }
 
 size_t lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int cus) {
-  return static_cast<size_t>(down_split(M, K, cus).n + down_split(M, N, cus).n) * M * R *
-         sizeof(float);
+  // slices, sums, and the sums' transposed parts (16-bit activations)
+  return static_cast<size_t>(2 + down_split(M, K, cus).n + down_split(M, N, cus).n) * M * R *
+             sizeof(float) +
+         static_cast<size_t>(2 * 3) * ((M + 31) & ~int64_t(31)) * R * sizeof(uint16_t);
 }
 
 bool lora_types_ok(int type, int atype) {
