@@ -24,6 +24,7 @@ blocks: binary16 scale + 16 bytes of nibbles, as stored in GGUF).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -414,29 +415,52 @@ def _addr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _matrix(t: torch.Tensor, name: str, shape, dtype=None) -> None:
-    """A contiguous tensor of `shape` with `dtype` (any activation type if None)."""
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    if (t.dtype != dtype) if dtype is not None else (t.dtype not in _TYPES):
-        raise ValueError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+def _matrix(t: torch.Tensor, name: str, shape, dtype) -> None:
+    """A contiguous tensor of `shape` and `dtype`."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)}")
 
 
-def _same_gpu(*ts) -> None:
-    """Every tensor on the current GPU (the library launches on the current device)."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t in ts:
-        if t is not None and not (t.is_cuda and t.get_device() == cur):
+def _activations(t: torch.Tensor, name: str) -> int:
+    """The type code of a contiguous activation matrix."""
+    code = _TYPES.get(t.dtype)
+    if code is None or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous matrix of float32, float16 or bfloat16")
+    return code
+
+
+def _gpu(first, *rest) -> int:
+    """The GPU all tensors live on, which has to be the current one (the library
+    launches on the current device)."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must live on the current GPU")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must live on the current GPU")
+    return dev
 
 
-def _scratch(workspace, nbytes: int, device):
-    """The caller's uint8 workspace, or one of `nbytes` from the current stream's pool."""
-    if workspace is None or workspace is True:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(query: str, dev: int, *args) -> int:
+    """A workspace size (it depends on the sizes and the device's CUs alone)."""
+    return int(getattr(lib(), query)(*args))
+
+
+def _scratch(workspace, query: str, dev: int, *args):
+    """The caller's uint8 workspace, or one from the current stream's pool."""
+    if workspace is None:
+        return torch.empty(_scratch_bytes(query, dev, *args), dtype=torch.uint8,
+                           device=torch.device("cuda", dev))
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same GPU")
     return workspace
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream's handle."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def matmul_dx(w_q4: torch.Tensor, dy: torch.Tensor, out: torch.Tensor | None = None,
@@ -444,21 +468,22 @@ def matmul_dx(w_q4: torch.Tensor, dy: torch.Tensor, out: torch.Tensor | None = N
     """dX = dY deq(W), the gradient of ``matmul`` with respect to x: dy is [M, N] of float32,
     float16 or bfloat16, the result [M, K] of its type.  Without ``workspace`` one is
     allocated (several times the decoded weights' size for float32)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return matmul_dx(w_q4, dy, out, workspace)
     n, k = q4_shape(w_q4)
-    if dy.dim() != 2:
+    t = _activations(dy, "dy")
+    m, n2 = dy.shape
+    if n2 != n:
         raise ValueError(f"dy must be [M, {n}]")
-    m = dy.shape[0]
-    _matrix(dy, "dy", (m, n))
     if out is not None:
         _matrix(out, "out", (m, k), dy.dtype)
-    _same_gpu(w_q4, dy, out, workspace if workspace is not True else None)
-    t = _TYPES[dy.dtype]
-    with _on(stream):
-        if out is None:
-            out = torch.empty((m, k), dtype=dy.dtype, device=dy.device)
-        ws = _scratch(workspace, lib().q4_matmul_dx_workspace_bytes(t, m, n, k), dy.device)
-        _check(lib().q4_matmul_dx(_addr(w_q4), _addr(dy), _addr(out), t, m, n, k, _addr(ws),
-                                  ws.numel(), _stream(stream)), "q4_matmul_dx")
+    dev = _gpu(w_q4, dy, out)
+    if out is None:
+        out = torch.empty((m, k), dtype=dy.dtype, device=dy.device)
+    ws = _scratch(workspace, "q4_matmul_dx_workspace_bytes", dev, t, m, n, k)
+    _check(lib().q4_matmul_dx(w_q4.data_ptr(), dy.data_ptr(), out.data_ptr(), t, m, n, k,
+                              ws.data_ptr(), ws.numel(), _raw_stream(dev)), "q4_matmul_dx")
     return out
 
 
@@ -470,48 +495,53 @@ def lmhead_xent(w_q4: torch.Tensor, x: torch.Tensor, targets: torch.Tensor, grad
     logit (float32), and with ``grad`` (or a ``dx`` to write) the gradient of
     sum(dloss * loss) with respect to x, in x's type; dx is None otherwise.  Rows whose
     target is outside [0, N) have loss 0 and dx 0.  The logits are never kept whole."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lmhead_xent(w_q4, x, targets, grad, dloss, loss, lse, dx, workspace)
     n, k = q4_shape(w_q4)
-    if x.dim() != 2:
+    t = _activations(x, "x")
+    m, k2 = x.shape
+    if k2 != k:
         raise ValueError(f"x must be [M, {k}]")
-    m = x.shape[0]
-    _matrix(x, "x", (m, k))
     _matrix(targets, "targets", (m,), torch.int32)
-    for t, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
-        if t is not None:
-            _matrix(t, name, (m,), torch.float32)
+    for v, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
+        if v is not None:
+            _matrix(v, name, (m,), torch.float32)
     if dx is not None:
         _matrix(dx, "dx", (m, k), x.dtype)
         grad = True
-    _same_gpu(w_q4, x, targets, dloss, loss, lse, dx, workspace if workspace is not True else None)
-    t = _TYPES[x.dtype]
-    with _on(stream):
-        if loss is None:
-            loss = torch.empty(m, dtype=torch.float32, device=x.device)
-        if lse is None:
-            lse = torch.empty(m, dtype=torch.float32, device=x.device)
-        if grad and dx is None:
-            dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
-        ws = _scratch(workspace, lib().q4_lmhead_xent_workspace_bytes(t, int(grad), m, n, k), x.device)
-        _check(lib().q4_lmhead_xent(_addr(w_q4), _addr(x), _addr(targets), _addr(dloss),
-                                    _addr(loss), _addr(lse), _addr(dx), t, m, n, k, _addr(ws),
-                                    ws.numel(), _stream(stream)), "q4_lmhead_xent")
+    dev = _gpu(w_q4, x, targets, dloss, loss, lse, dx)
+    if loss is None:
+        loss = torch.empty(m, dtype=torch.float32, device=x.device)
+    if lse is None:
+        lse = torch.empty(m, dtype=torch.float32, device=x.device)
+    if grad and dx is None:
+        dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+    ws = _scratch(workspace, "q4_lmhead_xent_workspace_bytes", dev, t, int(bool(grad)), m, n, k)
+    _check(lib().q4_lmhead_xent(w_q4.data_ptr(), x.data_ptr(), targets.data_ptr(), _addr(dloss),
+                                loss.data_ptr(), lse.data_ptr(), _addr(dx), t, m, n, k,
+                                ws.data_ptr(), ws.numel(), _raw_stream(dev)), "q4_lmhead_xent")
     return loss, lse, dx
 
 
 def _adapters(x, a, b, ids, scale):
-    """(M, N, K, R, adapters) of a low-rank adapter call."""
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
-        raise ValueError("x must be [M, K], a [adapters, R, K] and b [adapters, N, R]")
+    """(type code, adapters' type code, M, N, K, R, adapters) of a low-rank adapter call."""
+    t = _activations(x, "x")
     m, k = x.shape
-    na, r = a.shape[:2]
-    n = b.shape[1]
-    _matrix(x, "x", (m, k))
-    _matrix(a, "a", (na, r, k))
-    _matrix(b, "b", (na, n, r), a.dtype)
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [adapters, R, K] and b [adapters, N, R]")
+    na, rank, ka = a.shape
+    nb, n, rb = b.shape
+    if ka != k or nb != na or rb != rank or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError(f"a and b must be contiguous [adapters, R, {k}] and [adapters, N, R], "
+                         f"got {list(a.shape)} and {list(b.shape)}")
+    ta = _TYPES.get(a.dtype)
+    if ta is None or b.dtype != a.dtype:
+        raise ValueError("a and b must both be float32, float16 or bfloat16")
     _matrix(ids, "ids", (m,), torch.int32)
     if scale is not None:
         _matrix(scale, "scale", (na,), torch.float32)
-    return m, n, k, r, na
+    return t, ta, m, n, k, rank, na
 
 
 def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
@@ -522,19 +552,21 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
     b [adapters, N, R] (x's type, or float32; with a float32 x any of the three), ids int32
     [M]; an id outside [0, adapters) leaves y = r.  r (zeros if None) may be ``out``.
     With ``matmul_residual(w, x, y, out=y)`` after it, y is the adapted projection."""
-    m, n, k, rank, na = _adapters(x, a, b, ids, scale)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lora(x, a, b, ids, scale, r, out, workspace)
+    t, ta, m, n, k, rank, na = _adapters(x, a, b, ids, scale)
     if r is not None:
         _matrix(r, "r", (m, n), x.dtype)
     if out is not None:
         _matrix(out, "out", (m, n), x.dtype)
-    _same_gpu(x, a, b, ids, scale, r, out, workspace if workspace is not True else None)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-        ws = _scratch(workspace, lib().q4_lora_workspace_bytes(m, n, k, rank), x.device)
-        _check(lib().q4_lora(_addr(x), _addr(a), _addr(b), _addr(scale), _addr(ids), _addr(r),
-                             _addr(out), _TYPES[x.dtype], _TYPES[a.dtype], m, n, k, rank, na,
-                             _addr(ws), ws.numel(), _stream(stream)), "q4_lora")
+    dev = _gpu(x, a, b, ids, scale, r, out)
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    ws = _scratch(workspace, "q4_lora_workspace_bytes", dev, m, n, k, rank)
+    _check(lib().q4_lora(x.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), ids.data_ptr(),
+                         _addr(r), out.data_ptr(), t, ta, m, n, k, rank, na, ws.data_ptr(),
+                         ws.numel(), _raw_stream(dev)), "q4_lora")
     return out
 
 
@@ -546,7 +578,10 @@ def lora_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tenso
     dx = r + scale A^T B^T dy row by row (x's type; r zeros if None, or the gradient
     through the projection itself, may be ``dx``); da and db are float32, summed over
     the rows of each adapter, zeros for one without rows."""
-    m, n, k, rank, na = _adapters(x, a, b, ids, scale)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lora_grad(x, dy, a, b, ids, scale, r, dx, da, db, workspace)
+    t, ta, m, n, k, rank, na = _adapters(x, a, b, ids, scale)
     _matrix(dy, "dy", (m, n), x.dtype)
     if r is not None:
         _matrix(r, "r", (m, k), x.dtype)
@@ -556,19 +591,18 @@ def lora_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tenso
         _matrix(da, "da", (na, rank, k), torch.float32)
     if db is not None:
         _matrix(db, "db", (na, n, rank), torch.float32)
-    _same_gpu(x, dy, a, b, ids, scale, r, dx, da, db, workspace if workspace is not True else None)
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
-        if da is None:
-            da = torch.empty((na, rank, k), dtype=torch.float32, device=x.device)
-        if db is None:
-            db = torch.empty((na, n, rank), dtype=torch.float32, device=x.device)
-        ws = _scratch(workspace, lib().q4_lora_grad_workspace_bytes(m, n, k, rank), x.device)
-        _check(lib().q4_lora_grad(_addr(x), _addr(dy), _addr(a), _addr(b), _addr(scale),
-                                  _addr(ids), _addr(r), _addr(dx), _addr(da), _addr(db),
-                                  _TYPES[x.dtype], _TYPES[a.dtype], m, n, k, rank, na, _addr(ws),
-                                  ws.numel(), _stream(stream)), "q4_lora_grad")
+    dev = _gpu(x, dy, a, b, ids, scale, r, dx, da, db)
+    if dx is None:
+        dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+    if da is None:
+        da = torch.empty((na, rank, k), dtype=torch.float32, device=x.device)
+    if db is None:
+        db = torch.empty((na, n, rank), dtype=torch.float32, device=x.device)
+    ws = _scratch(workspace, "q4_lora_grad_workspace_bytes", dev, m, n, k, rank)
+    _check(lib().q4_lora_grad(x.data_ptr(), dy.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale),
+                              ids.data_ptr(), _addr(r), dx.data_ptr(), da.data_ptr(), db.data_ptr(),
+                              t, ta, m, n, k, rank, na, ws.data_ptr(), ws.numel(),
+                              _raw_stream(dev)), "q4_lora_grad")
     return dx, da, db
 
 

@@ -40,7 +40,8 @@ constexpr int LT = 64;          // rows per tile
 constexpr int SUB = LT / 16;    // MFMA row blocks of a tile
 constexpr int DOWN_WAVES = 8;   // waves of a "down" workgroup, each its part of the long axis
 constexpr int DOWN_STEP = 32;   // reduction indices per wave and step
-constexpr int FEW = 4;          // groups of up to this many rows take the vector unit
+constexpr int DECODE_ROWS = 256;  // calls of up to this many rows may be a decode batch
+constexpr int FEW = 8;          // groups of up to this many rows take the vector unit
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -92,20 +93,42 @@ __device__ __forceinline__ f32x4 mfma_parts(const Parts<NA>& a, const Parts<NB>&
   return c;
 }
 
-// The adapter groups of a 64-row tile: calls f(rows, id) for every group that
-// falls to this workgroup, rows a mask of the tile's rows.  Uniform over the
-// workgroup (every wave reads the same ids).
+// The rows of a tile that share an adapter, packed: member u is the tile's
+// row of(u), u < count.
+struct Group {
+  uint64_t rows;
+  int count, packed;  // packed: lane u holds member u's row
+  __device__ __forceinline__ explicit Group(uint64_t mask)
+      : rows(mask), count(__builtin_popcountll(mask)) {
+    // members first, in order, then the others: a permutation of the lanes
+    const int lane = threadIdx.x & 63;
+    const int before = __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
+    const int to = (mask >> lane) & 1u ? before : count + lane - before;
+    packed = __builtin_amdgcn_ds_permute(4 * to, lane);
+  }
+  __device__ __forceinline__ int of(int u) const { return __shfl(packed, u); }
+  __device__ __forceinline__ int blocks() const { return (count + 15) >> 4; }
+};
+
+// The adapter groups of a 64-row tile: calls f(group, id) for every group that
+// falls to this workgroup.  Uniform over the workgroup (every wave reads the
+// same ids).
 template <typename F>
 __device__ __forceinline__ void for_groups(const int32_t* __restrict__ ids, int64_t m0, int64_t M,
                                            int adapters, int mine, int of, F f) {
   const int64_t row = m0 + (threadIdx.x & 63);
   const int id = row < M ? ids[row] : -1;
   uint64_t left = __ballot(id >= 0 && id < adapters);
+  int next = mine;  // the next group of this workgroup's
   for (int n = 0; left != 0u; ++n) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     const uint64_t same = __ballot(id == a);
     left &= ~same;
-    if (n % of == mine) f(same, a);
+    if (n == next) {
+      f(Group(same), a);
+      next += of;
+    }
+    if (next - n > __builtin_popcountll(left)) break;  // there are not that many left
   }
 }
 
@@ -115,14 +138,6 @@ __device__ __forceinline__ uint64_t rows_without(const int32_t* __restrict__ ids
   const int64_t row = m0 + (threadIdx.x & 63);
   const int id = row < M ? ids[row] : 0;
   return __ballot(row < M && (id < 0 || id >= adapters));
-}
-
-// Which 16-row blocks of the tile hold rows of the mask.
-__device__ __forceinline__ unsigned blocks_of(uint64_t rows) {
-  unsigned b = 0;
-#pragma unroll
-  for (int s = 0; s < SUB; ++s) b |= ((rows >> (16 * s)) & 0xFFFFu) != 0u ? 1u << s : 0u;
-  return b;
 }
 
 // Eight consecutive elements c .. c + 7 of a row of C elements (zeros past
@@ -214,7 +229,7 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
   const int i = lane & 15, g = lane >> 4;
   const int64_t m0 = tile * LT;
   const int64_t c0 = split * span + wave * DOWN_STEP, c1 = min(C, (split + 1) * span);
-  for_groups(ids, m0, M, adapters, mine, of, [&](uint64_t rows, int a) {
+  for_groups(ids, m0, M, adapters, mine, of, [&](const Group& group, int a) {
     const TA* f = F + static_cast<int64_t>(a) * R * C;
     // the waves' parts of the 16 x 16 results of blocks s0, s0 + 1, ..., four at
     // a time, added in wave order
@@ -233,45 +248,37 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
           const int j = 16 * (mine % RT) + i;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int row = 16 * (s0 + mine / RT) + 4 * g + v;
-            if (((rows >> row) & 1u) && j < R)
+            const int u = 16 * (s0 + mine / RT) + 4 * g + v;
+            const int row = group.of(u);
+            if (u < group.count && j < R)
               P[(static_cast<int64_t>(split) * M + m0 + row) * R + j] = sum[v];
           }
         }
         __syncthreads();
       }
     };
-    const unsigned blocks = blocks_of(rows);
-    if ((blocks & (blocks - 1)) == 0u) {
-      // rows of one block of 16 (a decode batch)
-      const int s = __builtin_ctz(blocks);
-      const T* const zrow[1] = {Z + min(m0 + 16 * s + i, M - 1) * C};
-      const bool live[1] = {((rows >> (16 * s + i)) & 1u) != 0u};
-      f32x4 acc[1][RT];
+    auto steps = [&](auto ns, int s0) {
+      constexpr int NS = decltype(ns)::value;
+      const T* zrow[NS];
+      bool live[NS];
+      f32x4 acc[NS][RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      down_steps<T, TA, FT, VEC, RT, 1>(zrow, live, f, c0, c1, C, R, i, g, acc);
-      finish(acc, s);
-    } else {
-      // as many blocks at once as the registers hold beside the factor
-      constexpr int NS = RT <= 2 ? SUB : SUB / 2;
-#pragma unroll 1
-      for (int s0 = 0; s0 < SUB; s0 += NS) {
-        if (((blocks >> s0) & ((1u << NS) - 1)) == 0u) continue;
-        const T* zrow[NS];
-        bool live[NS];
-        f32x4 acc[NS][RT];
+      for (int s = 0; s < NS; ++s) {
+        const int u = 16 * (s0 + s) + i;
+        live[s] = u < group.count;
+        zrow[s] = Z + min(m0 + group.of(u), M - 1) * C;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          zrow[s] = Z + min(m0 + 16 * (s0 + s) + i, M - 1) * C;
-          live[s] = ((rows >> (16 * (s0 + s) + i)) & 1u) != 0u;
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        down_steps<T, TA, FT, VEC, RT, NS>(zrow, live, f, c0, c1, C, R, i, g, acc);
-        finish(acc, s0);
+        for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-    }
+      down_steps<T, TA, FT, VEC, RT, NS>(zrow, live, f, c0, c1, C, R, i, g, acc);
+      finish(acc, s0);
+    };
+    // as many blocks at once as the registers hold beside the factor
+    constexpr int NS = RT <= 2 ? SUB : SUB / 2;
+    if (group.count <= 16)
+      steps(std::integral_constant<int, 1>{}, 0);
+    else
+      for (int s0 = 0; s0 < group.blocks(); s0 += NS) steps(std::integral_constant<int, NS>{}, s0);
   });
 }
 
@@ -353,8 +360,8 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(
   }
 }
 
-// Rank vectors of a group as NP bfloat16 parts in LDS, hs[part][row][ld]: scale
-// * (the slices' sum); zero for the tile's other rows and for j in [R, R
+// Rank vectors of a group as NP bfloat16 parts in LDS, hs[part][member][ld]:
+// scale * (the slices' sum); zero past the last member and for j in [R, R
 // rounded up to 32).  ld = that + 8: rows 16-byte aligned, on different banks.
 __device__ __forceinline__ int rank_ld(int R) { return ((R + 31) & ~31) + 8; }
 template <int NP>
@@ -362,14 +369,16 @@ constexpr size_t rank_lds(int64_t R) { return static_cast<size_t>(NP) * LT * (((
 
 template <int NP>
 __device__ __forceinline__ void load_rank(const float* __restrict__ P, int splits, int64_t M, int R,
-                                          int64_t m0, uint64_t rows, float scale, uint16_t* hs) {
+                                          int64_t m0, const Group& group, float scale,
+                                          uint16_t* hs) {
   const int ld = rank_ld(R), o8 = (ld - 8) / 8;  // groups of eight in a row
   for (int e = threadIdx.x; e < LT * o8; e += blockDim.x) {
-    const int row = e / o8, j = 8 * (e - row * o8);
+    const int u8 = e / o8, j = 8 * (e - u8 * o8);  // (whole waves: LT is 64)
+    const int row = group.of(u8);
     float v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] = 0.f;
-    if (((rows >> row) & 1u) && j < R) {
+    if (u8 < group.count && j < R) {
       const float* p = P + (m0 + row) * R + j;
       for (int t = 0; t < splits; ++t) {
         const f32x4 a = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(t) * M * R);
@@ -382,7 +391,7 @@ __device__ __forceinline__ void load_rank(const float* __restrict__ P, int split
     }
     const Parts<NP> q = split8<NP>(v);
 #pragma unroll
-    for (int u = 0; u < NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + row) * ld + j) = q.p[u];
+    for (int u = 0; u < NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + u8) * ld + j) = q.p[u];
   }
 }
 
@@ -407,8 +416,11 @@ constexpr int rank_np = sizeof(T) == 4 ? 3 : 2;
 //    block t is column n = base + 16 (rho / 4) + 4 t + rho % 4, so a lane's
 //    results are 16 consecutive columns of one row; B is read once for the
 //    tile's 64 rows.
-template <typename T, typename TA, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(
+// NS: blocks of 16 rows multiplied at a time.  All four read B once (prompts);
+// one keeps the registers low, for decode batches, whose groups mostly are
+// few rows and whose speed is in how many workgroups are resident.
+template <typename T, typename TA, int WAVES, int NS>
+__global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
     const float* __restrict__ P, const TA* __restrict__ B, const float* __restrict__ scale,
     const int32_t* __restrict__ ids, const T* R_, T* Y, int64_t M, int64_t N, int R, int adapters,
     int splits, int chunks, int64_t chunk) {
@@ -450,82 +462,104 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(
     }
   };
 
-  for_groups(ids, m0, M, adapters, blockIdx.y, gridDim.y, [&](uint64_t rows, int a) {
+  for_groups(ids, m0, M, adapters, blockIdx.y, gridDim.y, [&](const Group& group, int a) {
     __syncthreads();  // the previous group's rank vectors are no longer read
     const TA* b = B + static_cast<int64_t>(a) * N * R;
     const float sc = scale ? scale[a] : 1.f;
-    const int count = __builtin_popcountll(rows);
+    const int count = group.count;
     if (count <= FEW) {
       int at[FEW];
-      uint64_t left = rows;
 #pragma unroll
-      for (int u = 0; u < FEW; ++u) {
-        at[u] = left ? __builtin_ctzll(left) : at[0];
-        left &= left - 1;
-      }
+      for (int u = 0; u < FEW; ++u) at[u] = __builtin_amdgcn_readlane(group.packed, u);
       float* hf = reinterpret_cast<float*>(hs);  // [FEW][R]
       for (int e = threadIdx.x; e < FEW * R; e += 64 * WAVES) {
         const int u = e / R, j = e - u * R;
-        const int row = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
+        const int row = group.of(u);  // (FEW * R is a multiple of 64: whole waves)
         if (u < count) hf[e] = sc * sum_slices(P + (m0 + row) * R + j, splits, M * R);
       }
       __syncthreads();
-      for (int64_t n = n0 + threadIdx.x; n < n1; n += 64 * WAVES) {
-        float acc[FEW] = {0.f, 0.f, 0.f, 0.f}, q[FEW];
+      // COLS columns per thread, so that their rows of B are in flight at once
+      auto columns = [&](auto cnt, auto cols) {
+        constexpr int U = decltype(cnt)::value, COLS = decltype(cols)::value;
+        for (int64_t n = n0 + threadIdx.x; n < n1; n += COLS * 64 * WAVES) {
+          float acc[COLS][U], q[COLS][U];
+          const TA* bn[COLS];
 #pragma unroll
-        for (int u = 0; u < FEW; ++u) q[u] = u < count && R_ ? to_f32(R_[(m0 + at[u]) * N + n]) : 0.f;
-        const TA* brow = b + n * R;
+          for (int c = 0; c < COLS; ++c) {
+            const int64_t nc = n + c * 64 * WAVES;
+            bn[c] = b + (nc < n1 ? nc : n) * R;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              q[c][u] = u < count && R_ && nc < n1 ? to_f32(R_[(m0 + at[u]) * N + nc]) : 0.f;
+              acc[c][u] = 0.f;
+            }
+          }
 #pragma unroll 2
-        for (int j = 0; j < R; j += 8) {
-          float w[8];
-          row8<true>(brow, j, R, true, w);
+          for (int j = 0; j < R; j += 8) {
+            float w[COLS][8];
 #pragma unroll
-          for (int u = 0; u < FEW; ++u) {
-            if (u < count) {
+            for (int c = 0; c < COLS; ++c) row8<true>(bn[c], j, R, true, w[c]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
               const f32x4 h0 = *reinterpret_cast<const f32x4*>(hf + u * R + j);
               const f32x4 h1 = *reinterpret_cast<const f32x4*>(hf + u * R + j + 4);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                acc[u] = __builtin_fmaf(w[e], h0[e], acc[u]);
-                acc[u] = __builtin_fmaf(w[4 + e], h1[e], acc[u]);
-              }
+              for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  acc[c][u] = __builtin_fmaf(w[c][e], h0[e], acc[c][u]);
+                  acc[c][u] = __builtin_fmaf(w[c][4 + e], h1[e], acc[c][u]);
+                }
             }
           }
-        }
 #pragma unroll
-        for (int u = 0; u < FEW; ++u)
-          if (u < count) Y[(m0 + at[u]) * N + n] = from_f32<T>(q[u] + acc[u]);
-      }
+          for (int c = 0; c < COLS; ++c) {
+            const int64_t nc = n + c * 64 * WAVES;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (u < count && nc < n1) Y[(m0 + at[u]) * N + nc] = from_f32<T>(q[c][u] + acc[c][u]);
+          }
+        }
+      };
+      using std::integral_constant;
+      if (count <= 2)
+        columns(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+      else
+        columns(integral_constant<int, FEW>{}, integral_constant<int, 1>{});
       return;
     }
-    load_rank<NP>(P, splits, M, R, m0, rows, sc, hs);
+    load_rank<NP>(P, splits, M, R, m0, group, sc, hs);
     __syncthreads();
-    const unsigned blocks = blocks_of(rows);
     for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES) {
-      f32x4 acc[SUB][4];
-#pragma unroll
-      for (int s = 0; s < SUB; ++s)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
       const TA* brow[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         brow[t] = b + min(base + 16 * (i >> 2) + 4 * t + (i & 3), N - 1) * R;
-      for (int j0 = 0; j0 < R; j0 += 32) {
-        Parts<parts_of<TA>> w[4];
+#pragma unroll 1
+      for (int s0 = 0; s0 < group.blocks(); s0 += NS) {
+        f32x4 acc[NS][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = load_parts<true>(brow[t], j0 + 8 * g, R, true);
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-          if (!((blocks >> s) & 1u)) continue;
-          const Parts<NP> h = rank_parts<NP>(hs, ld, 16 * s + i, j0 + 8 * g);
+          for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j0 = 0; j0 < R; j0 += 32) {
+          Parts<parts_of<TA>> w[4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts(w[t], h, acc[s][t]);
+          for (int t = 0; t < 4; ++t) w[t] = load_parts<true>(brow[t], j0 + 8 * g, R, true);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            if (NS > 1 && s >= group.blocks()) break;
+            const Parts<NP> h = rank_parts<NP>(hs, ld, 16 * (s0 + s) + i, j0 + 8 * g);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts(w[t], h, acc[s][t]);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const int u = 16 * (s0 + s) + i, row = group.of(u);
+          if (u < count) write(base, row, acc[s]);
         }
       }
-#pragma unroll
-      for (int s = 0; s < SUB; ++s)
-        if ((rows >> (16 * s + i)) & 1u) write(base, 16 * s + i, acc[s]);
     }
   });
   // rows without an adapter: y = r
@@ -554,14 +588,13 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int64_t m0 = tile * LT;
-  // rows 4 g .. 4 g + 3 of block s, four columns each
-  auto write = [&](uint64_t rows, int s, int64_t base, const f32x4 (&acc)[4]) {
+  // members 4 g .. 4 g + 3 of block s, four columns each
+  auto write = [&](const Group& group, int s, int64_t base, const f32x4 (&acc)[4]) {
     const int64_t k = base + 4 * i;
-    if (k >= k1) return;  // K % 32 == 0: four columns are in or out together
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int row = 16 * s + 4 * g + v;
-      if (!((rows >> row) & 1u)) continue;
+      const int u = 16 * s + 4 * g + v, row = group.of(u);
+      if (u >= group.count || k >= k1) continue;  // K % 32 == 0: four columns in or out together
       const int64_t at = (m0 + row) * K + k;
       float o[4] = {acc[0][v], acc[1][v], acc[2][v], acc[3][v]};
       if (R_) {
@@ -573,12 +606,12 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
       store_f32<4>(DX + at, o);
     }
   };
-  for_groups(ids, m0, M, adapters, mine, of, [&](uint64_t rows, int a) {
+  for_groups(ids, m0, M, adapters, mine, of, [&](const Group& group, int a) {
     __syncthreads();
-    load_rank<NP>(G, 1, M, R, m0, rows, 1.f, hs);
+    load_rank<NP>(G, 1, M, R, m0, group, 1.f, hs);
     __syncthreads();
     const TA* ad = A + static_cast<int64_t>(a) * R * K;
-    const unsigned blocks = blocks_of(rows);
+    const int blocks = group.blocks();
     for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES) {
       f32x4 acc[SUB][4];
 #pragma unroll
@@ -603,23 +636,23 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
           const Parts<parts_of<TA>> w = split8<parts_of<TA>>(col);
 #pragma unroll
           for (int s = 0; s < SUB; ++s) {
-            if (!((blocks >> s) & 1u)) continue;
+            if (s >= blocks) break;
             acc[s][t] = mfma_parts(rank_parts<NP>(hs, ld, 16 * s + i, j), w, acc[s][t]);
           }
         }
       }
 #pragma unroll
       for (int s = 0; s < SUB; ++s)
-        if ((blocks >> s) & 1u) write(rows, s, base, acc[s]);
+        if (s < blocks) write(group, s, base, acc[s]);
     }
   });
   if (mine == 0 && R_ != DX) {
     const uint64_t rows = rows_without(ids, m0, M, adapters);
     if (rows != 0u) {
+      const Group group(rows);
       const f32x4 zero[4] = {};
       for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES)
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) write(rows, s, base, zero);
+        for (int s = 0; s < group.blocks(); ++s) write(group, s, base, zero);
     }
   }
 }
@@ -790,36 +823,37 @@ __global__ __launch_bounds__(64 * G_WAVES) void lora_grad_kernel(
   }
 }
 
-// Slices of a long axis of C for M rows: enough workgroups to fill the GPU,
-// at least DOWN_WAVES steps each.
+// Workgroups a tile's adapter groups are dealt to: one per possible group
+// for a decode batch, two for longer inputs (a tile of a prompt holds one
+// request, or the seam of two).
+unsigned group_blocks(int64_t M, int64_t adapters) {
+  return static_cast<unsigned>(std::min<int64_t>({M, adapters, M <= DECODE_ROWS ? LT : 2}));
+}
+
+// Slices of a long axis of C for M rows: workgroups to fill the GPU once (a
+// decode batch, whose groups may all be at work) or twice (a prompt, where
+// about half find no group of theirs).
 struct Split {
   int n;
   int64_t span;
 };
-Split down_split(int64_t M, int64_t C, int cus) {
+Split down_split(int64_t M, int64_t C, int64_t adapters, int cus) {
   const int64_t tiles = (M + LT - 1) / LT;
   constexpr int64_t unit = DOWN_WAVES * DOWN_STEP;
   const int64_t units = (C + unit - 1) / unit;
-  int64_t n = std::min<int64_t>(units, std::max<int64_t>(1, 2 * cus / tiles));
+  int64_t n = std::min<int64_t>(units, std::max<int64_t>(1, M <= DECODE_ROWS ? cus / (tiles * group_blocks(M, adapters)) : 2 * cus / tiles));
   n = std::min<int64_t>(n, 24);
   const int64_t span = (units + n - 1) / n * unit;
   return {static_cast<int>((C + span - 1) / span), span};
 }
 
-// Workgroups a tile's adapter groups are dealt to: one per possible group
-// for a decode batch, two for longer inputs (a tile of a prompt holds one
-// request, or the seam of two).
-unsigned group_blocks(int64_t M, int64_t adapters) {
-  return static_cast<unsigned>(std::min<int64_t>({M, adapters, M <= 256 ? LT : 2}));
-}
-
 // Whether the slices of M rows are summed by a launch of their own.
-bool sum_first(int64_t M, int splits) { return M > 256 && splits > 1; }
+bool sum_first(int64_t M, int splits) { return M > DECODE_ROWS && splits > 1; }
 
 template <typename T, typename TA, int RT>
 hipError_t lora_rt(const LoraArgs& p, int cus) {
   const int64_t tiles = (p.M + LT - 1) / LT;
-  const Split sp = down_split(p.M, p.K, cus);
+  const Split sp = down_split(p.M, p.K, p.adapters, cus);
   float* P = static_cast<float*>(p.ws);
   const unsigned gy = group_blocks(p.M, p.adapters);
   hipLaunchKernelGGL((lora_down_kernel<T, TA, RT>), dim3(static_cast<unsigned>(tiles * sp.n), gy),
@@ -849,21 +883,28 @@ hipError_t lora_rt(const LoraArgs& p, int cus) {
   const int64_t unit = 64 * WAVES, units = (p.N + unit - 1) / unit;
   // all workgroups resident at once (four per CU), so that each pays for its
   // rank vectors once
-  const int64_t want = std::max<int64_t>(1, 4 * cus / (tiles * (p.M <= 256 ? gy : 1)));
+  const int64_t want = std::max<int64_t>(1, 4 * cus / (tiles * (p.M <= DECODE_ROWS ? gy : 1)));
   const int64_t per = (units + want - 1) / want;
   const int chunks = static_cast<int>((units + per - 1) / per);
-  hipLaunchKernelGGL((lora_up_kernel<T, TA, WAVES>),
-                     dim3(static_cast<unsigned>(tiles * chunks), gy), dim3(64 * WAVES),
-                     rank_lds<rank_np<T>>(p.R), p.stream, H, static_cast<const TA*>(p.b), scale, p.ids, static_cast<const T*>(p.r),
-                     static_cast<T*>(p.y), p.M, p.N, static_cast<int>(p.R),
-                     static_cast<int>(p.adapters), slices, chunks, per * unit);
+  auto up = [&](auto ns) {
+    hipLaunchKernelGGL((lora_up_kernel<T, TA, WAVES, decltype(ns)::value>),
+                       dim3(static_cast<unsigned>(tiles * chunks), gy), dim3(64 * WAVES),
+                       rank_lds<rank_np<T>>(p.R), p.stream, H, static_cast<const TA*>(p.b), scale,
+                       p.ids, static_cast<const T*>(p.r), static_cast<T*>(p.y), p.M, p.N,
+                       static_cast<int>(p.R), static_cast<int>(p.adapters), slices, chunks,
+                       per * unit);
+  };
+  if (p.M <= DECODE_ROWS)
+    up(std::integral_constant<int, 1>{});
+  else
+    up(std::integral_constant<int, SUB>{});
   return hipGetLastError();
 }
 
 template <typename T, typename TA, int RT, bool VEC>
 hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
   const int64_t tiles = (p.M + LT - 1) / LT;
-  const Split sh = down_split(p.M, p.K, cus), sg = down_split(p.M, p.N, cus);
+  const Split sh = down_split(p.M, p.K, p.adapters, cus), sg = down_split(p.M, p.N, p.adapters, cus);
   const int64_t MR = p.M * p.R;
   float* H = static_cast<float*>(p.ws);
   float* G = H + MR;
@@ -920,14 +961,15 @@ hipError_t lora_types(const LoraArgs& p, int cus) {
 
 }  // namespace
 
+// The size for any number of adapters: one gives the most slices.
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int cus) {
-  const int n = down_split(M, K, cus).n;
+  const int n = down_split(M, K, 1, cus).n;
   return static_cast<size_t>(n + (sum_first(M, n) ? 1 : 0)) * M * R * sizeof(float);
 }
 
 size_t lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int cus) {
   // slices, sums, and the sums' transposed parts (16-bit activations)
-  return static_cast<size_t>(2 + down_split(M, K, cus).n + down_split(M, N, cus).n) * M * R *
+  return static_cast<size_t>(2 + down_split(M, K, 1, cus).n + down_split(M, N, 1, cus).n) * M * R *
              sizeof(float) +
          static_cast<size_t>(2 * 3) * ((M + 31) & ~int64_t(31)) * R * sizeof(uint16_t);
 }
