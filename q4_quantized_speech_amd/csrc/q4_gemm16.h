@@ -81,6 +81,28 @@ struct PlainGemm {
 };
 hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s);
 
+// part[slice][m][k] (alpha as above), or with splits == 1 and part null out[m][k]
+// = inv[m] * the sum rounded once to `type`: sum over n of G[m, n] deq(W)[n, k]
+// for the weight rows [n0, min(N, n0 + 32 CB)), read as Q4_0 (K % 64 == 0:
+// rows start on a dword).
+struct TransposedGemm {
+  const f16x8* g;
+  int pa, pb, type;
+  const uint8_t* w;
+  int64_t n0, N, M, K, CB;
+  int splits;
+  float* part;
+  const float *alpha, *inv;
+  void* out;
+};
+struct TransposedPlan {
+  double us;  // estimate
+  int splits;
+};
+inline int transposed_rt(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus);
+hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s);
+
 // Logits of weight rows n0 .. n0 + cols: l[m][n] = inv[m] sum_b scale[n][b]
 // (A[m, block b] . (q - 8)[n, block b]), float32 over exact products.  With
 // `logits`, [M][ld] floats are written and tmax[m][n / 64 cols] holds the

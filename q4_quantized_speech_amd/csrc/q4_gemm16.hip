@@ -40,68 +40,97 @@ __device__ __forceinline__ float row_scale(float top) {
 // Operand preparation
 // ---------------------------------------------------------------------------
 
-// One wave per row, 16 rows per workgroup.
+// One wave per row, 16 rows per workgroup, gridDim.y parts of the columns.
+// Every workgroup takes the rows' maxima over all columns (its siblings' reads
+// come from the L2), then its columns, 512 at a time.  The fragments are put
+// together in LDS and written whole: a wave's own 16-byte pieces lie 256 bytes
+// apart (12.4 us for 16 x 3072 float32 that way).
 template <typename T, bool NIB, int PARTS, bool VEC>
 __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X,
                                                          f16x8* __restrict__ out,
                                                          float* __restrict__ inv, int64_t M,
-                                                         int64_t C, int64_t CB) {
+                                                         int64_t C, int64_t CB, int64_t bspan) {
+  __shared__ f16x8 tile[2][PARTS][16][64];  // [buffer][part][block][swizzled lane]
   const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + i;
   const bool live = m < M;
   const T* row = X + (live ? m : 0) * C;
-  auto load4 = [&](int64_t c, float (&v)[4]) {
+  auto load4 = [&](int64_t c, float* v) {
     if constexpr (VEC) {
-      if (live && c < C) {
-        load_f32<4>(row + c, v);
-        return;
-      }
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live && c < C) load_f32<4>(row + c, t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = 0.f;
+      for (int e = 0; e < 4; ++e) v[e] = t[e];
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = live && c + e < C ? to_f32(row[c + e]) : 0.f;
     }
   };
+  constexpr int PU = 4;  // groups of eight values in flight
   float top = 0.f;
-  for (int64_t c = 4 * lane; c < C; c += 256) {
-    float v[4];
-    load4(c, v);
+  for (int64_t c = 8 * lane; c < C; c += 512 * PU) {
+    float v[PU][8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[e]));
+    for (int u = 0; u < PU; ++u) {
+      load4(c + 512 * u, v[u]);
+      load4(c + 512 * u + 4, v[u] + 4);
+    }
+#pragma unroll
+    for (int u = 0; u < PU; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[u][e]));
   }
   top = wave_max(top);
   const float s = row_scale(top);
-  if (live && lane == 0) inv[m] = 1.f / s;
+  if (live && lane == 0 && blockIdx.y == 0) inv[m] = 1.f / s;
   const int64_t part = static_cast<int64_t>(gridDim.x) * CB * 64;
-  for (int64_t q = lane; q < CB * 4; q += 64) {  // slot: block q / 4, group q % 4
-    const int64_t blk = q >> 2;
-    const int g = static_cast<int>(q & 3);
-    float a[4], b[4];
-    load4(32 * blk + (NIB ? 4 * g : 8 * g), a);
-    load4(32 * blk + (NIB ? 16 + 4 * g : 8 * g + 4), b);
+  const int64_t b0 = blockIdx.y * bspan, b1 = min(CB, b0 + bspan);
+  const int blk = lane >> 2, g = lane & 3;  // this lane's slot of 16 blocks
+  float v[8];
+  auto load = [&](int64_t b) {
+    const int64_t c = 32 * (b + blk);
+    load4(c + (NIB ? 4 * g : 8 * g), v);
+    load4(c + (NIB ? 16 + 4 * g : 8 * g + 4), v + 4);
+  };
+  load(b0);
+  int cur = 0;
+  for (int64_t b = b0; b < b1; b += 16, cur ^= 1) {
     f16x8 hi, lo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float v = (e < 4 ? a[e & 3] : b[e & 3]) * s;
-      hi[e] = static_cast<_Float16>(v);
-      if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(v - static_cast<float>(hi[e]));
+      const float x = v[e] * s;
+      hi[e] = static_cast<_Float16>(x);
+      if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
     }
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * CB + blk) * 64 + i + 16 * g;
-    out[at] = hi;
-    if constexpr (PARTS == 2) out[part + at] = lo;
+    if (b + 16 < b1) load(b + 16);
+    // lane i + 16 g of a block sits at (i ^ (4 blk + g)) + 16 g: the lanes of a
+    // wave (one i) then hit distinct banks, and so do the readers (one block)
+    const int at = 16 * g + (i ^ (lane & 15));
+    tile[cur][0][blk][at] = hi;
+    if constexpr (PARTS == 2) tile[cur][1][blk][at] = lo;
+    __syncthreads();
+    if (b + i < b1) {  // wave i writes block b + i
+      const int from = (lane & 48) + ((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));
+      const int64_t to = (static_cast<int64_t>(blockIdx.x) * CB + b + i) * 64 + lane;
+      out[to] = tile[cur][0][i][from];
+      if constexpr (PARTS == 2) out[part + to] = tile[cur][1][i][from];
+    }
   }
 }
 
 template <typename T>
 void prep_rows_t(const T* x, Order order, int parts, f16x8* frag, float* inv, int64_t M, int64_t C,
                  hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((M + 15) / 16)), block(1024);
-  const int64_t CB = blocks32(C);
+  const int64_t CB = blocks32(C), tiles = (M + 15) / 16;
+  // about a workgroup per CU, each at least 16 blocks
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((CB + 15) / 16, 256 / tiles));
+  const int64_t bspan = ((CB + want - 1) / want + 15) / 16 * 16;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((CB + bspan - 1) / bspan));
+  const dim3 block(1024);
   const bool vec = C % 4 == 0;
   auto go = [&](auto nib, auto p, auto v) {
     hipLaunchKernelGGL((prep_rows_kernel<T, decltype(nib)::value, decltype(p)::value, decltype(v)::value>),
-                       grid, block, 0, s, x, frag, inv, M, C, CB);
+                       grid, block, 0, s, x, frag, inv, M, C, CB, bspan);
   };
   using std::integral_constant;
   const integral_constant<int, 1> p1;
@@ -502,6 +531,205 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
   }
 }
 
+// ---------------------------------------------------------------------------
+// The transposed product straight from the Q4_0 bytes: out[m, k] = sum_n
+// G[m, n] deq(W)[n, k] for 16 RT rows and 128 columns per workgroup.  Its
+// eight waves take every eighth block of 32 weight rows of the workgroup's
+// range and add their sums at the end.
+//
+// A block's 32 rows x 72 bytes go to the wave's own LDS as they are (DMA of
+// consecutive dwords; loading each lane's codes from memory took 20 loads of
+// four rows a block and 39.9 us instead of 23 at 1500 x 5120 x 1280).  A lane (i, g) takes
+// one dword of codes of block i / 4 of the 128 columns
+// from each of the rows 8 g .. 8 g + 7: eight rows of eight columns, turned
+// in registers into the operands of the columns k = 32 (i / 4) + 4 (i % 4) +
+// (c & 3) + 16 (c >> 2), c < 8, with the rows as the reduction.  A result lane
+// then holds 32 consecutive columns of one row of G.  Weights are decoded
+// once per 64 rows of G; at 64 rows that takes the vector unit about as long
+// as the products take the matrix cores.
+// ---------------------------------------------------------------------------
+constexpr int TW = 8;  // waves
+
+template <int RT, int PA, int PB, typename T>
+__global__ __launch_bounds__(64 * TW) __attribute__((amdgpu_waves_per_eu(2, RT <= 1 ? 4 : 2)))
+void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restrict__ W, int64_t n0,
+                            int64_t N, int64_t M, int64_t K, int64_t CB, int mtiles, int tiles,
+                            int64_t span, float* __restrict__ part, const float* __restrict__ alpha,
+                            const float* __restrict__ inv, T* __restrict__ out) {
+  constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time
+  __shared__ f32x4 red[4][RP * 8][64];
+  // two arrays: reading one does not have to wait for loads into the other.
+  // 18 dwords a row, and one that the last row's pair of reads touches
+  __shared__ uint32_t raw0[TW][32 * 18 + 16], raw1[TW][32 * 18 + 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const unsigned item = xcd_order(blockIdx.x, gridDim.x);
+  const int split = item / tiles, tile = item % tiles;
+  const int mt = tile % mtiles, kt = tile / mtiles;
+  const int64_t rb = K / 32 * BLOCK_BYTES;
+  const int64_t rta = (M + 15) / 16, live = min(CB, (N - n0 + 31) / 32);
+  const int64_t b1 = min(live, (split + 1) * span);
+
+  // this lane's nine dwords of a block: byte offsets from its first row; rows
+  // past the matrix repeat its last one (G is zero there), columns past it
+  // its last dword (their results are dropped)
+  uint32_t off[9];
+  auto offsets = [&](int64_t nb) {
+    const int64_t rows = min<int64_t>(32, N - n0 - nb * 32), most = rb / 4 - 1 - kt * 18;
+#pragma unroll
+    for (int u = 0; u < 9; ++u) {
+      const int e = u * 64 + lane;
+      off[u] = static_cast<uint32_t>(min<int64_t>(e / 18, rows - 1) * rb + min<int64_t>(e % 18, most) * 4);
+    }
+  };
+  offsets(0);
+
+  struct Acts {
+    f16x8 a[RT][PA];
+  };
+  auto load = [&](int64_t nb, uint32_t* raw, Acts& x) {
+    if (n0 + nb * 32 + 32 > N) offsets(nb);  // the last, partial block
+    const uint8_t* base = W + (n0 + nb * 32) * rb + static_cast<int64_t>(kt) * 72;
+#pragma unroll
+    for (int u = 0; u < 9; ++u) to_lds<4>(base + off[u], raw + u * 64);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int p = 0; p < PA; ++p) {
+        const int64_t rt = min(static_cast<int64_t>(mt) * RT + t, rta - 1);
+        x.a[t][p] = G[((p * rta + rt) * CB + nb) * 64 + lane];
+      }
+    issued();
+  };
+
+  f32x4 acc[RT][8];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // block i / 4 starts at byte 18 (i / 4) of a row: its scale in either half of
+  // a dword, its codes from the next half on
+  const int first = 18 * (i >> 2), code = first + 2 + 4 * (i & 3);
+  auto compute = [&](const uint32_t* raw, const Acts& x) {
+    uint32_t q8[8];
+    f16x2 d[4];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const uint32_t* p = raw + (8 * g + r) * 18;
+      const uint32_t* c = p + (code >> 2);
+      q8[r] = __builtin_amdgcn_alignbit(c[1], c[0], 8 * (code & 2));
+      d[r >> 1][r & 1] = reinterpret_cast<const _Float16*>(p)[first >> 1];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t nib[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) nib[r] = (h ? q8[r] >> 4 : q8[r]) & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        // byte b of two rows as binary16 1024 + q, then (q - 8) d, rounded once
+        f16x8 hi, lo;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t pair =
+              __builtin_amdgcn_perm(nib[2 * q + 1], nib[2 * q], 0x0C000C00u | ((4u + b) << 16) | b) |
+              0x64006400u;
+          const f16x2 off8 = {static_cast<_Float16>(-1032.0f), static_cast<_Float16>(-1032.0f)};
+          const f16x2 w = __builtin_bit_cast(f16x2, pair) + off8;
+          const f16x2 wd = w * d[q];
+          hi[2 * q] = wd[0];
+          hi[2 * q + 1] = wd[1];
+          if constexpr (PB == 2) {  // the exact rest
+            const f16x2 rest = __builtin_elementwise_fma(w, d[q], -wd);
+            lo[2 * q] = rest[0];
+            lo[2 * q + 1] = rest[1];
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          f32x4& s = acc[t][4 * h + b];
+          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, x.a[t][0], s, 0, 0, 0);
+          if constexpr (PB == 2) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, x.a[t][0], s, 0, 0, 0);
+          if constexpr (PA == 2) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, x.a[t][1], s, 0, 0, 0);
+        }
+      }
+    }
+  };
+
+  // one block is multiplied while the next one's loads are in flight; the
+  // bytes are the wave's own, so its counter of loads is all there is to wait
+  // for
+  Acts x0, x1;
+  int64_t nb = split * span + wave;
+  if (nb < b1) load(nb, raw0[wave], x0);
+  for (; nb < b1; nb += 2 * TW) {
+    arrived();
+    const bool two = nb + TW < b1;
+    if (two) load(nb + TW, raw1[wave], x1);
+    compute(raw0[wave], x0);
+    if (two) {
+      arrived();
+      if (nb + 2 * TW < b1) load(nb + 2 * TW, raw0[wave], x0);
+      compute(raw1[wave], x1);
+    }
+  }
+
+  // the waves' sums, RP row blocks at a time: 4-7 onto 0-3, then those four;
+  // wave w finishes half (c >> 2) = w & 1 of the pass's row block w >> 1
+  const int h = wave & 1;
+  f32x4 s[4];
+#pragma unroll
+  for (int t0 = 0; t0 < RT; t0 += RP) {
+    if (t0) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < RP * 8; ++e)
+      if (wave >= 4) red[wave - 4][e][lane] = acc[t0 + e / 8][e % 8];
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+      for (int e = 0; e < RP * 8; ++e)
+        red[wave][e][lane] = acc[t0 + e / 8][e % 8] + red[wave][e][lane];
+    }
+    __syncthreads();
+    const int t = wave >> 1;
+    if (t >= t0 && t < t0 + RP) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[c] = red[0][(t - t0) * 8 + 4 * h + c][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) s[c] += red[w][(t - t0) * 8 + 4 * h + c][lane];
+      }
+    }
+  }
+  const int t = wave >> 1;
+  const int64_t m = (static_cast<int64_t>(mt) * RT + t) * 16 + i;
+  const int64_t k = static_cast<int64_t>(kt) * 128 + 32 * g + 16 * h;
+  if (t >= RT || m >= M || k >= K) return;
+  if (part) {
+    f32x4* o = reinterpret_cast<f32x4*>(part + (static_cast<int64_t>(split) * M + m) * K + k);
+    const float al = alpha ? alpha[m] : 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      f32x4 r = {s[0][v], s[1][v], s[2][v], s[3][v]};
+      if (alpha) {
+        const f32x4 q = o[v];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = __builtin_fmaf(al, q[e], r[e]);
+      }
+      o[v] = r;
+    }
+  } else {
+    const float f = inv[m];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float r[4] = {f * s[0][v], f * s[1][v], f * s[2][v], f * s[3][v]};
+      store_f32<4>(out + m * K + k + 4 * v, r);
+    }
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ part, int splits,
                                                    const float* __restrict__ inv,
@@ -511,8 +739,16 @@ __global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ par
        e += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t m = e / quads;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int t = 0; t < splits; ++t)
-      s += *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(t) * M * K + 4 * e);
+    for (int t = 0; t < splits; t += 4) {  // four slices in flight
+      f32x4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        v[u] = t + u < splits
+                   ? *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(t + u) * M * K + 4 * e)
+                   : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s += v[u];
+    }
     const float f = inv[m];
     const float v[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
     store_f32<4>(out + 4 * e, v);
@@ -576,6 +812,23 @@ double tile_time_us(Tile t, int64_t M, int64_t N, int64_t C, int units, int spli
   return gemm + 2.0 * splits * M * N * 4.0 / 4e6;  // slices written and read at 4 TB/s
 }
 
+TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus) {
+  const int rt = transposed_rt(M);
+  const int64_t tiles = (M + 16 * rt - 1) / (16 * rt) * ((K + 127) / 128);
+  const int64_t blocks = (N + 31) / 32;
+  TransposedPlan best = {1e30, 1};
+  for (int s = 1; s <= 64 && (s == 1 || blocks >= s * TW); s = s < 4 ? s + 1 : s + s / 4) {
+    const double rounds = static_cast<double>((tiles * s + cus - 1) / cus);
+    // a wave's blocks, two waves on a SIMD; cycles of one: products and decode
+    const int64_t per_wave = ((blocks + s - 1) / s + TW - 1) / TW;
+    const double clk = std::max(8.0 * rt * units * 16, 800.0) * 1.4;
+    double us = rounds * (2.0 * per_wave * clk / 2400.0 + 3.0);
+    if (s > 1) us += 3.0 + 2.0 * s * M * K * 4 / 4e6;
+    if (us < best.us) best = {us, s};
+  }
+  return best;
+}
+
 hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s) {
   const TileDim d = tile_dim(t);
   const int tm = static_cast<int>((p.M + d.m - 1) / d.m), tn = static_cast<int>((p.N + d.n - 1) / d.n);
@@ -595,6 +848,35 @@ hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s) {
     else if (p.pa == 1) go(one, two, one);
     else go(two, two, one);
   });
+}
+
+hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
+  const int rt = transposed_rt(p.M);
+  const int mtiles = static_cast<int>((p.M + 16 * rt - 1) / (16 * rt));
+  const int tiles = static_cast<int>(mtiles * ((p.K + 127) / 128));
+  const int64_t span = (p.CB + p.splits - 1) / p.splits;
+  auto go = [&](auto rtc, auto pa, auto pb, auto type) {
+    using T = decltype(type);
+    hipLaunchKernelGGL((gemm_transposed_kernel<decltype(rtc)::value, decltype(pa)::value,
+                                               decltype(pb)::value, T>),
+                       dim3(static_cast<unsigned>(static_cast<int64_t>(tiles) * p.splits)),
+                       dim3(64 * TW), 0, s, p.g, p.w, p.n0, p.N, p.M, p.K, p.CB, mtiles, tiles, span,
+                       p.part, p.alpha, p.inv, static_cast<T*>(p.out));
+  };
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  auto parts = [&](auto rtc) {
+    // float32 has two parts of both, float16 and bfloat16 one of G
+    if (p.pa == 2) go(rtc, two, two, float{});
+    else if (p.pb == 2) go(rtc, one, two, _Float16{});
+    else if (p.type == TYPE_F16) go(rtc, one, one, _Float16{});
+    else go(rtc, one, one, __bf16{});
+  };
+  if (rt == 1) parts(one);
+  else if (rt == 2) parts(two);
+  else parts(integral_constant<int, 4>{});
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
@@ -643,6 +925,7 @@ hipError_t launch_fold(const float* part, int splits, const float* inv, void* ou
 namespace {
 
 struct DxPlan {
+  bool direct;  // straight from the Q4_0 bytes
   Tile tile;
   int pa, pb, splits;
   int64_t rows;  // weight rows, padded
@@ -668,12 +951,16 @@ DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
       }
     }
   }
-  p.splits = even_splits(p.rows / 32, p.splits);
+  // the transposed copy: written and read at about 3 TB/s, and its launch
+  best += 2.0 * N * K * p.pb * 2 / 3e6 + 3;
+  const TransposedPlan d = transposed_plan(M, N, K, units, cus);
+  p.direct = K % 64 == 0 && d.us < best;
+  p.splits = p.direct ? d.splits : even_splits(p.rows / 32, p.splits);
   Carver c;
   p.dy = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * p.pa);
   p.inv = c.take(static_cast<size_t>(M) * 4);
-  p.w = c.take(static_cast<size_t>(K) * p.rows * 2 * p.pb);
-  p.part = c.take(static_cast<size_t>(p.splits) * M * K * 4);
+  p.w = c.take(p.direct ? 0 : static_cast<size_t>(K) * p.rows * 2 * p.pb);
+  p.part = c.take(p.direct && p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * M * K * 4);
   p.total = c.at;
   return p;
 }
@@ -693,6 +980,25 @@ hipError_t launch_matmul_dx(const uint8_t* w, const void* dy, void* dx, int type
   f16x8* fb = reinterpret_cast<f16x8*>(base + p.w);
   float* part = reinterpret_cast<float*>(base + p.part);
   hipError_t e = prep_rows(dy, type, Order::NATURAL, p.pa, fa, inv, M, N, s);
+  if (e == hipSuccess && p.direct) {
+    TransposedGemm g = {};
+    g.g = fa;
+    g.pa = p.pa;
+    g.pb = p.pb;
+    g.type = type;
+    g.w = w;
+    g.N = N;
+    g.M = M;
+    g.K = K;
+    g.CB = p.rows / 32;
+    g.splits = p.splits;
+    g.part = p.splits > 1 ? part : nullptr;
+    g.inv = inv;
+    g.out = dx;
+    e = launch_gemm_transposed(g, s);
+    if (e == hipSuccess && p.splits > 1) e = launch_fold(part, p.splits, inv, dx, type, M, K, s);
+    return e;
+  }
   if (e == hipSuccess) e = prep_weights(w, 0, p.rows, N, K, nullptr, nullptr, fb, p.pb, s);
   if (e == hipSuccess) {
     const PlainGemm g = {fa, fb, p.pa, p.pb, M, K, p.rows / 32, p.splits, part, K, nullptr};
