@@ -312,30 +312,42 @@ void gemm_plain_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B,
     for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const St st(A, B, ma, rta, mb, rtb, CB, wave);
+  // Steps of one row of fragments; a row's operand is read from LDS two steps
+  // before its products, the next block's B half a block before.  The empty
+  // volatile asm keeps that order.
   auto compute = [&](const f16x8 (*buf)[64]) {
+    constexpr int STEPS = KS * S::FM;
+    f16x8 a[3][PA], b[2][PB][S::FN];
+    auto load_a = [&](int s) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      f16x8 b[PB][S::FN];
+      for (int p = 0; p < PA; ++p)
+        a[s % 3][p] = buf[(p * S::WM * S::FM + wm * S::FM + s % S::FM) * KS + s / S::FM][lane];
+    };
+    auto load_b = [&](int k) {
 #pragma unroll
       for (int p = 0; p < PB; ++p)
 #pragma unroll
         for (int j = 0; j < S::FN; ++j)
-          b[p][j] = buf[St::FA + (p * S::WN * S::FN + wn * S::FN + j) * KS + k][lane];
+          b[k & 1][p][j] = buf[St::FA + (p * S::WN * S::FN + wn * S::FN + j) * KS + k][lane];
+    };
+    load_b(0);
+    load_a(0);
+    if constexpr (STEPS > 1) load_a(1);
 #pragma unroll
-      for (int i = 0; i < S::FM; ++i) {
-        f16x8 a[PA];
+    for (int s = 0; s < STEPS; ++s) {
+      const int i = s % S::FM, k = s / S::FM;
+      if (s + 2 < STEPS) load_a(s + 2);
+      if (i == S::FM / 2 && k + 1 < KS) load_b(k + 1);
+      // D rows are B's (the columns of out), D columns A's (its rows)
 #pragma unroll
-        for (int p = 0; p < PA; ++p) a[p] = buf[(p * S::WM * S::FM + wm * S::FM + i) * KS + k][lane];
-        // D rows are B's (the columns of out), D columns A's (its rows)
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0][j], a[0], acc[i][j], 0, 0, 0);
-          if constexpr (PB == 2)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[1][j], a[0], acc[i][j], 0, 0, 0);
-          if constexpr (PA == 2)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0][j], a[1], acc[i][j], 0, 0, 0);
-        }
+      for (int j = 0; j < S::FN; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[k & 1][0][j], a[s % 3][0], acc[i][j], 0, 0, 0);
+        if constexpr (PB == 2)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[k & 1][1][j], a[s % 3][0], acc[i][j], 0, 0, 0);
+        if constexpr (PA == 2)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[k & 1][0][j], a[s % 3][1], acc[i][j], 0, 0, 0);
       }
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3])::"memory");
     }
   };
   if (c0 < c1) {  // a slice of a short reduction may be empty: its sum is zero
@@ -430,47 +442,57 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
     }
     issued();
   };
+  // Row s + 1's products are started before row s's scaled sums are taken, so
+  // the matrix cores and the vector unit overlap within the wave, and operands
+  // are read from LDS two rows (B and its scales half a block) ahead.  The
+  // empty volatile asm keeps that order (pure arithmetic would otherwise be
+  // regrouped, all products first, whose temporaries then spill).
   auto compute = [&](const f16x8 (*buf)[64], const float* sc) {
+    constexpr int STEPS = KS * S::FM;
+    f16x8 a[3][PA], b[2][S::FN];
+    float d[2][S::FN];
+    auto load_a = [&](int s) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      f16x8 b[S::FN];
-      float d[S::FN];
+      for (int p = 0; p < PA; ++p)
+        a[s % 3][p] = buf[(p * S::WM * S::FM + wm * S::FM + s % S::FM) * KS + s / S::FM][lane];
+    };
+    auto load_b = [&](int k) {
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
-        b[j] = buf[St::FA + (wn * S::FN + j) * KS + k][lane];
-        d[j] = sc[((wn * S::FN + j) * KS + k) * 16 + (lane & 15)];
+        b[k & 1][j] = buf[St::FA + (wn * S::FN + j) * KS + k][lane];
+        d[k & 1][j] = sc[((wn * S::FN + j) * KS + k) * 16 + (lane & 15)];
       }
-      // Row i + 1's products are started before row i's scaled sums are taken,
-      // so the matrix cores and the vector unit overlap within the wave.  The
-      // empty volatile asm keeps that order (pure arithmetic would otherwise
-      // be regrouped, all products first, whose temporaries then spill).
-      f32x4 t[2][S::FN];
-      auto products = [&](int i) {
-        f16x8 a[PA];
+    };
+    f32x4 t[2][S::FN];
+    auto products = [&](int s) {
+      const int k = s / S::FM;
 #pragma unroll
-        for (int p = 0; p < PA; ++p) a[p] = buf[(p * S::WM * S::FM + wm * S::FM + i) * KS + k][lane];
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-          t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[j], f32x4{0.f, 0.f, 0.f, 0.f},
-                                                               0, 0, 0);
-          if constexpr (PA == 2)
-            t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], b[j], t[i & 1][j], 0, 0, 0);
-        }
-        asm volatile("" : "+v"(t[i & 1][0]), "+v"(t[i & 1][1]), "+v"(t[i & 1][2]), "+v"(t[i & 1][3]));
-      };
-      products(0);
-#pragma unroll
-      for (int i = 0; i < S::FM; ++i) {
-        if (i + 1 < S::FM) products(i + 1);
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-          acc[i][j].x = __builtin_fmaf(d[j], t[i & 1][j].x, acc[i][j].x);
-          acc[i][j].y = __builtin_fmaf(d[j], t[i & 1][j].y, acc[i][j].y);
-          acc[i][j].z = __builtin_fmaf(d[j], t[i & 1][j].z, acc[i][j].z);
-          acc[i][j].w = __builtin_fmaf(d[j], t[i & 1][j].w, acc[i][j].w);
-        }
-        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+      for (int j = 0; j < S::FN; ++j) {
+        t[s & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[s % 3][0], b[k & 1][j],
+                                                             f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        if constexpr (PA == 2)
+          t[s & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[s % 3][1], b[k & 1][j], t[s & 1][j], 0, 0, 0);
       }
+      asm volatile("" : "+v"(t[s & 1][0]), "+v"(t[s & 1][1]), "+v"(t[s & 1][2]), "+v"(t[s & 1][3])::"memory");
+    };
+    load_b(0);
+    load_a(0);
+    if constexpr (STEPS > 1) load_a(1);
+    products(0);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int i = s % S::FM, k = s / S::FM;
+      if (s + 2 < STEPS) load_a(s + 2);
+      if (i == S::FM / 2 - 1 && k + 1 < KS) load_b(k + 1);
+      if (s + 1 < STEPS) products(s + 1);
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        acc[i][j].x = __builtin_fmaf(d[k & 1][j], t[s & 1][j].x, acc[i][j].x);
+        acc[i][j].y = __builtin_fmaf(d[k & 1][j], t[s & 1][j].y, acc[i][j].y);
+        acc[i][j].z = __builtin_fmaf(d[k & 1][j], t[s & 1][j].z, acc[i][j].z);
+        acc[i][j].w = __builtin_fmaf(d[k & 1][j], t[s & 1][j].w, acc[i][j].w);
+      }
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
     }
   };
   issue(buf0, sc0, 0);
