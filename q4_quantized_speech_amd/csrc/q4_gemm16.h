@@ -120,6 +120,11 @@ struct LogitGemm {
 };
 hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s);
 
+// The same for up to 64 rows with K = 32 CB a multiple of 128, straight from the
+// Q4_0 bytes (q and scale unused).
+constexpr int64_t DIRECT_ROWS = 64;
+hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_t s);
+
 // dx[m][k] = inv[m] * sum over the slices of part[slice][m][k], rounded once.
 hipError_t launch_fold(const float* part, int splits, const float* inv, void* out, int type,
                        int64_t M, int64_t K, hipStream_t s);

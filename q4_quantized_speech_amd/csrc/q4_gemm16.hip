@@ -401,6 +401,56 @@ __device__ __forceinline__ float row16_max(float v) {
   return v;
 }
 
+// What the logits' accumulators leave: fragments of 16 rows from row `m0` and
+// four of 16 columns from local column c0 (of `cols`, a multiple of 64); lane:
+// column lane % 16 of a fragment, rows 4 g + v.
+template <bool STATS, int FM>
+__device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0, int64_t c0,
+                                           int64_t cols, const float* __restrict__ inv, int64_t M,
+                                           int64_t n0, int64_t N, const int32_t* __restrict__ targets,
+                                           float* __restrict__ logits, float* __restrict__ tmax,
+                                           float* __restrict__ tsum, float* __restrict__ tlogit,
+                                           int64_t ld, int64_t tld) {
+  if (c0 >= cols) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t nl = c0 + (lane & 15), entry = c0 / 64;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
+      const bool live = m < M;
+      const float is = live ? inv[m] : 0.f;
+      float l[4], top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        l[j] = n0 + nl + 16 * j < N ? acc[i][j][v] * is : -__builtin_inff();
+        top = fmaxf(top, l[j]);
+      }
+      top = row16_max(top);
+      if constexpr (STATS) {
+        const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 - nl : -1;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool is_target = t == 16 * j && n0 + nl + 16 * j < N;
+          if (is_target) tlogit[m] = l[j];
+          if (!is_target && l[j] != -__builtin_inff()) s += expf(l[j] - top);
+        }
+        s = row16_sum(s);
+        if (live && (lane & 15) == 0) {
+          tmax[m * tld + entry] = top;
+          tsum[m * tld + entry] = s;
+        }
+      } else if (live) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) logits[m * ld + nl + 16 * j] = l[j];
+        if ((lane & 15) == 0) tmax[m * tld + entry] = top;
+      }
+    }
+  }
+}
+
 template <typename S, int PA, int KS, bool STATS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
@@ -511,46 +561,140 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
   }
   if (c < CB) compute(buf0, sc0);
 
-  // lane: column lane % 16 of a fragment, rows 4 g + v
-  const int64_t nl = (mb + wn * S::FN) * 16 + (lane & 15);  // local column of fragment 0
-  const int64_t entry = (mb + wn * S::FN) / 4;
-  if (mb + wn * S::FN >= rtb) return;
+  logits_out<STATS>(acc, (ma + wm * S::FM) * 16, (mb + wn * S::FN) * 16, cols, inv, M, n0, N, targets,
+                    logits, tmax, tsum, tlogit, ld, tld);
+}
+
+// ---------------------------------------------------------------------------
+// Logits of up to 64 rows straight from the Q4_0 bytes: they are read once, at
+// their size, and bound by it.  A workgroup of eight waves owns 512 weight
+// rows, each wave 64 of them; per chunk of 128 k the waves' raw bytes (72 a
+// row) and the rows' fragments go to LDS by DMA while the previous chunk is
+// multiplied.  A lane (i, g) of a wave reads dword g of a block's codes of
+// weight row i: the operand of the exact codes q - 8, the block scale applied
+// to the product (as in gemm_logits_kernel).  K % 128 == 0.
+// ---------------------------------------------------------------------------
+constexpr int DW = 8;  // waves
+
+template <int RT, int PA, bool STATS>
+__global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict__ W,
+                          const float* __restrict__ inv, int64_t M, int64_t cols, int64_t K,
+                          int64_t n0, int64_t N, const int32_t* __restrict__ targets,
+                          float* __restrict__ logits, float* __restrict__ tmax,
+                          float* __restrict__ tsum, float* __restrict__ tlogit, int64_t ld,
+                          int64_t tld) {
+  constexpr int FA = RT * PA * 4, PER = (FA + DW - 1) / DW;  // fragments of a chunk, per wave
+  __shared__ f16x8 a0[FA][64], a1[FA][64];                   // [part][row tile][block]
+  __shared__ uint32_t raw0[DW][64 * 18], raw1[DW][64 * 18];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t rb = K / 32 * BLOCK_BYTES, CB = K / 32, rta = (M + 15) / 16;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (64 * DW) + 64 * wave;
+
+  // this lane's 18 dwords of the wave's 64 rows; rows past the matrix repeat
+  // its last one (their logits are dropped)
+  const int64_t row0 = min(n0 + c0, N - 1);
+  const uint8_t* base = W + row0 * rb;
+  uint32_t off[18];
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i) {
+  for (int u = 0; u < 18; ++u) {
+    const int e = u * 64 + lane;
+    off[u] = static_cast<uint32_t>((min(n0 + c0 + e / 18, N - 1) - row0) * rb + e % 18 * 4);
+  }
+  auto issue = [&](f16x8 (*a)[64], uint32_t* raw, int64_t chunk) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t m = (ma + wm * S::FM + i) * 16 + 4 * (lane >> 4) + v;
-      const bool live = m < M;
-      const float is = live ? inv[m] : 0.f;
-      float l[S::FN], top = -__builtin_inff();
+    for (int u = 0; u < 18; ++u) to_lds<4>(base + chunk * 72 + off[u], raw + u * 64);
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j) {
-        l[j] = n0 + nl + 16 * j < N ? acc[i][j][v] * is : -__builtin_inff();
-        top = fmaxf(top, l[j]);
+    for (int u = 0; u < PER; ++u) {
+      const int f = wave * PER + u;
+      if (FA % DW != 0 && f >= FA) break;  // wave-uniform
+      const int p = f / (RT * 4), t = f / 4 % RT, b = f % 4;
+      const int64_t rt = min<int64_t>(t, rta - 1);
+      to_lds<16>(A + ((p * rta + rt) * CB + chunk * 4 + b) * 64 + lane, &a[f][0]);
+    }
+    issued();
+  };
+
+  f32x4 acc[RT][4];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // 16 steps: block b = s / 4, weight rows 16 j .. of j = s % 4; a step's
+  // codes are read one step ahead, and its scaled sums are taken while the
+  // next step's products run
+  auto compute = [&](const f16x8 (*a)[64], const uint32_t* raw) {
+    uint32_t lo[2], hi[2];
+    uint32_t dw[3];
+    f16x8 x[RT][PA];
+    f32x4 t[2][RT];
+    auto codes = [&](int s) {
+      const int b = s / 4, j = s % 4, at = 18 * b + 2;  // byte of the block's codes in a row
+      const uint32_t* p = raw + (16 * j + i) * 18;
+      lo[s & 1] = p[at / 4 + g];
+      if (at & 2) hi[s & 1] = p[at / 4 + g + 1];
+      dw[s % 3] = p[18 * b / 4];
+    };
+    auto acts = [&](int b) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int p = 0; p < PA; ++p) x[r][p] = a[(p * RT + r) * 4 + b][lane];
+    };
+    auto products = [&](int s) {
+      const int b = s / 4, at = 18 * b + 2;
+      const f16x8 q = codes8(at & 2 ? shift16(hi[s & 1], lo[s & 1]) : lo[s & 1]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        if constexpr (PA == 2)
+          t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][1], q, t[s & 1][r], 0, 0, 0);
+        asm volatile("" : "+v"(t[s & 1][r])::"memory");
       }
-      top = row16_max(top);
-      if constexpr (STATS) {
-        const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 - nl : -1;
-        float s = 0.f;
+    };
+    codes(0);
+    acts(0);
+    codes(1);
+    products(0);
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-          const bool is_target = t == 16 * j && n0 + nl + 16 * j < N;
-          if (is_target) tlogit[m] = l[j];
-          if (!is_target && l[j] != -__builtin_inff()) s += expf(l[j] - top);
-        }
-        s = row16_sum(s);
-        if (live && (lane & 15) == 0) {
-          tmax[m * tld + entry] = top;
-          tsum[m * tld + entry] = s;
-        }
-      } else if (live) {
+    for (int s = 0; s < 16; ++s) {
+      if (s + 2 < 16) codes(s + 2);
+      if (s + 1 < 16) {
+        if ((s + 1) % 4 == 0) acts((s + 1) / 4);
+        products(s + 1);
+      }
+      const int b = s / 4, j = s % 4;
+      const float d = half_bits_to_float((18 * b) & 2 ? dw[s % 3] >> 16 : dw[s % 3] & 0xFFFFu);
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j)
-          if (nl + 16 * j < cols) logits[m * ld + nl + 16 * j] = l[j];
-        if ((lane & 15) == 0) tmax[m * tld + entry] = top;
+      for (int r = 0; r < RT; ++r) {
+        acc[r][j].x = __builtin_fmaf(d, t[s & 1][r].x, acc[r][j].x);
+        acc[r][j].y = __builtin_fmaf(d, t[s & 1][r].y, acc[r][j].y);
+        acc[r][j].z = __builtin_fmaf(d, t[s & 1][r].z, acc[r][j].z);
+        acc[r][j].w = __builtin_fmaf(d, t[s & 1][r].w, acc[r][j].w);
+        asm volatile("" : "+v"(acc[r][j]));
       }
     }
+  };
+  const int64_t chunks = K / 128;
+  issue(a0, raw0[wave], 0);
+  arrived();
+  __syncthreads();
+  int64_t c = 0;
+  for (; c + 2 <= chunks; c += 2) {
+    issue(a1, raw1[wave], c + 1);
+    compute(a0, raw0[wave]);
+    arrived();
+    __syncthreads();
+    if (c + 2 < chunks) issue(a0, raw0[wave], c + 2);
+    compute(a1, raw1[wave]);
+    arrived();
+    __syncthreads();
   }
+  if (c < chunks) compute(a0, raw0[wave]);
+  logits_out<STATS>(acc, 0, c0, cols, inv, M, n0, N, targets, logits, tmax, tsum, tlogit, ld, tld);
 }
 
 // ---------------------------------------------------------------------------
@@ -923,6 +1067,30 @@ hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
       if (p.pa == 1) go(one, two, yes); else go(two, one, yes);
     }
   });
+}
+
+hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>((p.cols + 64 * DW - 1) / (64 * DW));
+  auto go = [&](auto rt, auto pa, auto stats) {
+    hipLaunchKernelGGL((logits_direct_kernel<decltype(rt)::value, decltype(pa)::value, decltype(stats)::value>),
+                       dim3(grid), dim3(64 * DW), 0, s, p.a, w, p.inv, p.M, p.cols, p.CB * 32, p.n0, p.N,
+                       p.targets, p.logits, p.tmax, p.tsum, p.tlogit, p.ld, p.tld);
+  };
+  using std::integral_constant;
+  auto parts = [&](auto rt) {
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    if (p.logits) {
+      if (p.pa == 1) go(rt, one, std::false_type{}); else go(rt, two, std::false_type{});
+    } else {
+      if (p.pa == 1) go(rt, one, std::true_type{}); else go(rt, two, std::true_type{});
+    }
+  };
+  if (p.M <= 16) parts(integral_constant<int, 1>{});
+  else if (p.M <= 32) parts(integral_constant<int, 2>{});
+  else if (p.M <= 48) parts(integral_constant<int, 3>{});
+  else parts(integral_constant<int, 4>{});
+  return hipGetLastError();
 }
 
 hipError_t launch_fold(const float* part, int splits, const float* inv, void* out, int type,

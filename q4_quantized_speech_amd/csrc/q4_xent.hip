@@ -15,8 +15,9 @@
 // the sum of the other probabilities, so a row the model is sure of keeps its
 // small gradient and loss.
 //
-// A few rows without a gradient go through the matvec-accuracy kernels four
-// rows at a time instead: they read the table at its Q4_0 size.
+// Up to 64 rows read the table at its Q4_0 size instead, for the logits and for
+// the gradient (K % 128 == 0); up to four rows without a gradient go through
+// the matvec-accuracy kernels.
 
 #include <algorithm>
 
@@ -249,11 +250,13 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
   }
 }
 
-// Rows whose loss alone goes through the matvec-accuracy kernels.
-constexpr int64_t FEW_ROWS = 16;
+// Rows whose loss alone goes through the matvec-accuracy kernels, four at a
+// time: where the direct kernel does not serve K, a table read per four rows
+// still beats unpacking it (measured up to 16).
+int64_t few_rows(int64_t K) { return K % 128 == 0 ? 4 : 16; }
 
 struct XentPlan {
-  bool few;
+  bool few, direct;
   int pa, pp, pb, splits;      // parts of x, of the probabilities and of the transposed weights
   Tile t1, t2;
   int64_t piece, entries, chunks;
@@ -264,7 +267,8 @@ struct XentPlan {
 XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus) {
   XentPlan p = {};
   Carver c;
-  p.few = !grad && M <= FEW_ROWS;
+  p.few = !grad && M <= few_rows(K);
+  p.direct = !p.few && M <= DIRECT_ROWS && K % 128 == 0;
   p.run_max = c.take(M * 4);
   p.run_sum = c.take(M * 4);
   p.tlogit = c.take(M * 4);
@@ -280,40 +284,47 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus
   p.pa = type == TYPE_F32 ? 2 : 1;
   p.pp = p.pa;  // probabilities and weights: binary16's 11 bits below a 16-bit result's rounding
   p.pb = p.pa;
-  // pieces of equal size, their logits up to 256 MiB
-  const int64_t cap = std::max<int64_t>(2048, std::min<int64_t>(32768, (int64_t(1) << 26) / M / 256 * 256));
+  // pieces of equal size, their logits up to 256 MiB, their unpacked weights too
+  int64_t cap = std::max<int64_t>(2048, (int64_t(1) << 26) / M / 256 * 256);
+  if (!p.direct) cap = std::min<int64_t>(cap, 32768);
   const int64_t pieces = (N + cap - 1) / cap;
   p.piece = ((N + pieces - 1) / pieces + 255) / 256 * 256;
   p.piece = std::min<int64_t>(p.piece, (N + 63) / 64 * 64);
   p.entries = p.piece / 64;
   p.chunks = (p.piece + PC_CHUNK - 1) / PC_CHUNK;
-  double best1 = 1e30, best2 = 1e30;
-  for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
-    const double us = tile_time_us(t, M, p.piece, K, p.pa, 1, cus);
-    if (us < best1) {
-      best1 = us;
-      p.t1 = t;
-    }
-    for (int s = 1; s <= 16 && (s == 1 || p.piece / s >= 128); ++s) {
-      const double u2 = tile_time_us(t, M, K, p.piece, p.pp + p.pb - 1, s, cus);
-      if (u2 < best2) {
-        best2 = u2;
-        p.t2 = t;
-        p.splits = s;
+  if (p.direct) {
+    p.splits = transposed_plan(M, p.piece, K, p.pp + p.pb - 1, cus).splits;
+  } else {
+    double best1 = 1e30, best2 = 1e30;
+    for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
+      const double us = tile_time_us(t, M, p.piece, K, p.pa, 1, cus);
+      if (us < best1) {
+        best1 = us;
+        p.t1 = t;
+      }
+      for (int s = 1; s <= 16 && (s == 1 || p.piece / s >= 128); ++s) {
+        const double u2 = tile_time_us(t, M, K, p.piece, p.pp + p.pb - 1, s, cus);
+        if (u2 < best2) {
+          best2 = u2;
+          p.t2 = t;
+          p.splits = s;
+        }
       }
     }
+    p.splits = even_splits(p.piece / 32, p.splits);
   }
-  p.splits = even_splits(p.piece / 32, p.splits);
   p.x = c.take(static_cast<size_t>(frag_elems(M, K)) * 16 * p.pa);
   p.inv = c.take(M * 4);
   p.alpha = c.take(M * 4);
   p.tmax = c.take(static_cast<size_t>(M) * p.entries * 4);
-  p.codes = c.take(static_cast<size_t>(frag_elems(p.piece, K)) * 16);
-  p.scale = c.take(static_cast<size_t>(p.piece) * blocks32(K) * 4);
+  if (!p.direct) {
+    p.codes = c.take(static_cast<size_t>(frag_elems(p.piece, K)) * 16);
+    p.scale = c.take(static_cast<size_t>(p.piece) * blocks32(K) * 4);
+  }
   if (grad) {
     p.psum = c.take(static_cast<size_t>(p.chunks) * M * 4);
     p.logits = c.take(static_cast<size_t>(M) * p.piece * 4);
-    p.wt = c.take(static_cast<size_t>(K) * p.piece * 2 * p.pb);
+    if (!p.direct) p.wt = c.take(static_cast<size_t>(K) * p.piece * 2 * p.pb);
     p.prob = c.take(static_cast<size_t>(frag_elems(M, p.piece)) * 16 * p.pp);
     p.part = c.take(static_cast<size_t>(p.splits) * M * K * 4);
   } else {
@@ -380,7 +391,7 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
     for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
       const bool first = n0 == 0;
       const int64_t cols = std::min<int64_t>(p.piece, (N - n0 + 63) / 64 * 64);
-      Q4_TRY(prep_weights(w, n0, cols, N, K, codes, f32(p.scale), wt, p.pb, s));
+      if (!p.direct) Q4_TRY(prep_weights(w, n0, cols, N, K, codes, f32(p.scale), wt, p.pb, s));
       LogitGemm lg = {};
       lg.a = xa;
       lg.q = codes;
@@ -399,7 +410,7 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
       lg.tlogit = tlogit;
       lg.ld = p.piece;
       lg.tld = p.entries;
-      Q4_TRY(launch_gemm_logits(p.t1, lg, s));
+      Q4_TRY(p.direct ? launch_logits_direct(w, lg, s) : launch_gemm_logits(p.t1, lg, s));
       const int64_t entries = cols / 64;
       if (!grad) {
         hipLaunchKernelGGL(xent_rows_kernel<false>, rows4, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
@@ -422,6 +433,24 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
       Q4_TRY(hipGetLastError());
       // a shorter last piece may fill fewer slices: the others keep their sums
       // but still have to move to the new maximum, so every piece uses p.splits
+      if (p.direct) {
+        TransposedGemm g = {};
+        g.g = prob;
+        g.pa = p.pp;
+        g.pb = p.pb;
+        g.type = type;
+        g.w = w;
+        g.n0 = n0;
+        g.N = N;
+        g.M = M;
+        g.K = K;
+        g.CB = cols / 32;
+        g.splits = p.splits;
+        g.part = f32(p.part);
+        g.alpha = first ? nullptr : f32(p.alpha);
+        Q4_TRY(launch_gemm_transposed(g, s));
+        continue;
+      }
       PlainGemm g = {};
       g.a = prob;
       g.b = wt;

@@ -199,6 +199,16 @@ def test_xent_shapes(m, n, k, dtype):
     xent_case(m, n, k, dtype, 4500 + m + n, grad=False, targets=ODD if m > 5 else None)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("m,n,k", [(1, 31, 128), (5, 300, 128), (15, 513, 256), (16, 512, 384), (17, 1025, 128),
+                                   (32, 700, 640), (33, 2000, 256), (48, 511, 128), (49, 65, 256), (64, 3000, 384),
+                                   (65, 600, 128)])
+def test_xent_few_rows(m, n, k, dtype):
+    """Up to 64 rows with K a multiple of 128: straight from the Q4_0 bytes; one row more."""
+    xent_case(m, n, k, dtype, 4700 + m + n, targets=ODD if m > 5 else None)
+    xent_case(m, n, k, dtype, 4800 + m + n, grad=False, targets=ODD if m > 5 else None)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_xent_pieces(dtype):
     """Several pieces of the vocabulary, a short last one, the maximum growing through them;
@@ -208,6 +218,13 @@ def test_xent_pieces(dtype):
         xent_case(20, n, 64, dtype, 5000 + n, ramp=True, targets=t)
         xent_case(20, n, 64, dtype, 5000 + n, ramp=True, targets=t, grad=False)
     xent_case(3000, 45000, 32, dtype, 5100, ramp=True, targets=ODD)
+
+
+def test_xent_few_rows_pieces():
+    """The direct form's pieces are of 2^26 / M columns: 64 rows over a table past one of them."""
+    n = (1 << 20) + 777
+    xent_case(64, n, 128, BF16, 5150, ramp=True, targets=[0, n - 1, (n + 1) // 2 // 256 * 256, -1])
+    xent_case(64, n, 128, F32, 5150, ramp=True, grad=False)
 
 
 @pytest.mark.parametrize("grad", [False, True])
