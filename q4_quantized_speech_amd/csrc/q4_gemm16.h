@@ -22,12 +22,13 @@ namespace q4 {
 
 enum class Order { NIBBLE, NATURAL };
 
-// Fragments of M x C activations: `parts` copies (hi, then lo) of
-// [ceil(M / 16)][CB] fragments, CB = ceil(C / 64) * 2 blocks of 32, zeros past
-// M and C.  Each row is scaled by a power of two that brings its largest
-// magnitude to [2^14, 2^15); inv[m] is the inverse.
-hipError_t prep_rows(const void* x, int type, Order order, int parts, f16x8* frag, float* inv,
-                     int64_t M, int64_t C, hipStream_t s);
+// Fragments of M x C activations: [ceil(M / 16)][CB] of them, CB = ceil(C / 64)
+// * 2 blocks of 32, zeros past M and C, in two copies (hi, then lo) for float32
+// and one for the 16-bit types.  Each row of float32 or bfloat16 is scaled by a
+// power of two that brings its largest magnitude to [2^14, 2^15); inv[m] is the
+// inverse (1 for float16).
+hipError_t prep_rows(const void* x, int type, Order order, f16x8* frag, float* inv, int64_t M,
+                     int64_t C, hipStream_t s);
 
 inline int64_t blocks32(int64_t c) { return (c + 63) / 64 * 2; }
 inline int64_t frag_elems(int64_t rows, int64_t c) { return (rows + 15) / 16 * blocks32(c) * 64; }

@@ -36,13 +36,31 @@ __device__ __forceinline__ float row_scale(float top) {
   return ldexpf(1.f, min(15 - e, 126));
 }
 
+// Memory to LDS without registers: lane l's `SIZE` bytes at g land at
+// l + SIZE * lane.  Asynchronous: arrived() before the barrier that publishes.
+template <int SIZE>
+__device__ __forceinline__ void to_lds(const void* g, void* l) {
+  static_assert(SIZE == 16 || SIZE == 4, "bytes per lane");
+  const auto gp = (const __attribute__((address_space(1))) void*)g;
+  const auto lp = (__attribute__((address_space(3))) void*)l;
+  if constexpr (SIZE == 16)
+    __builtin_amdgcn_global_load_lds(gp, lp, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds(gp, lp, 4, 0, 0);
+}
+// The loads to LDS before this point are issued before the work after it (they
+// touch other arrays, so the compiler would be free to start them late).
+__device__ __forceinline__ void issued() { asm volatile("" ::: "memory"); }
+// This wave's loads to LDS are complete, and no LDS access moves across.
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // Operand preparation
 // ---------------------------------------------------------------------------
 
 // One wave per row, 16 rows per workgroup, gridDim.y parts of the columns.
 // Every workgroup takes the rows' maxima over all columns (its siblings' reads
-// come from the L2), then its columns, 512 at a time.  The fragments are put
+// come from the L2), then its columns, 1024 at a time.  The fragments are put
 // together in LDS and written whole: a wave's own 16-byte pieces lie 256 bytes
 // apart (12.4 us for 16 x 3072 float32 that way).
 template <typename T, bool NIB, int PARTS, bool VEC>
@@ -50,7 +68,8 @@ __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X
                                                          f16x8* __restrict__ out,
                                                          float* __restrict__ inv, int64_t M,
                                                          int64_t C, int64_t CB, int64_t bspan) {
-  __shared__ f16x8 tile[2][PARTS][16][64];  // [buffer][part][block][swizzled lane]
+  constexpr int SL = 2;  // slots of eight values per lane and pass: 32 blocks
+  __shared__ f16x8 tile[2][PARTS][16 * SL][64];  // [buffer][part][block][swizzled lane]
   const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + i;
   const bool live = m < M;
@@ -66,84 +85,90 @@ __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X
       for (int e = 0; e < 4; ++e) v[e] = live && c + e < C ? to_f32(row[c + e]) : 0.f;
     }
   };
-  constexpr int PU = 4;  // groups of eight values in flight
-  float top = 0.f;
-  for (int64_t c = 8 * lane; c < C; c += 512 * PU) {
-    float v[PU][8];
+  // float16 needs no scale: every value is one already
+  float s = 1.f;
+  if constexpr (!__is_same(T, _Float16)) {
+    constexpr int PU = sizeof(T) == 4 ? 4 : 8;  // groups of eight values in flight
+    float top = 0.f;
+    for (int64_t c = 8 * lane; c < C; c += 512 * PU) {
+      float v[PU][8];
 #pragma unroll
-    for (int u = 0; u < PU; ++u) {
-      load4(c + 512 * u, v[u]);
-      load4(c + 512 * u + 4, v[u] + 4);
+      for (int u = 0; u < PU; ++u) {
+        load4(c + 512 * u, v[u]);
+        load4(c + 512 * u + 4, v[u] + 4);
+      }
+#pragma unroll
+      for (int u = 0; u < PU; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[u][e]));
     }
-#pragma unroll
-    for (int u = 0; u < PU; ++u)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[u][e]));
+    s = row_scale(wave_max(top));
   }
-  top = wave_max(top);
-  const float s = row_scale(top);
   if (live && lane == 0 && blockIdx.y == 0) inv[m] = 1.f / s;
   const int64_t part = static_cast<int64_t>(gridDim.x) * CB * 64;
   const int64_t b0 = blockIdx.y * bspan, b1 = min(CB, b0 + bspan);
-  const int blk = lane >> 2, g = lane & 3;  // this lane's slot of 16 blocks
-  float v[8];
+  const int blk = lane >> 2, g = lane & 3;  // this lane's slot of each 16 blocks
+  float v[SL][8];
   auto load = [&](int64_t b) {
-    const int64_t c = 32 * (b + blk);
-    load4(c + (NIB ? 4 * g : 8 * g), v);
-    load4(c + (NIB ? 16 + 4 * g : 8 * g + 4), v + 4);
+#pragma unroll
+    for (int u = 0; u < SL; ++u) {
+      const int64_t c = 32 * (b + 16 * u + blk);
+      load4(c + (NIB ? 4 * g : 8 * g), v[u]);
+      load4(c + (NIB ? 16 + 4 * g : 8 * g + 4), v[u] + 4);
+    }
   };
   load(b0);
   int cur = 0;
-  for (int64_t b = b0; b < b1; b += 16, cur ^= 1) {
-    f16x8 hi, lo;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = v[e] * s;
-      hi[e] = static_cast<_Float16>(x);
-      if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
-    }
-    if (b + 16 < b1) load(b + 16);
+  for (int64_t b = b0; b < b1; b += 16 * SL, cur ^= 1) {
     // lane i + 16 g of a block sits at (i ^ (4 blk + g)) + 16 g: the lanes of a
     // wave (one i) then hit distinct banks, and so do the readers (one block)
     const int at = 16 * g + (i ^ (lane & 15));
-    tile[cur][0][blk][at] = hi;
-    if constexpr (PARTS == 2) tile[cur][1][blk][at] = lo;
+#pragma unroll
+    for (int u = 0; u < SL; ++u) {
+      f16x8 hi, lo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[u][e] * s;
+        hi[e] = static_cast<_Float16>(x);
+        if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
+      }
+      tile[cur][0][16 * u + blk][at] = hi;
+      if constexpr (PARTS == 2) tile[cur][1][16 * u + blk][at] = lo;
+    }
+    if (b + 16 * SL < b1) load(b + 16 * SL);
     __syncthreads();
-    if (b + i < b1) {  // wave i writes block b + i
-      const int from = (lane & 48) + ((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));
-      const int64_t to = (static_cast<int64_t>(blockIdx.x) * CB + b + i) * 64 + lane;
-      out[to] = tile[cur][0][i][from];
-      if constexpr (PARTS == 2) out[part + to] = tile[cur][1][i][from];
+    const int from = (lane & 48) + ((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));
+#pragma unroll
+    for (int u = 0; u < SL; ++u) {  // wave i writes blocks b + i and b + 16 + i
+      const int64_t mine = b + 16 * u + i;
+      if (mine >= b1) break;
+      const int64_t to = (static_cast<int64_t>(blockIdx.x) * CB + mine) * 64 + lane;
+      out[to] = tile[cur][0][16 * u + i][from];
+      if constexpr (PARTS == 2) out[part + to] = tile[cur][1][16 * u + i][from];
     }
   }
 }
 
 template <typename T>
-void prep_rows_t(const T* x, Order order, int parts, f16x8* frag, float* inv, int64_t M, int64_t C,
+void prep_rows_t(const T* x, Order order, f16x8* frag, float* inv, int64_t M, int64_t C,
                  hipStream_t s) {
   const int64_t CB = blocks32(C), tiles = (M + 15) / 16;
-  // about a workgroup per CU, each at least 16 blocks
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((CB + 15) / 16, 256 / tiles));
-  const int64_t bspan = ((CB + want - 1) / want + 15) / 16 * 16;
+  // about a workgroup per CU, each at least 32 blocks
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((CB + 31) / 32, 256 / tiles));
+  const int64_t bspan = ((CB + want - 1) / want + 31) / 32 * 32;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((CB + bspan - 1) / bspan));
   const dim3 block(1024);
+  constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
   const bool vec = C % 4 == 0;
-  auto go = [&](auto nib, auto p, auto v) {
-    hipLaunchKernelGGL((prep_rows_kernel<T, decltype(nib)::value, decltype(p)::value, decltype(v)::value>),
-                       grid, block, 0, s, x, frag, inv, M, C, CB, bspan);
-  };
-  using std::integral_constant;
-  const integral_constant<int, 1> p1;
-  const integral_constant<int, 2> p2;
-  const std::true_type yes;
-  const std::false_type no;
-  if (order == Order::NIBBLE) {  // K is a multiple of 32
-    if (parts == 2) go(yes, p2, yes); else go(yes, p1, yes);
-  } else if (parts == 2) {
-    if (vec) go(no, p2, yes); else go(no, p2, no);
-  } else {
-    if (vec) go(no, p1, yes); else go(no, p1, no);
-  }
+  if (order == Order::NIBBLE)  // K is a multiple of 32
+    hipLaunchKernelGGL((prep_rows_kernel<T, true, PARTS, true>), grid, block, 0, s, x, frag, inv, M,
+                       C, CB, bspan);
+  else if (vec)
+    hipLaunchKernelGGL((prep_rows_kernel<T, false, PARTS, true>), grid, block, 0, s, x, frag, inv, M,
+                       C, CB, bspan);
+  else
+    hipLaunchKernelGGL((prep_rows_kernel<T, false, PARTS, false>), grid, block, 0, s, x, frag, inv, M,
+                       C, CB, bspan);
 }
 
 // (q - 8) of the eight codes of a dword, binary16, NIBBLE order.
@@ -175,7 +200,7 @@ __global__ __launch_bounds__(256) void prep_codes_kernel(const uint8_t* __restri
   scale[f * 16 + i] = half_bits_to_float(d);
 }
 
-// One thread per (32-row block, group of 8 rows, block of 32 weights, code
+// Any K (the kernel below takes K % 64 == 0).  One thread per (32-row block, group of 8 rows, block of 32 weights, code
 // dword): eight rows' dwords hold eight columns, whose operands are written
 // with the eight rows as the reduction.
 template <int PARTS>
@@ -218,6 +243,124 @@ __global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __re
   }
 }
 
+// A wave's 32 rows x 72 bytes (128 columns from column 128 kt) to its own LDS,
+// as consecutive dwords: byte offsets of this lane's nine from the first row.
+// Rows past `rows` repeat the last one, dwords past the row (rb bytes) its last.
+__device__ __forceinline__ void raw_offsets(int64_t rows, int64_t rb, int kt, uint32_t (&off)[9]) {
+  const int lane = threadIdx.x & 63;
+  const int64_t most = rb / 4 - 1 - kt * 18;
+#pragma unroll
+  for (int u = 0; u < 9; ++u) {
+    const int e = u * 64 + lane;
+    off[u] = static_cast<uint32_t>(min<int64_t>(e / 18, rows - 1) * rb + min<int64_t>(e % 18, most) * 4);
+  }
+}
+constexpr int RAW = 32 * 18 + 16;  // dwords of it, and what the last row's pair of reads touches
+
+// Lane (i, g): dword i % 4 of the codes of block i / 4 and that block's scale
+// in rows 8 g .. 8 g + 7.  A block starts at byte 18 (i / 4) of a row: its
+// scale in either half of a dword, its codes from the next half on.
+struct RawCodes {
+  uint32_t q[8];
+  f16x2 d[4];
+  __device__ __forceinline__ explicit RawCodes(const uint32_t* raw) {
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int first = 18 * (i >> 2), code = first + 2 + 4 * (i & 3);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const uint32_t* p = raw + (8 * g + r) * 18;
+      const uint32_t* c = p + (code >> 2);
+      q[r] = __builtin_amdgcn_alignbit(c[1], c[0], 8 * (code & 2));
+      d[r >> 1][r & 1] = reinterpret_cast<const _Float16*>(p)[first >> 1];
+    }
+  }
+  // Low (h = 0) or high codes of every byte.
+  __device__ __forceinline__ void half(int h, uint32_t (&nib)[8]) const {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) nib[r] = (h ? q[r] >> 4 : q[r]) & 0x0F0F0F0Fu;
+  }
+  // The eight rows' weights (q - 8) d of byte b: hi rounded once to binary16,
+  // lo the exact rest.
+  template <int PB>
+  __device__ __forceinline__ void column(const uint32_t (&nib)[8], int b, f16x8& hi, f16x8& lo) const {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t pair =
+          __builtin_amdgcn_perm(nib[2 * p + 1], nib[2 * p], 0x0C000C00u | ((4u + b) << 16) | b) | 0x64006400u;
+      const f16x2 off8 = {static_cast<_Float16>(-1032.0f), static_cast<_Float16>(-1032.0f)};
+      const f16x2 w = __builtin_bit_cast(f16x2, pair) + off8;
+      const f16x2 wd = w * d[p];
+      hi[2 * p] = wd[0];
+      hi[2 * p + 1] = wd[1];
+      if constexpr (PB == 2) {
+        // w has at most 15 significant bits and is a multiple of 2^-24 like
+        // its scale, so the rest fits binary16
+        const f16x2 rest = __builtin_elementwise_fma(w, d[p], -wd);
+        lo[2 * p] = rest[0];
+        lo[2 * p + 1] = rest[1];
+      }
+    }
+  }
+};
+
+// K % 64 == 0: a wave takes 32 rows x 128 columns, turned in registers, put
+// together in LDS and written as whole fragments (16-byte pieces 64 bytes
+// apart, as above, take 1.9 times as long on 32768 rows of 3072).
+template <int PARTS>
+__global__ __launch_bounds__(256) void prep_transpose64_kernel(const uint8_t* __restrict__ W,
+                                                               int64_t n0, int64_t N, int64_t K,
+                                                               int64_t NB, int ktiles,
+                                                               f16x8* __restrict__ tfrag) {
+  __shared__ uint32_t raw[4][RAW];
+  __shared__ f16x8 tile[4][8][64];  // [wave][fragment][swizzled lane]
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t nb = item / ktiles;
+  const int kt = static_cast<int>(item - nb * ktiles);
+  if (nb >= NB) return;
+  const int64_t rb = K / 32 * BLOCK_BYTES, n = n0 + nb * 32;
+  const int64_t rows = max<int64_t>(1, min<int64_t>(32, N - n));
+  uint32_t off[9];
+  raw_offsets(rows, rb, kt, off);
+  const uint8_t* base = W + min(n, N - 1) * rb + static_cast<int64_t>(kt) * 72;
+#pragma unroll
+  for (int u = 0; u < 9; ++u) to_lds<4>(base + off[u], raw[wave] + u * 64);
+  arrived();
+  RawCodes codes(raw[wave]);
+  // rows past the matrix: weights of zero
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (n + 8 * g + r >= N) codes.d[r >> 1][r & 1] = static_cast<_Float16>(0.f);
+  const int64_t part = K / 16 * NB * 64;
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t nib[8];
+      codes.half(h, nib);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        f16x8 hi, lo;
+        codes.column<PARTS>(nib, b, hi, lo);
+        // fragment 2 (i / 4) + h, its lane 4 (i % 4) + b + 16 g; the low bits
+        // are mixed with g so that the lanes of a store spread over the banks
+        tile[wave][2 * (i >> 2) + h][4 * (i & 3) + (b ^ g) + 16 * g] = p ? lo : hi;
+      }
+    }
+    // the tile is the wave's own, and LDS operations of a wave complete in order
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      const int64_t kf = static_cast<int64_t>(kt) * 8 + f;
+      const f16x8 v = tile[wave][f][lane ^ (lane >> 4)];
+      if (kf < K / 16) tfrag[p * part + (kf * NB + nb) * 64 + lane] = v;
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The product.  WM x WN waves, each FM x FN fragments of 16 x 16 outputs; a
 // stage is KS blocks of 32 reduction indices of every fragment row of the
@@ -231,24 +374,6 @@ struct Shape {
 using S256 = Shape<2, 4, 8, 4>;
 using S128 = Shape<2, 2, 4, 4>;
 using S32 = Shape<1, 4, 2, 4>;
-
-// Memory to LDS without registers: lane l's `SIZE` bytes at g land at
-// l + SIZE * lane.  Asynchronous: arrived() before the barrier that publishes.
-template <int SIZE>
-__device__ __forceinline__ void to_lds(const void* g, void* l) {
-  static_assert(SIZE == 16 || SIZE == 4, "bytes per lane");
-  const auto gp = (const __attribute__((address_space(1))) void*)g;
-  const auto lp = (__attribute__((address_space(3))) void*)l;
-  if constexpr (SIZE == 16)
-    __builtin_amdgcn_global_load_lds(gp, lp, 16, 0, 0);
-  else
-    __builtin_amdgcn_global_load_lds(gp, lp, 4, 0, 0);
-}
-// The loads to LDS before this point are issued before the work after it (they
-// touch other arrays, so the compiler would be free to start them late).
-__device__ __forceinline__ void issued() { asm volatile("" ::: "memory"); }
-// This wave's loads to LDS are complete, and no LDS access moves across.
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <typename S, int PA, int PB, int KS>
 struct Stage {
@@ -724,9 +849,8 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
                             const float* __restrict__ inv, T* __restrict__ out) {
   constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time
   __shared__ f32x4 red[4][RP * 8][64];
-  // two arrays: reading one does not have to wait for loads into the other.
-  // 18 dwords a row, and one that the last row's pair of reads touches
-  __shared__ uint32_t raw0[TW][32 * 18 + 16], raw1[TW][32 * 18 + 16];
+  // two arrays: reading one does not have to wait for loads into the other
+  __shared__ uint32_t raw0[TW][RAW], raw1[TW][RAW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -737,25 +861,16 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
   const int64_t rta = (M + 15) / 16, live = min(CB, (N - n0 + 31) / 32);
   const int64_t b1 = min(live, (split + 1) * span);
 
-  // this lane's nine dwords of a block: byte offsets from its first row; rows
-  // past the matrix repeat its last one (G is zero there), columns past it
+  // rows past the matrix repeat its last one (G is zero there), columns past it
   // its last dword (their results are dropped)
   uint32_t off[9];
-  auto offsets = [&](int64_t nb) {
-    const int64_t rows = min<int64_t>(32, N - n0 - nb * 32), most = rb / 4 - 1 - kt * 18;
-#pragma unroll
-    for (int u = 0; u < 9; ++u) {
-      const int e = u * 64 + lane;
-      off[u] = static_cast<uint32_t>(min<int64_t>(e / 18, rows - 1) * rb + min<int64_t>(e % 18, most) * 4);
-    }
-  };
-  offsets(0);
+  raw_offsets(min<int64_t>(32, N - n0), rb, kt, off);
 
   struct Acts {
     f16x8 a[RT][PA];
   };
   auto load = [&](int64_t nb, uint32_t* raw, Acts& x) {
-    if (n0 + nb * 32 + 32 > N) offsets(nb);  // the last, partial block
+    if (n0 + nb * 32 + 32 > N) raw_offsets(N - n0 - nb * 32, rb, kt, off);  // the last, partial block
     const uint8_t* base = W + (n0 + nb * 32) * rb + static_cast<int64_t>(kt) * 72;
 #pragma unroll
     for (int u = 0; u < 9; ++u) to_lds<4>(base + off[u], raw + u * 64);
@@ -775,44 +890,16 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // block i / 4 starts at byte 18 (i / 4) of a row: its scale in either half of
-  // a dword, its codes from the next half on
-  const int first = 18 * (i >> 2), code = first + 2 + 4 * (i & 3);
   auto compute = [&](const uint32_t* raw, const Acts& x) {
-    uint32_t q8[8];
-    f16x2 d[4];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const uint32_t* p = raw + (8 * g + r) * 18;
-      const uint32_t* c = p + (code >> 2);
-      q8[r] = __builtin_amdgcn_alignbit(c[1], c[0], 8 * (code & 2));
-      d[r >> 1][r & 1] = reinterpret_cast<const _Float16*>(p)[first >> 1];
-    }
+    const RawCodes codes(raw);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t nib[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) nib[r] = (h ? q8[r] >> 4 : q8[r]) & 0x0F0F0F0Fu;
+      codes.half(h, nib);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        // byte b of two rows as binary16 1024 + q, then (q - 8) d, rounded once
         f16x8 hi, lo;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t pair =
-              __builtin_amdgcn_perm(nib[2 * q + 1], nib[2 * q], 0x0C000C00u | ((4u + b) << 16) | b) |
-              0x64006400u;
-          const f16x2 off8 = {static_cast<_Float16>(-1032.0f), static_cast<_Float16>(-1032.0f)};
-          const f16x2 w = __builtin_bit_cast(f16x2, pair) + off8;
-          const f16x2 wd = w * d[q];
-          hi[2 * q] = wd[0];
-          hi[2 * q + 1] = wd[1];
-          if constexpr (PB == 2) {  // the exact rest
-            const f16x2 rest = __builtin_elementwise_fma(w, d[q], -wd);
-            lo[2 * q] = rest[0];
-            lo[2 * q + 1] = rest[1];
-          }
-        }
+        codes.template column<PB>(nib, b, hi, lo);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           f32x4& s = acc[t][4 * h + b];
@@ -933,14 +1020,14 @@ hipError_t with_tile(Tile t, F f) {
 
 }  // namespace
 
-hipError_t prep_rows(const void* x, int type, Order order, int parts, f16x8* frag, float* inv,
-                     int64_t M, int64_t C, hipStream_t s) {
+hipError_t prep_rows(const void* x, int type, Order order, f16x8* frag, float* inv, int64_t M,
+                     int64_t C, hipStream_t s) {
   if (type == TYPE_F32)
-    prep_rows_t(static_cast<const float*>(x), order, parts, frag, inv, M, C, s);
+    prep_rows_t(static_cast<const float*>(x), order, frag, inv, M, C, s);
   else if (type == TYPE_F16)
-    prep_rows_t(static_cast<const _Float16*>(x), order, parts, frag, inv, M, C, s);
+    prep_rows_t(static_cast<const _Float16*>(x), order, frag, inv, M, C, s);
   else
-    prep_rows_t(static_cast<const __bf16*>(x), order, parts, frag, inv, M, C, s);
+    prep_rows_t(static_cast<const __bf16*>(x), order, frag, inv, M, C, s);
   return hipGetLastError();
 }
 
@@ -951,7 +1038,16 @@ hipError_t prep_weights(const uint8_t* w, int64_t n0, int64_t rows, int64_t N, i
   if (qfrag)
     hipLaunchKernelGGL(prep_codes_kernel, dim3(static_cast<unsigned>(rows / 16), gy), dim3(256), 0,
                        s, w, n0, N, kblocks, KB, qfrag, scale);
-  if (tfrag) {
+  if (tfrag && K % 64 == 0) {
+    const int ktiles = static_cast<int>((K + 127) / 128);
+    const dim3 grid(static_cast<unsigned>((rows / 32 * ktiles + 3) / 4));
+    if (parts == 2)
+      hipLaunchKernelGGL(prep_transpose64_kernel<2>, grid, dim3(256), 0, s, w, n0, N, K, rows / 32,
+                         ktiles, tfrag);
+    else
+      hipLaunchKernelGGL(prep_transpose64_kernel<1>, grid, dim3(256), 0, s, w, n0, N, K, rows / 32,
+                         ktiles, tfrag);
+  } else if (tfrag) {
     const dim3 grid(static_cast<unsigned>(rows / 32), gy);
     if (parts == 2)
       hipLaunchKernelGGL(prep_transpose_kernel<2>, grid, dim3(256), 0, s, w, n0, N, kblocks,
@@ -1169,7 +1265,7 @@ hipError_t launch_matmul_dx(const uint8_t* w, const void* dy, void* dx, int type
   float* inv = reinterpret_cast<float*>(base + p.inv);
   f16x8* fb = reinterpret_cast<f16x8*>(base + p.w);
   float* part = reinterpret_cast<float*>(base + p.part);
-  hipError_t e = prep_rows(dy, type, Order::NATURAL, p.pa, fa, inv, M, N, s);
+  hipError_t e = prep_rows(dy, type, Order::NATURAL, fa, inv, M, N, s);
   if (e == hipSuccess && p.direct) {
     TransposedGemm g = {};
     g.g = fa;

@@ -42,47 +42,85 @@ __device__ __forceinline__ float wave_max(float v) {
 // exp(a - b) for a <= b; 1 where both are the same infinity.
 __device__ __forceinline__ float exp_below(float a, float b) { return a == b ? 1.f : expf(a - b); }
 
-// Per row, one wave each.  GRAD: the new running maximum, alpha = the factor
-// that moves sums and gradients to it, and the running sum with the previous
-// piece's partial sums (psum [chunks][M]).  Else: the piece's own (tmax,
-// tsum) entries folded into the running pair.
+// Over the four waves of a workgroup, in all threads.
+__device__ __forceinline__ float group_max(float v, float* red) {
+  v = wave_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+__device__ __forceinline__ float group_sum(float v, float* red) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return ((red[0] + red[1]) + red[2]) + red[3];
+}
+
+// loss and lse of a row from its maximum and its sum without the target (et:
+// the target's term, 0 for a row without one).
+__device__ __forceinline__ void row_loss(float top, float rest, float et, float target_logit,
+                                         bool valid, float& loss, float& lse) {
+  lse = top + logf(rest + et);
+  loss = !valid ? 0.f : et >= rest ? log1pf(rest / et) : logf(rest + et) + (top - target_logit);
+}
+
+// Per row, one workgroup each.  GRAD: the new running maximum, alpha = the
+// factor that moves sums and gradients to it, and the running sum with the
+// previous piece's partial sums (psum [chunks][M]).  Else: the piece's own
+// (tmax, tsum) entries folded into the running pair, and after the last piece
+// (loss not null) the results.
 template <bool GRAD>
-__global__ __launch_bounds__(256) void xent_rows_kernel(const float* __restrict__ tmax,
-                                                        const float* __restrict__ tsum,
-                                                        int64_t entries, int64_t tld,
-                                                        const float* __restrict__ psum, int chunks,
-                                                        float* __restrict__ run_max,
-                                                        float* __restrict__ run_sum,
-                                                        float* __restrict__ alpha, int64_t M,
-                                                        bool first) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (m >= M) return;
+__global__ __launch_bounds__(256) void xent_rows_kernel(
+    const float* __restrict__ tmax, const float* __restrict__ tsum, int64_t entries, int64_t tld,
+    const float* __restrict__ psum, int chunks, float* __restrict__ run_max,
+    float* __restrict__ run_sum, float* __restrict__ alpha, int64_t M, bool first,
+    const float* __restrict__ tlogit, const int32_t* __restrict__ targets, int64_t N,
+    float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float red[4];
+  constexpr int U = 8;  // entries in flight per thread
+  const int64_t m = blockIdx.x;
   float top = -__builtin_inff();
-  for (int64_t e = lane; e < entries; e += 64) top = fmaxf(top, tmax[m * tld + e]);
-  top = wave_max(top);
+  for (int64_t e0 = threadIdx.x; e0 < entries; e0 += 256 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e0 + 256 * u < entries) top = fmaxf(top, tmax[m * tld + e0 + 256 * u]);
+  }
+  top = group_max(top, red);
   const float old = first ? -__builtin_inff() : run_max[m];
   top = fmaxf(top, old);
   const float al = first ? 0.f : exp_below(old, top);
   float s = 0.f;
   if constexpr (GRAD) {
     if (!first)
-      for (int c = lane; c < chunks; c += 64) s += psum[static_cast<int64_t>(c) * M + m];
-    s = wave_sum(s);
-    if (lane == 0) {
+      for (int c = threadIdx.x; c < chunks; c += 256) s += psum[static_cast<int64_t>(c) * M + m];
+    s = group_sum(s, red);
+    if (threadIdx.x == 0) {
       run_sum[m] = first ? 0.f : (run_sum[m] + s) * al;
       alpha[m] = al;
       run_max[m] = top;
     }
   } else {
-    for (int64_t e = lane; e < entries; e += 64) {
-      const float t = tsum[m * tld + e];
-      if (t != 0.f) s += t * exp_below(tmax[m * tld + e], top);
+    for (int64_t e0 = threadIdx.x; e0 < entries; e0 += 256 * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t e = e0 + 256 * u;
+        const float t = e < entries ? tsum[m * tld + e] : 0.f;
+        if (t != 0.f) s += t * exp_below(tmax[m * tld + e], top);
+      }
     }
-    s = wave_sum(s);
-    if (lane == 0) {
-      run_sum[m] = (first ? 0.f : run_sum[m] * al) + s;
-      run_max[m] = top;
+    s = group_sum(s, red);
+    if (threadIdx.x == 0) {
+      const float sum = (first ? 0.f : run_sum[m] * al) + s;
+      if (loss) {
+        const int64_t t = targets[m];
+        const bool valid = t >= 0 && t < N;
+        row_loss(top, sum, valid ? exp_below(tlogit[m], top) : 0.f, tlogit[m], valid, loss[m], lse[m]);
+      } else {
+        run_sum[m] = sum;
+        run_max[m] = top;
+      }
     }
   }
 }
@@ -149,7 +187,7 @@ __global__ __launch_bounds__(256) void xent_prob_kernel(const float* __restrict_
   }
 }
 
-// loss, lse and (dx not null) the gradient: one workgroup per row.
+// loss, lse and the gradient: one workgroup per row.
 template <typename T>
 __global__ __launch_bounds__(256) void xent_final_kernel(
     const float* __restrict__ run_max, const float* __restrict__ run_sum,
@@ -165,13 +203,7 @@ __global__ __launch_bounds__(256) void xent_final_kernel(
   for (int c = 0; c < chunks; ++c) rest += psum[static_cast<int64_t>(c) * M + m];
   const float top = run_max[m];
   const float et = valid ? exp_below(tlogit[m], top) : 0.f;
-  if (threadIdx.x == 0) {
-    lse[m] = top + logf(rest + et);
-    loss[m] = !valid ? 0.f
-              : et >= rest ? log1pf(rest / et)
-                           : logf(rest + et) + (top - tlogit[m]);
-  }
-  if (!dx) return;
+  if (threadIdx.x == 0) row_loss(top, rest, et, tlogit[m], valid, loss[m], lse[m]);
   const float g = valid ? (dloss ? dloss[m] : 1.f) : 0.f;
   const float f = 1.f / (rest + et);
   T* o = dx + m * K;
@@ -354,10 +386,8 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
   char* base = static_cast<char*>(ws);
   auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
   float *run_max = f32(p.run_max), *run_sum = f32(p.run_sum), *tlogit = f32(p.tlogit);
-  const dim3 rows4(static_cast<unsigned>((M + 3) / 4));
-  const float* psum = nullptr;
+  const dim3 rows(static_cast<unsigned>(M));
   int chunks = 0;
-  const float* part = nullptr;
 
   if (p.few) {
     const float* xf = static_cast<const float*>(x);
@@ -379,99 +409,99 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
     hipLaunchKernelGGL(xent_chunk_kernel,
                        dim3(static_cast<unsigned>(p.entries), static_cast<unsigned>(M)), dim3(256), 0,
                        s, f32(p.logits), targets, f32(p.tmax), f32(p.tsum), tlogit, N);
-    hipLaunchKernelGGL(xent_rows_kernel<false>, rows4, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
-                       p.entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, true);
-    Q4_TRY(hipGetLastError());
-  } else {
-    f16x8* xa = reinterpret_cast<f16x8*>(base + p.x);
-    f16x8* codes = reinterpret_cast<f16x8*>(base + p.codes);
-    f16x8* wt = grad ? reinterpret_cast<f16x8*>(base + p.wt) : nullptr;
-    f16x8* prob = reinterpret_cast<f16x8*>(base + p.prob);
-    Q4_TRY(prep_rows(x, type, Order::NIBBLE, p.pa, xa, f32(p.inv), M, K, s));
-    for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
-      const bool first = n0 == 0;
-      const int64_t cols = std::min<int64_t>(p.piece, (N - n0 + 63) / 64 * 64);
-      if (!p.direct) Q4_TRY(prep_weights(w, n0, cols, N, K, codes, f32(p.scale), wt, p.pb, s));
-      LogitGemm lg = {};
-      lg.a = xa;
-      lg.q = codes;
-      lg.pa = p.pa;
-      lg.scale = f32(p.scale);
-      lg.inv = f32(p.inv);
-      lg.M = M;
-      lg.cols = cols;
-      lg.CB = blocks32(K);
-      lg.n0 = n0;
-      lg.N = N;
-      lg.targets = targets;
-      lg.logits = grad ? f32(p.logits) : nullptr;
-      lg.tmax = f32(p.tmax);
-      lg.tsum = grad ? nullptr : f32(p.tsum);
-      lg.tlogit = tlogit;
-      lg.ld = p.piece;
-      lg.tld = p.entries;
-      Q4_TRY(p.direct ? launch_logits_direct(w, lg, s) : launch_gemm_logits(p.t1, lg, s));
-      const int64_t entries = cols / 64;
-      if (!grad) {
-        hipLaunchKernelGGL(xent_rows_kernel<false>, rows4, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
-                           entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, first);
-        Q4_TRY(hipGetLastError());
-        continue;
-      }
-      // `chunks` still is the previous piece's count
-      hipLaunchKernelGGL(xent_rows_kernel<true>, rows4, dim3(256), 0, s, f32(p.tmax), nullptr,
-                         entries, p.entries, f32(p.psum), chunks, run_max, run_sum, f32(p.alpha), M,
-                         first);
-      chunks = static_cast<int>((cols + PC_CHUNK - 1) / PC_CHUNK);
-      const dim3 pg(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>(chunks));
-      if (p.pp == 2)
-        hipLaunchKernelGGL(xent_prob_kernel<2>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
-                           prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
-      else
-        hipLaunchKernelGGL(xent_prob_kernel<1>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
-                           prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
+    hipLaunchKernelGGL(xent_rows_kernel<false>, rows, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
+                       p.entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, true, tlogit,
+                       targets, N, loss, lse);
+    return hipGetLastError();
+  }
+  f16x8* xa = reinterpret_cast<f16x8*>(base + p.x);
+  f16x8* codes = reinterpret_cast<f16x8*>(base + p.codes);
+  f16x8* wt = grad ? reinterpret_cast<f16x8*>(base + p.wt) : nullptr;
+  f16x8* prob = reinterpret_cast<f16x8*>(base + p.prob);
+  Q4_TRY(prep_rows(x, type, Order::NIBBLE, xa, f32(p.inv), M, K, s));
+  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
+    const bool first = n0 == 0;
+    const int64_t cols = std::min<int64_t>(p.piece, (N - n0 + 63) / 64 * 64);
+    if (!p.direct) Q4_TRY(prep_weights(w, n0, cols, N, K, codes, f32(p.scale), wt, p.pb, s));
+    LogitGemm lg = {};
+    lg.a = xa;
+    lg.q = codes;
+    lg.pa = p.pa;
+    lg.scale = f32(p.scale);
+    lg.inv = f32(p.inv);
+    lg.M = M;
+    lg.cols = cols;
+    lg.CB = blocks32(K);
+    lg.n0 = n0;
+    lg.N = N;
+    lg.targets = targets;
+    lg.logits = grad ? f32(p.logits) : nullptr;
+    lg.tmax = f32(p.tmax);
+    lg.tsum = grad ? nullptr : f32(p.tsum);
+    lg.tlogit = tlogit;
+    lg.ld = p.piece;
+    lg.tld = p.entries;
+    Q4_TRY(p.direct ? launch_logits_direct(w, lg, s) : launch_gemm_logits(p.t1, lg, s));
+    const int64_t entries = cols / 64;
+    if (!grad) {
+      const bool last = n0 + p.piece >= N;
+      hipLaunchKernelGGL(xent_rows_kernel<false>, rows, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
+                         entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, first, tlogit,
+                         targets, N, last ? loss : nullptr, lse);
       Q4_TRY(hipGetLastError());
-      // a shorter last piece may fill fewer slices: the others keep their sums
-      // but still have to move to the new maximum, so every piece uses p.splits
-      if (p.direct) {
-        TransposedGemm g = {};
-        g.g = prob;
-        g.pa = p.pp;
-        g.pb = p.pb;
-        g.type = type;
-        g.w = w;
-        g.n0 = n0;
-        g.N = N;
-        g.M = M;
-        g.K = K;
-        g.CB = cols / 32;
-        g.splits = p.splits;
-        g.part = f32(p.part);
-        g.alpha = first ? nullptr : f32(p.alpha);
-        Q4_TRY(launch_gemm_transposed(g, s));
-        continue;
-      }
-      PlainGemm g = {};
-      g.a = prob;
-      g.b = wt;
+      continue;
+    }
+    // `chunks` still is the previous piece's count
+    hipLaunchKernelGGL(xent_rows_kernel<true>, rows, dim3(256), 0, s, f32(p.tmax), nullptr, entries,
+                       p.entries, f32(p.psum), chunks, run_max, run_sum, f32(p.alpha), M, first,
+                       nullptr, nullptr, N, nullptr, nullptr);
+    chunks = static_cast<int>((cols + PC_CHUNK - 1) / PC_CHUNK);
+    const dim3 pg(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>(chunks));
+    if (p.pp == 2)
+      hipLaunchKernelGGL(xent_prob_kernel<2>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
+                         prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
+    else
+      hipLaunchKernelGGL(xent_prob_kernel<1>, pg, dim3(256), 0, s, f32(p.logits), run_max, targets,
+                         prob, f32(p.psum), tlogit, M, cols, p.piece, n0, N);
+    Q4_TRY(hipGetLastError());
+    // a shorter last piece may fill fewer slices: the others keep their sums
+    // but still have to move to the new maximum, so every piece uses p.splits
+    if (p.direct) {
+      TransposedGemm g = {};
+      g.g = prob;
       g.pa = p.pp;
       g.pb = p.pb;
+      g.type = type;
+      g.w = w;
+      g.n0 = n0;
+      g.N = N;
       g.M = M;
-      g.N = K;
+      g.K = K;
       g.CB = cols / 32;
       g.splits = p.splits;
-      g.out = f32(p.part);
-      g.ld = K;
+      g.part = f32(p.part);
       g.alpha = first ? nullptr : f32(p.alpha);
-      Q4_TRY(launch_gemm_plain(p.t2, g, s));
+      Q4_TRY(launch_gemm_transposed(g, s));
+      continue;
     }
-    if (grad) {
-      psum = f32(p.psum);
-      part = f32(p.part);
-    }
+    PlainGemm g = {};
+    g.a = prob;
+    g.b = wt;
+    g.pa = p.pp;
+    g.pb = p.pb;
+    g.M = M;
+    g.N = K;
+    g.CB = cols / 32;
+    g.splits = p.splits;
+    g.out = f32(p.part);
+    g.ld = K;
+    g.alpha = first ? nullptr : f32(p.alpha);
+    Q4_TRY(launch_gemm_plain(p.t2, g, s));
   }
+  if (!grad) return hipSuccess;
+  const float *psum = f32(p.psum), *part = f32(p.part);
   const dim3 grid(static_cast<unsigned>(M));
-  const int splits = grad ? p.splits : 0;
+  const int splits = p.splits;
   if (type == TYPE_F32)
     hipLaunchKernelGGL(xent_final_kernel<float>, grid, dim3(256), 0, s, run_max, run_sum, psum,
                        chunks, tlogit, targets, dloss, part, splits, w, loss, lse,
