@@ -468,9 +468,6 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
     const float sc = scale ? scale[a] : 1.f;
     const int count = group.count;
     if (count <= FEW) {
-      int at[FEW];
-#pragma unroll
-      for (int u = 0; u < FEW; ++u) at[u] = __builtin_amdgcn_readlane(group.packed, u);
       float* hf = reinterpret_cast<float*>(hs);  // [FEW][R]
       for (int e = threadIdx.x; e < FEW * R; e += 64 * WAVES) {
         const int u = e / R, j = e - u * R;
@@ -478,54 +475,46 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
         if (u < count) hf[e] = sc * sum_slices(P + (m0 + row) * R + j, splits, M * R);
       }
       __syncthreads();
-      // COLS columns per thread, so that their rows of B are in flight at once
-      auto columns = [&](auto cnt, auto cols) {
-        constexpr int U = decltype(cnt)::value, COLS = decltype(cols)::value;
-        for (int64_t n = n0 + threadIdx.x; n < n1; n += COLS * 64 * WAVES) {
-          float acc[COLS][U], q[COLS][U];
-          const TA* bn[COLS];
-#pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            const int64_t nc = n + c * 64 * WAVES;
-            bn[c] = b + (nc < n1 ? nc : n) * R;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              q[c][u] = u < count && R_ && nc < n1 ? to_f32(R_[(m0 + at[u]) * N + nc]) : 0.f;
-              acc[c][u] = 0.f;
-            }
+      // two rows and two columns per thread at a time: four sums, two rows of B
+      // in flight (short code matters: each workgroup runs it a few times)
+#pragma unroll 1
+      for (int u = 0; u < count; u += 2) {
+        const bool both = u + 1 < count;
+        const int64_t row0 = (m0 + __builtin_amdgcn_readlane(group.packed, u)) * N;
+        const int64_t row1 = both ? (m0 + __builtin_amdgcn_readlane(group.packed, u + 1)) * N : row0;
+        const float *h0 = hf + u * R, *h1 = both ? h0 + R : h0;
+#pragma unroll 1
+        for (int64_t n = n0 + threadIdx.x; n < n1; n += 2 * 64 * WAVES) {
+          const bool two = n + 64 * WAVES < n1;
+          const int64_t n2 = two ? n + 64 * WAVES : n;
+          float q[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if (R_) {
+            q[0] = to_f32(R_[row0 + n]);
+            q[1] = to_f32(R_[row0 + n2]);
+            q[2] = to_f32(R_[row1 + n]);
+            q[3] = to_f32(R_[row1 + n2]);
           }
+          const TA *b0 = b + n * R, *b1 = b + n2 * R;
 #pragma unroll 2
           for (int j = 0; j < R; j += 8) {
-            float w[COLS][8];
+            float w0[8], w1[8];
+            row8<true>(b0, j, R, true, w0);
+            row8<true>(b1, j, R, true, w1);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) row8<true>(bn[c], j, R, true, w[c]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const f32x4 h0 = *reinterpret_cast<const f32x4*>(hf + u * R + j);
-              const f32x4 h1 = *reinterpret_cast<const f32x4*>(hf + u * R + j + 4);
-#pragma unroll
-              for (int c = 0; c < COLS; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  acc[c][u] = __builtin_fmaf(w[c][e], h0[e], acc[c][u]);
-                  acc[c][u] = __builtin_fmaf(w[c][4 + e], h1[e], acc[c][u]);
-                }
+            for (int e = 0; e < 8; ++e) {
+              const float x0 = h0[j + e], x1 = h1[j + e];
+              acc[0] = __builtin_fmaf(w0[e], x0, acc[0]);
+              acc[1] = __builtin_fmaf(w1[e], x0, acc[1]);
+              acc[2] = __builtin_fmaf(w0[e], x1, acc[2]);
+              acc[3] = __builtin_fmaf(w1[e], x1, acc[3]);
             }
           }
-#pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            const int64_t nc = n + c * 64 * WAVES;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-              if (u < count && nc < n1) Y[(m0 + at[u]) * N + nc] = from_f32<T>(q[c][u] + acc[c][u]);
-          }
+          Y[row0 + n] = from_f32<T>(q[0] + acc[0]);
+          if (two) Y[row0 + n2] = from_f32<T>(q[1] + acc[1]);
+          if (both) Y[row1 + n] = from_f32<T>(q[2] + acc[2]);
+          if (both && two) Y[row1 + n2] = from_f32<T>(q[3] + acc[3]);
         }
-      };
-      using std::integral_constant;
-      if (count <= 2)
-        columns(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-      else
-        columns(integral_constant<int, FEW>{}, integral_constant<int, 1>{});
+      }
       return;
     }
     load_rank<NP>(P, splits, M, R, m0, group, sc, hs);
@@ -564,13 +553,21 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
   });
   // rows without an adapter: y = r
   if (blockIdx.y == 0 && R_ != Y) {
-    const uint64_t rows = rows_without(ids, m0, M, adapters);
-    if (rows != 0u) {
-      const f32x4 zero[4] = {};
-      for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES)
-#pragma unroll
-        for (int s = 0; s < SUB; ++s)
-          if ((rows >> (16 * s + i)) & 1u) write(base, 16 * s + i, zero);
+    const Group group(rows_without(ids, m0, M, adapters));
+    typedef T piece __attribute__((ext_vector_type(V)));
+    const int step = vec ? V : 1, per = static_cast<int>((n1 - n0 + step - 1) / step);
+    const int total = group.count * per;
+    for (int e0 = 0; e0 < total; e0 += 64 * WAVES) {
+      const int e = e0 + static_cast<int>(threadIdx.x), u = e / per;
+      const int64_t at = (m0 + group.of(u < LT ? u : 0)) * N + n0 + static_cast<int64_t>(e - u * per) * step;
+      if (e >= total) continue;
+      if (vec) {
+        piece p = {};
+        if (R_) p = *reinterpret_cast<const piece*>(R_ + at);
+        *reinterpret_cast<piece*>(Y + at) = p;
+      } else {
+        Y[at] = R_ ? R_[at] : from_f32<T>(0.f);
+      }
     }
   }
 }
