@@ -274,7 +274,7 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
       finish(acc, s0);
     };
     // as many blocks at once as the registers hold beside the factor
-    constexpr int NS = RT <= 2 ? SUB : SUB / 2;
+    constexpr int NS = RT <= 2 && sizeof(T) == 4 ? SUB : SUB / 2;
     if (group.count <= 16)
       steps(std::integral_constant<int, 1>{}, 0);
     else
@@ -283,7 +283,7 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
 }
 
 template <typename T, typename TA, int RT>
-__global__ __launch_bounds__(64 * DOWN_WAVES, RT == 1 && sizeof(T) == 2 ? 4 : 2) void lora_down_kernel(
+__global__ __launch_bounds__(64 * DOWN_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_down_kernel(
     const T* __restrict__ X, const TA* __restrict__ A, const int32_t* __restrict__ ids,
     float* __restrict__ P, int64_t M, int64_t K, int R, int adapters, int splits, int64_t span) {
   __shared__ f32x4 red[DOWN_WAVES][4][64];
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES, RT == 1 && sizeof(T) == 2 ? 4 : 2)
 // Both rank vectors of the backward pass: workgroups below `hblocks` h (from
 // x), the rest g (from dy).
 template <typename T, typename TA, int RT, bool VEC>
-__global__ __launch_bounds__(64 * DOWN_WAVES, RT == 1 && sizeof(T) == 2 ? 4 : 2) void lora_down2_kernel(
+__global__ __launch_bounds__(64 * DOWN_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_down2_kernel(
     const T* __restrict__ X, const T* __restrict__ DY, const TA* __restrict__ A,
     const TA* __restrict__ B, const int32_t* __restrict__ ids, float* __restrict__ PH,
     float* __restrict__ PG, int64_t M, int64_t N, int64_t K, int R, int adapters, int hsplits,
@@ -608,39 +608,51 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
     load_rank<NP>(G, 1, M, R, m0, group, 1.f, hs);
     __syncthreads();
     const TA* ad = A + static_cast<int64_t>(a) * R * K;
-    const int blocks = group.blocks();
+    // blocks of 16 rows at a time: two leave the registers for two workgroups on
+    // a CU (1500 x 5120 x 1280, rank 32: 30.6 -> 18.0 us for the kernel)
+    constexpr int NS = sizeof(T) == 2 ? 2 : SUB;
     for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES) {
-      f32x4 acc[SUB][4];
-#pragma unroll
-      for (int s = 0; s < SUB; ++s)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
       const int64_t k = min(base + 4 * i, K - 4);
-      for (int j0 = 0; j0 < R; j0 += 32) {
-        // rows j0 + 8 g .. + 7 of A, four columns each, turned into the
-        // operands of the four columns
-        const int j = j0 + 8 * g;
-        float v[8][4];
+#pragma unroll 1
+      for (int s0 = 0; s0 < group.blocks(); s0 += NS) {
+        f32x4 acc[NS][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) v[e][t] = 0.f;
-          if (j < R) load_f32<4>(ad + static_cast<int64_t>(j + e) * K + k, v[e]);  // R % 8 == 0
-        }
+          for (int t = 0; t < 4; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int j0 = 0; j0 < R; j0 += 32) {
+          // rows j0 + 8 g .. + 7 of A, four columns each, turned into the
+          // operands of the four columns
+          const int j = j0 + 8 * g;
+          typedef TA piece __attribute__((ext_vector_type(4)));
+          piece v[8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float col[8] = {v[0][t], v[1][t], v[2][t], v[3][t], v[4][t], v[5][t], v[6][t], v[7][t]};
-          const Parts<parts_of<TA>> w = split8<parts_of<TA>>(col);
+          for (int e = 0; e < 8; ++e) {
+            v[e] = piece{};
+            if (j < R) v[e] = *reinterpret_cast<const piece*>(ad + static_cast<int64_t>(j + e) * K + k);  // R % 8 == 0
+          }
+          Parts<NP> h[NS];
 #pragma unroll
-          for (int s = 0; s < SUB; ++s) {
-            if (s >= blocks) break;
-            acc[s][t] = mfma_parts(rank_parts<NP>(hs, ld, 16 * s + i, j), w, acc[s][t]);
+          for (int s = 0; s < NS; ++s) h[s] = rank_parts<NP>(hs, ld, 16 * (s0 + s) + i, j);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            Parts<parts_of<TA>> w;
+            if constexpr (__is_same(TA, __bf16)) {
+              w.p[0] = bf16x8{v[0][t], v[1][t], v[2][t], v[3][t], v[4][t], v[5][t], v[6][t], v[7][t]};
+            } else {
+              float col[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) col[e] = to_f32(static_cast<TA>(v[e][t]));
+              w = split8<parts_of<TA>>(col);
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s) acc[s][t] = mfma_parts(h[s], w, acc[s][t]);
           }
         }
-      }
 #pragma unroll
-      for (int s = 0; s < SUB; ++s)
-        if (s < blocks) write(group, s, base, acc[s]);
+        for (int s = 0; s < NS; ++s) write(group, s0 + s, base, acc[s]);
+      }
     }
   });
   if (mine == 0 && R_ != DX) {
@@ -676,24 +688,25 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
     const int64_t mine = r0 + lane;
     const uint64_t match = __ballot(mine < M && ids[min(mine, M - 1)] == a);
     if constexpr (sizeof(T) == 2) {
-      // 32 rows at a time: lane (i, g) has rows 8 g .. 8 g + 7
+      // 32 rows at a time: lane (i, g) has rows 8 g .. 8 g + 7, four columns
+      // each as they are in memory
 #pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         if ((static_cast<uint32_t>(match >> (32 * q))) == 0u) continue;
         const unsigned ok = static_cast<unsigned>(match >> (32 * q + 8 * g)) & 0xFFu;
         const int64_t m = r0 + 32 * q + 8 * g;
-        float z[8][4];
+        typedef T piece __attribute__((ext_vector_type(4)));
+        piece z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const T* zr = Z + min(m + e, M - 1) * C;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) z[e][u] = 0.f;
+          z[e] = piece{};
           if constexpr (VEC) {
-            if (((ok >> e) & 1u) && c < C) load_f32<4>(zr + c, z[e]);
+            if (((ok >> e) & 1u) && c < C) z[e] = *reinterpret_cast<const piece*>(zr + c);
           } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              if (((ok >> e) & 1u) && c + u < C) z[e][u] = to_f32(zr[c + u]);
+              if (((ok >> e) & 1u) && c + u < C) z[e][u] = zr[c + u];
           }
         }
         u32x4 keep;  // both halves of a dword: two rows
@@ -714,8 +727,15 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float col[8] = {z[0][u], z[1][u], z[2][u], z[3][u], z[4][u], z[5][u], z[6][u], z[7][u]};
-          const Parts<parts_of<T>> w = split8<parts_of<T>>(col);
+          Parts<parts_of<T>> w;
+          if constexpr (__is_same(T, __bf16)) {
+            w.p[0] = bf16x8{z[0][u], z[1][u], z[2][u], z[3][u], z[4][u], z[5][u], z[6][u], z[7][u]};
+          } else {
+            float col[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) col[e] = to_f32(static_cast<T>(z[e][u]));
+            w = split8<parts_of<T>>(col);
+          }
 #pragma unroll
           for (int t = 0; t < RT; ++t) acc[t][u] = mfma_parts(l[t], w, acc[t][u]);
         }
@@ -787,7 +807,7 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
 // adapters * achunks dA, the rest dB.
 constexpr int G_WAVES = 8;
 template <typename T, typename TA, int RT, bool VEC>
-__global__ __launch_bounds__(64 * G_WAVES) void lora_grad_kernel(
+__global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_grad_kernel(
     const float* __restrict__ H, const float* __restrict__ G, const uint16_t* __restrict__ HT,
     const uint16_t* __restrict__ GT, int64_t MP, const T* __restrict__ X,
     const T* __restrict__ DY, const TA* __restrict__ A, const int32_t* __restrict__ ids,
