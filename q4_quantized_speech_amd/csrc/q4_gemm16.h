@@ -121,7 +121,7 @@ struct LogitGemm {
 };
 hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s);
 
-// The same for up to 64 rows with K = 32 CB a multiple of 128, straight from the
+// The same for up to 64 rows with K = 32 CB a multiple of 64, straight from the
 // Q4_0 bytes (q and scale unused).
 constexpr int64_t DIRECT_ROWS = 64;
 hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_t s);

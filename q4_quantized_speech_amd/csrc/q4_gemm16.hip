@@ -63,6 +63,8 @@ __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::
 // come from the L2), then its columns, 1024 at a time.  The fragments are put
 // together in LDS and written whole: a wave's own 16-byte pieces lie 256 bytes
 // apart (12.4 us for 16 x 3072 float32 that way).
+// VEC: C % 4 == 0 (without it, reading the last elements one by one makes the
+// kernel 18.7 us long for 1500 x 5120 bfloat16, with it 15).
 template <typename T, bool NIB, int PARTS, bool VEC>
 __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X,
                                                          f16x8* __restrict__ out,
@@ -75,14 +77,17 @@ __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X
   const bool live = m < M;
   const T* row = X + (live ? m : 0) * C;
   auto load4 = [&](int64_t c, float* v) {
-    if constexpr (VEC) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live && c < C) load_f32<4>(row + c, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = 0.f;
+    if (live && c + (VEC ? 0 : 3) < C) {
+      float t[4];
+      load_any_f32<4>(row + c, t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = t[e];
-    } else {
+    } else if (!VEC && live) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = live && c + e < C ? to_f32(row[c + e]) : 0.f;
+      for (int e = 0; e < 4; ++e)
+        if (c + e < C) v[e] = to_f32(row[c + e]);
     }
   };
   // float16 needs no scale: every value is one already
@@ -159,11 +164,10 @@ void prep_rows_t(const T* x, Order order, f16x8* frag, float* inv, int64_t M, in
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((CB + bspan - 1) / bspan));
   const dim3 block(1024);
   constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
-  const bool vec = C % 4 == 0;
-  if (order == Order::NIBBLE)  // K is a multiple of 32
+  if (order == Order::NIBBLE)  // C is K, a multiple of 32
     hipLaunchKernelGGL((prep_rows_kernel<T, true, PARTS, true>), grid, block, 0, s, x, frag, inv, M,
                        C, CB, bspan);
-  else if (vec)
+  else if (C % 4 == 0)
     hipLaunchKernelGGL((prep_rows_kernel<T, false, PARTS, true>), grid, block, 0, s, x, frag, inv, M,
                        C, CB, bspan);
   else
@@ -697,11 +701,12 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
 // row) and the rows' fragments go to LDS by DMA while the previous chunk is
 // multiplied.  A lane (i, g) of a wave reads dword g of a block's codes of
 // weight row i: the operand of the exact codes q - 8, the block scale applied
-// to the product (as in gemm_logits_kernel).  K % 128 == 0.
+// to the product (as in gemm_logits_kernel).  K % 64 == 0 (rows start on a
+// dword).
 // ---------------------------------------------------------------------------
 constexpr int DW = 8;  // waves
 
-template <int RT, int PA, bool STATS>
+template <int RT, int PA, bool STATS, bool HALF>
 __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict__ W,
                           const float* __restrict__ inv, int64_t M, int64_t cols, int64_t K,
@@ -728,16 +733,23 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
     const int e = u * 64 + lane;
     off[u] = static_cast<uint32_t>((min(n0 + c0 + e / 18, N - 1) - row0) * rb + e % 18 * 4);
   }
+  const int64_t chunks = (K + (HALF ? 127 : 0)) / 128;
   auto issue = [&](f16x8 (*a)[64], uint32_t* raw, int64_t chunk) {
+    // HALF, K % 128 == 64: the last chunk is half one; the second half's places are
+    // filled with its first again, and not used
+    const bool half = HALF && (chunk + 1) * 128 > K;
 #pragma unroll
-    for (int u = 0; u < 18; ++u) to_lds<4>(base + chunk * 72 + off[u], raw + u * 64);
+    for (int u = 0; u < 18; ++u) {
+      const uint32_t back = half && (u * 64 + lane) % 18 >= 9 ? 36u : 0u;
+      to_lds<4>(base + chunk * 72 + off[u] - back, raw + u * 64);
+    }
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int f = wave * PER + u;
       if (FA % DW != 0 && f >= FA) break;  // wave-uniform
       const int p = f / (RT * 4), t = f / 4 % RT, b = f % 4;
       const int64_t rt = min<int64_t>(t, rta - 1);
-      to_lds<16>(A + ((p * rta + rt) * CB + chunk * 4 + b) * 64 + lane, &a[f][0]);
+      to_lds<16>(A + ((p * rta + rt) * CB + (HALF ? min(chunk * 4 + b, CB - 1) : chunk * 4 + b)) * 64 + lane, &a[f][0]);
     }
     issued();
   };
@@ -751,7 +763,8 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
   // 16 steps: block b = s / 4, weight rows 16 j .. of j = s % 4; a step's
   // codes are read one step ahead, and its scaled sums are taken while the
   // next step's products run
-  auto compute = [&](const f16x8 (*a)[64], const uint32_t* raw) {
+  auto compute = [&](auto steps, const f16x8 (*a)[64], const uint32_t* raw) {
+    constexpr int STEPS = decltype(steps)::value;
     uint32_t lo[2], hi[2];
     uint32_t dw[3];
     f16x8 x[RT][PA];
@@ -785,9 +798,9 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
     codes(1);
     products(0);
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
-      if (s + 2 < 16) codes(s + 2);
-      if (s + 1 < 16) {
+    for (int s = 0; s < STEPS; ++s) {
+      if (s + 2 < STEPS) codes(s + 2);
+      if (s + 1 < STEPS) {
         if ((s + 1) % 4 == 0) acts((s + 1) / 4);
         products(s + 1);
       }
@@ -803,22 +816,34 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
       }
     }
   };
-  const int64_t chunks = K / 128;
+  const std::integral_constant<int, 16> whole;
+  const std::integral_constant<int, 8> halved;
+  const int64_t full = K / 128;
   issue(a0, raw0[wave], 0);
   arrived();
   __syncthreads();
   int64_t c = 0;
-  for (; c + 2 <= chunks; c += 2) {
+  for (; c + 2 <= full; c += 2) {
     issue(a1, raw1[wave], c + 1);
-    compute(a0, raw0[wave]);
+    compute(whole, a0, raw0[wave]);
     arrived();
     __syncthreads();
     if (c + 2 < chunks) issue(a0, raw0[wave], c + 2);
-    compute(a1, raw1[wave]);
+    compute(whole, a1, raw1[wave]);
     arrived();
     __syncthreads();
   }
-  if (c < chunks) compute(a0, raw0[wave]);
+  if (c < full) {
+    if constexpr (HALF) issue(a1, raw1[wave], c + 1);
+    compute(whole, a0, raw0[wave]);
+    if constexpr (HALF) {
+      arrived();
+      __syncthreads();
+      compute(halved, a1, raw1[wave]);
+    }
+  } else if constexpr (HALF) {
+    compute(halved, a0, raw0[wave]);
+  }
   logits_out<STATS>(acc, 0, c0, cols, inv, M, n0, N, targets, logits, tmax, tsum, tlogit, ld, tld);
 }
 
@@ -1168,8 +1193,11 @@ hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
 hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>((p.cols + 64 * DW - 1) / (64 * DW));
   auto go = [&](auto rt, auto pa, auto stats) {
-    hipLaunchKernelGGL((logits_direct_kernel<decltype(rt)::value, decltype(pa)::value, decltype(stats)::value>),
-                       dim3(grid), dim3(64 * DW), 0, s, p.a, w, p.inv, p.M, p.cols, p.CB * 32, p.n0, p.N,
+    constexpr int RT = decltype(rt)::value, PA = decltype(pa)::value;
+    constexpr bool STATS = decltype(stats)::value;
+    auto* kernel = p.CB % 4 == 0 ? logits_direct_kernel<RT, PA, STATS, false>
+                                 : logits_direct_kernel<RT, PA, STATS, true>;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * DW), 0, s, p.a, w, p.inv, p.M, p.cols, p.CB * 32, p.n0, p.N,
                        p.targets, p.logits, p.tmax, p.tsum, p.tlogit, p.ld, p.tld);
   };
   using std::integral_constant;

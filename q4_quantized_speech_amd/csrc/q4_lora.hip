@@ -142,7 +142,7 @@ __device__ __forceinline__ uint64_t rows_without(const int32_t* __restrict__ ids
 
 // Eight consecutive elements c .. c + 7 of a row of C elements (zeros past
 // its end, or where `live` is false); VEC: C % 8 == 0 and the row is 16-byte
-// aligned.
+// aligned (the model's K; N may be anything).
 template <bool VEC, typename T>
 __device__ __forceinline__ void row8(const T* __restrict__ row, int64_t c, int64_t C, bool live,
                                      float (&v)[8]) {
@@ -160,6 +160,8 @@ __device__ __forceinline__ void row8(const T* __restrict__ row, int64_t c, int64
         load_f32<8>(row + c, v);
       }
     }
+  } else if (live && c + 8 <= C) {
+    load_any_f32<8>(row + c, v);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -453,6 +455,14 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
           }
           store_f32<V>(Y + at + u, v);
         }
+      } else if (n + u + V <= n1) {
+        if (R_) {
+          float q[V];
+          load_any_f32<V>(R_ + at + u, q);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] += q[e];
+        }
+        store_any_f32<V>(Y + at + u, v);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -670,7 +680,7 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
 // vectors: 64 columns c per workgroup, the rows split over its waves.  OT
 // false: out[j][c] (dA), true: out[c][j] (dB).  Rows of other adapters are
 // read as zeros on both sides, so nothing of theirs (infinities, NaN) enters.
-template <typename T, bool OT, int RT, int WAVES, bool VEC>
+template <typename T, bool OT, int RT, int WAVES>
 __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T* __restrict__ Z,
                                            const int32_t* __restrict__ ids, float* __restrict__ out,
                                            const uint16_t* __restrict__ LT3, int64_t MP, int64_t M,
@@ -701,8 +711,8 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
         for (int e = 0; e < 8; ++e) {
           const T* zr = Z + min(m + e, M - 1) * C;
           z[e] = piece{};
-          if constexpr (VEC) {
-            if (((ok >> e) & 1u) && c < C) z[e] = *reinterpret_cast<const piece*>(zr + c);
+          if (c + 4 <= C) {
+            if ((ok >> e) & 1u) z[e] = load_any<4>(zr + c);
           } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -751,13 +761,14 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
           const bool ok = (rows >> (4 * s + g)) & 1u;
           const int64_t m = min(r0 + 16 * q + 4 * s + g, M - 1);
           const T* zr = Z + m * C;
-          if constexpr (VEC) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) z[s][u] = 0.f;
-            if (ok && c < C) load_f32<4>(zr + c, z[s]);
+          for (int u = 0; u < 4; ++u) z[s][u] = 0.f;
+          if (c + 4 <= C) {
+            if (ok) load_any_f32<4>(zr + c, z[s]);
           } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) z[s][u] = ok && c + u < C ? to_f32(zr[c + u]) : 0.f;
+            for (int u = 0; u < 4; ++u)
+              if (ok && c + u < C) z[s][u] = to_f32(zr[c + u]);
           }
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
@@ -806,7 +817,7 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
 // Last launch of the backward pass: workgroups [0, dxblocks) dx, the next
 // adapters * achunks dA, the rest dB.
 constexpr int G_WAVES = 8;
-template <typename T, typename TA, int RT, bool VEC>
+template <typename T, typename TA, int RT>
 __global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_grad_kernel(
     const float* __restrict__ H, const float* __restrict__ G, const uint16_t* __restrict__ HT,
     const uint16_t* __restrict__ GT, int64_t MP, const T* __restrict__ X,
@@ -829,13 +840,13 @@ __global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) vo
     const unsigned b = bid - dxblocks;
     const int a = static_cast<int>(b / achunks);
     const int64_t c0 = static_cast<int64_t>(b - static_cast<unsigned>(a) * achunks) * 64;
-    outer_body<T, false, RT, G_WAVES, true>(G, X, ids, DA + static_cast<int64_t>(a) * R * K, GT, MP,
+    outer_body<T, false, RT, G_WAVES>(G, X, ids, DA + static_cast<int64_t>(a) * R * K, GT, MP,
                                             M, K, R, a, c0, sh.red);
   } else {
     const unsigned b = bid - dxblocks - ablocks;
     const int a = static_cast<int>(b / bchunks);
     const int64_t c0 = static_cast<int64_t>(b - static_cast<unsigned>(a) * bchunks) * 64;
-    outer_body<T, true, RT, G_WAVES, VEC>(H, DY, ids, DB + static_cast<int64_t>(a) * N * R, HT, MP, M,
+    outer_body<T, true, RT, G_WAVES>(H, DY, ids, DB + static_cast<int64_t>(a) * N * R, HT, MP, M,
                                           N, R, a, c0, sh.red);
   }
 }
@@ -918,8 +929,8 @@ hipError_t lora_rt(const LoraArgs& p, int cus) {
   return hipGetLastError();
 }
 
-template <typename T, typename TA, int RT, bool VEC>
-hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
+template <typename T, typename TA, int RT>
+hipError_t lora_grad_rt(const LoraArgs& p, int cus) {
   const int64_t tiles = (p.M + LT - 1) / LT;
   const Split sh = down_split(p.M, p.K, p.adapters, cus), sg = down_split(p.M, p.N, p.adapters, cus);
   const int64_t MR = p.M * p.R;
@@ -935,7 +946,9 @@ hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
   const unsigned gb = need_g ? static_cast<unsigned>(tiles * sg.n) : 0u;
   const unsigned gy = group_blocks(p.M, p.adapters);
   const int R = static_cast<int>(p.R), adapters = static_cast<int>(p.adapters);
-  hipLaunchKernelGGL((lora_down2_kernel<T, TA, RT, VEC>), dim3(hb + gb, gy), dim3(64 * DOWN_WAVES),
+  // N is a multiple of 8: dy's rows are whole 16-byte pieces
+  auto* down2 = p.N % 8 == 0 ? lora_down2_kernel<T, TA, RT, true> : lora_down2_kernel<T, TA, RT, false>;
+  hipLaunchKernelGGL(down2, dim3(hb + gb, gy), dim3(64 * DOWN_WAVES),
                      0, p.stream, static_cast<const T*>(p.x), static_cast<const T*>(p.dy),
                      static_cast<const TA*>(p.a), static_cast<const TA*>(p.b), p.ids, PH, PG, p.M,
                      p.N, p.K, R, adapters, sh.n, sh.span, sg.n, sg.span, hb);
@@ -953,7 +966,7 @@ hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
   const unsigned dxb = p.y ? static_cast<unsigned>(tiles * chunks * gy) : 0u;
   const unsigned ab = p.da ? static_cast<unsigned>(p.adapters * achunks) : 0u;
   const unsigned bb = p.db ? static_cast<unsigned>(p.adapters * bchunks) : 0u;
-  hipLaunchKernelGGL((lora_grad_kernel<T, TA, RT, VEC>), dim3(dxb + ab + bb), dim3(64 * G_WAVES), 0,
+  hipLaunchKernelGGL((lora_grad_kernel<T, TA, RT>), dim3(dxb + ab + bb), dim3(64 * G_WAVES), 0,
                      p.stream, H, G, HT, GT, MP, static_cast<const T*>(p.x), static_cast<const T*>(p.dy),
                      static_cast<const TA*>(p.a), p.ids, static_cast<const T*>(p.r),
                      static_cast<T*>(p.y), p.da, p.db, p.M, p.N, p.K, R, adapters, chunks,
@@ -964,11 +977,10 @@ hipError_t lora_grad_vec(const LoraArgs& p, int cus) {
 template <typename T, typename TA>
 hipError_t lora_types(const LoraArgs& p, int cus) {
   if (p.grad) {
-    const bool vec = p.N % 8 == 0;
-    if (p.R <= 16) return vec ? lora_grad_vec<T, TA, 1, true>(p, cus) : lora_grad_vec<T, TA, 1, false>(p, cus);
-    if (p.R <= 32) return vec ? lora_grad_vec<T, TA, 2, true>(p, cus) : lora_grad_vec<T, TA, 2, false>(p, cus);
-    if (p.R <= 64) return vec ? lora_grad_vec<T, TA, 4, true>(p, cus) : lora_grad_vec<T, TA, 4, false>(p, cus);
-    return vec ? lora_grad_vec<T, TA, 8, true>(p, cus) : lora_grad_vec<T, TA, 8, false>(p, cus);
+    if (p.R <= 16) return lora_grad_rt<T, TA, 1>(p, cus);
+    if (p.R <= 32) return lora_grad_rt<T, TA, 2>(p, cus);
+    if (p.R <= 64) return lora_grad_rt<T, TA, 4>(p, cus);
+    return lora_grad_rt<T, TA, 8>(p, cus);
   }
   if (p.R <= 16) return lora_rt<T, TA, 1>(p, cus);
   if (p.R <= 32) return lora_rt<T, TA, 2>(p, cus);

@@ -29,6 +29,22 @@ __device__ __forceinline__ void load_f32(const T* p, float (&v)[V]) {
   for (int i = 0; i < V; ++i) v[i] = to_f32(static_cast<T>(a[i]));
 }
 
+// V consecutive elements at any element address (the hardware takes vector
+// accesses of any alignment in global memory).
+template <int V, typename T>
+__device__ __forceinline__ auto load_any(const T* p) {
+  typedef T vec __attribute__((ext_vector_type(V)));
+  typedef T loose __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+  const loose a = *reinterpret_cast<const loose*>(p);
+  return static_cast<vec>(a);
+}
+template <int V, typename T>
+__device__ __forceinline__ void load_any_f32(const T* p, float (&v)[V]) {
+  const auto a = load_any<V>(p);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = to_f32(static_cast<T>(a[i]));
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float v) {
   return static_cast<T>(v);
@@ -42,6 +58,16 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) a[i] = from_f32<T>(v[i]);
   *reinterpret_cast<vec*>(p) = a;
+}
+
+// ... to any element address.
+template <int V, typename T>
+__device__ __forceinline__ void store_any_f32(T* p, const float (&v)[V]) {
+  typedef T loose __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+  loose a;
+#pragma unroll
+  for (int i = 0; i < V; ++i) a[i] = from_f32<T>(v[i]);
+  *reinterpret_cast<loose*>(p) = a;
 }
 
 }  // namespace q4

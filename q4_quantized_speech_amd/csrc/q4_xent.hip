@@ -16,7 +16,7 @@
 // small gradient and loss.
 //
 // Up to 64 rows read the table at its Q4_0 size instead, for the logits and for
-// the gradient (K % 128 == 0); up to four rows without a gradient go through
+// the gradient (K % 64 == 0); up to four rows without a gradient go through
 // the matvec-accuracy kernels.
 
 #include <algorithm>
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
 // Rows whose loss alone goes through the matvec-accuracy kernels, four at a
 // time: where the direct kernel does not serve K, a table read per four rows
 // still beats unpacking it (measured up to 16).
-int64_t few_rows(int64_t K) { return K % 128 == 0 ? 4 : 16; }
+int64_t few_rows(int64_t K) { return K % 64 == 0 ? 4 : 16; }
 
 struct XentPlan {
   bool few, direct;
@@ -300,7 +300,7 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus
   XentPlan p = {};
   Carver c;
   p.few = !grad && M <= few_rows(K);
-  p.direct = !p.few && M <= DIRECT_ROWS && K % 128 == 0;
+  p.direct = !p.few && M <= DIRECT_ROWS && K % 64 == 0;
   p.run_max = c.take(M * 4);
   p.run_sum = c.take(M * 4);
   p.tlogit = c.take(M * 4);

@@ -202,9 +202,9 @@ def test_xent_shapes(m, n, k, dtype):
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("m,n,k", [(1, 31, 128), (5, 300, 128), (15, 513, 256), (16, 512, 384), (17, 1025, 128),
                                    (32, 700, 640), (33, 2000, 256), (48, 511, 128), (49, 65, 256), (64, 3000, 384),
-                                   (65, 600, 128)])
+                                   (65, 600, 128), (7, 100, 64), (40, 900, 192), (64, 129, 320), (20, 1300, 448)])
 def test_xent_few_rows(m, n, k, dtype):
-    """Up to 64 rows with K a multiple of 128: straight from the Q4_0 bytes; one row more."""
+    """Up to 64 rows with K a multiple of 64: straight from the Q4_0 bytes; one row more."""
     xent_case(m, n, k, dtype, 4700 + m + n, targets=ODD if m > 5 else None)
     xent_case(m, n, k, dtype, 4800 + m + n, grad=False, targets=ODD if m > 5 else None)
 
