@@ -318,7 +318,7 @@ q4_status q4_quantize(const float* w, void* w_q4, int64_t N, int64_t K,
  * Q4_TYPE_F16 or Q4_TYPE_BF16; the adapters' type is that one, or
  * Q4_TYPE_F32, or, with float32 activations, any of the three
  * (Q4_ERR_FORMAT otherwise).  Sums are float32 whatever the types, and each
- * output is rounded once.
+ * output is rounded once.  An output overlaps no input unless it is said so.
  */
 enum { Q4_TYPE_F32 = 0, Q4_TYPE_F16 = 1, Q4_TYPE_BF16 = 30 };
 
@@ -365,7 +365,9 @@ q4_status q4_matmul_dx(const void* w_q4, const void* dy, void* dx, int32_t type,
  * target is taken as the sum of the others, so small losses and gradients
  * keep their relative precision.  For float16 and bfloat16 the gradient's
  * probabilities and weights are rounded to binary16 (float32 keeps two parts
- * of each).  Deterministic.
+ * of each; |deq(T)| must stay below 65504 for dx).  Deterministic; a row that
+ * holds an infinity or NaN gives non-finite values in that row only, and
+ * loss 0 and dx 0 if it is padding.
  */
 size_t q4_lmhead_xent_workspace_bytes(int32_t type, int32_t grad, int64_t M, int64_t N,
                                       int64_t K);
@@ -388,8 +390,11 @@ q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets
  *   4194304, R a multiple of 8 from 8 to 128, 1 <= adapters <= 65535.
  *   workspace : q4_lora_workspace_bytes(M, N, K, R) bytes of device scratch;
  *           its contents do not matter.  Calls that share it must be ordered.
- * Two launches; A_a x is kept in float32.  Deterministic; the order of a row's
- * float32 sums depends on the sizes and on how many rows share its adapter.
+ * Two launches, three for more than 256 rows; A_a x is kept in float32.
+ * Deterministic; the order of a row's float32 sums depends on the sizes and on
+ * how many rows share its adapter.  An infinity or NaN in a row gives
+ * non-finite values in that row only (an infinity may come out as NaN); the
+ * rows of other adapters do not see an adapter's.
  */
 size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 q4_status q4_lora(const void* x, const void* a, const void* b, const float* scale,
@@ -408,7 +413,8 @@ q4_status q4_lora(const void* x, const void* a, const void* b, const float* scal
  *   da, db: [adapters, R, K] and [adapters, N, R] float32, written (not
  *           accumulated; zeros for an adapter without rows), or NULL.  At
  *           least one of dx, da, db is given.
- *   Rows without an adapter: dx = r, nothing to da and db.  s_a is a constant.
+ *   Rows without an adapter: dx = r, nothing to da and db, whatever they hold.
+ *   s_a is a constant.
  *   Ranges as for q4_lora, and adapters * (ceil(K/64) + ceil(N/64)) <= 2^21.
  * Three launches.  Deterministic.
  */

@@ -282,10 +282,16 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
   }
 }
 
-// Rows whose loss alone goes through the matvec-accuracy kernels, four at a
-// time: where the direct kernel does not serve K, a table read per four rows
-// still beats unpacking it (measured up to 16).
-int64_t few_rows(int64_t K) { return K % 64 == 0 ? 4 : 16; }
+// Losses alone (no gradient) that go through the matvec-accuracy kernels, four
+// rows at a time, instead of the matrix cores.  K % 64 == 0: up to four rows
+// (51 us against the direct kernel's 60 for one row of 262144 x 1280).
+// Otherwise the table would have to be unpacked: 1184 columns, one row of
+// 65392 take 53 us against 105, 14 rows of 2000 35 against 41, but 14 rows of
+// 65392 573 against 108.
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+  if (K % 64 == 0) return M <= 4;
+  return M == 1 || (M <= 16 && M * N * K <= int64_t(1) << 25);
+}
 
 struct XentPlan {
   bool few, direct;
@@ -299,7 +305,7 @@ struct XentPlan {
 XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus) {
   XentPlan p = {};
   Carver c;
-  p.few = !grad && M <= few_rows(K);
+  p.few = !grad && few_rows(M, N, K);
   p.direct = !p.few && M <= DIRECT_ROWS && K % 64 == 0;
   p.run_max = c.take(M * 4);
   p.run_sum = c.take(M * 4);
