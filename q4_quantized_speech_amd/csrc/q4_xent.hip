@@ -16,8 +16,8 @@
 // small gradient and loss.
 //
 // Up to 64 rows read the table at its Q4_0 size instead, for the logits and for
-// the gradient (K % 64 == 0); up to four rows without a gradient go through
-// the matvec-accuracy kernels.
+// the gradient (K % 64 == 0); a few rows without a gradient go through the
+// matvec-accuracy kernels.
 
 #include <algorithm>
 
@@ -284,12 +284,15 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
 
 // Losses alone (no gradient) that go through the matvec-accuracy kernels, four
 // rows at a time, instead of the matrix cores.  K % 64 == 0: up to four rows
-// (51 us against the direct kernel's 60 for one row of 262144 x 1280).
-// Otherwise the table would have to be unpacked: 1184 columns, one row of
-// 65392 take 53 us against 105, 14 rows of 2000 35 against 41, but 14 rows of
-// 65392 573 against 108.
+// (131072 x 3072, one row: 49 us against the direct kernel's 69, four 57
+// against 71), and up to 16 of a table that gives few of the direct kernel's
+// 512-row workgroups long rows to walk (16 rows of 8192 x 3072: 43 against 57;
+// of 8192 x 1280 34 against 32).  Otherwise the table would
+// have to be unpacked: one row of 65392 x 1248 takes 55 us against 109, eight
+// of 2000 24 against 40; from two rows on, 65392 take 110 either way, and more
+// here at five.
 bool few_rows(int64_t M, int64_t N, int64_t K) {
-  if (K % 64 == 0) return M <= 4;
+  if (K % 64 == 0) return M <= (N <= 16384 && K >= 2048 ? 16 : 4);
   return M == 1 || (M <= 16 && M * N * K <= int64_t(1) << 25);
 }
 

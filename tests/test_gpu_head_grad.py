@@ -352,3 +352,21 @@ def test_training_step():
     assert float((loss.double() - loss6).abs().max()) <= 2e-3 * float(y6.detach().abs().max())
     for got, want in ((dx, x6.grad), (da, a6.grad), (db, b6.grad)):
         assert float((got.double() - want).norm() / want.norm()) <= 2e-3
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_xent_pieces_unpacked(dtype):
+    """Several pieces of an unpacked table: more than 64 rows, and K an odd multiple of 32."""
+    for m, n, k in ((70, 40001, 64), (20, 70000, 96)):
+        t = [0, n - 1, 32767, 32768, n // 2, -1]
+        xent_case(m, n, k, dtype, 5300 + n, ramp=True, targets=t)
+        xent_case(m, n, k, dtype, 5300 + n, ramp=True, targets=t, grad=False)
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 1000, 2048), (5, 1000, 2048), (16, 16384, 2112), (16, 16385, 2048),
+                                   (17, 500, 2048), (16, 300, 1984), (1, 40000, 96), (2, 40000, 96),
+                                   (16, 21845, 96), (16, 21846, 96)])
+def test_xent_loss_routes(m, n, k):
+    """Losses alone on both sides of the sizes that choose between the kernels."""
+    for dtype in (F32, BF16):
+        xent_case(m, n, k, dtype, 5400 + m, grad=False, targets=ODD if m > 5 else None)
