@@ -84,8 +84,7 @@ hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s);
 
 // part[slice][m][k] (alpha as above), or with splits == 1 and part null out[m][k]
 // = inv[m] * the sum rounded once to `type`: sum over n of G[m, n] deq(W)[n, k]
-// for the weight rows [n0, min(N, n0 + 32 CB)), read as Q4_0 (K % 64 == 0:
-// rows start on a dword).
+// for the weight rows [n0, min(N, n0 + 32 CB)), read as Q4_0 (n0 even).
 struct TransposedGemm {
   const f16x8* g;
   int pa, pb, type;
@@ -113,7 +112,7 @@ struct LogitGemm {
   const f16x8 *a, *q;
   int pa;
   const float *scale, *inv;
-  int64_t M, cols, CB;
+  int64_t M, cols, K, CB;
   int64_t n0, N;
   const int32_t* targets;
   float *logits, *tmax, *tsum, *tlogit;
@@ -121,8 +120,8 @@ struct LogitGemm {
 };
 hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s);
 
-// The same for up to 64 rows with K = 32 CB a multiple of 64, straight from the
-// Q4_0 bytes (q and scale unused).
+// The same for up to 64 rows, straight from the Q4_0 bytes (q and scale unused;
+// n0 even).
 constexpr int64_t DIRECT_ROWS = 64;
 hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_t s);
 

@@ -204,78 +204,69 @@ __global__ __launch_bounds__(256) void prep_codes_kernel(const uint8_t* __restri
   scale[f * 16 + i] = half_bits_to_float(d);
 }
 
-// Any K (the kernel below takes K % 64 == 0).  One thread per (32-row block, group of 8 rows, block of 32 weights, code
-// dword): eight rows' dwords hold eight columns, whose operands are written
-// with the eight rows as the reduction.
-template <int PARTS>
-__global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __restrict__ W,
-                                                             int64_t n0, int64_t N, int64_t kblocks,
-                                                             int64_t NB, f16x8* __restrict__ tfrag) {
-  const int j = threadIdx.x & 3, g = (threadIdx.x >> 2) & 3;
-  const int64_t kb = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
-  if (kb >= kblocks) return;
-  const int64_t nb = blockIdx.x;
-  uint32_t qs[8];
-  float d[8];
+// A wave's 32 rows x 72 bytes (128 columns from column 128 kt, first row even)
+// to its own LDS, as consecutive dwords.  ODD: K is an odd multiple of 32, so a
+// row's bytes are an odd number of half dwords and odd rows start in the middle
+// of one: a row takes 19 dwords from the one it starts in, its bytes at 0 (even
+// rows) or 2 (odd).  An even last row of the table ends in the middle of a
+// dword, which is not loaded but put there by last_codes.
+template <bool ODD>
+struct Raw {
+  static constexpr int ROW = ODD ? 19 : 18;    // dwords of a row
+  static constexpr int LOADS = ODD ? 10 : 9;   // per lane
+  static constexpr int SIZE = ODD ? 640 : 592;  // with what the last row's pair of reads touches
+  static __device__ __forceinline__ int most(int rb, int kt) {  // a row's last dword
+    return (ODD ? rb + 2 : rb) / 4 - 1 - kt * 18;
+  }
+  // Byte offsets of this lane's dwords from the first row, `left` of the table
+  // (at most 32) from there on.  Rows past them repeat the last one, dwords past
+  // the row (rb bytes) its last.
+  static __device__ __forceinline__ void offsets(int left, int rb, int kt, uint32_t (&off)[LOADS]) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // nothing of this is kept in registers for the last block
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int64_t n = n0 + nb * 32 + 8 * g + r;
-    qs[r] = 0;
-    d[r] = 0.f;
-    if (n < N) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(W + (n * kblocks + kb) * BLOCK_BYTES);
-      d[r] = half_bits_to_float(p[0]);
-      qs[r] = p[1 + 2 * j] | (static_cast<uint32_t>(p[2 + 2 * j]) << 16);
+    for (int u = 0; u < LOADS; ++u) {
+      const int e = u * 64 + lane;
+      const int row = min(e / ROW, left - 1);
+      const bool cut = ODD && (left & 1) && row + 1 == left;
+      const int at = min(e % ROW, most(rb, kt) - (cut ? 1 : 0));
+      off[u] = static_cast<uint32_t>(row * rb - (ODD ? 2 * (row & 1) : 0) + at * 4);
     }
   }
-  const int64_t part = kblocks * 2 * NB * 64;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {  // codes 0-3: low nibbles, columns 4 j + c; 4-7: high, 16 + ...
-    f16x8 hi, lo;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const uint32_t q = (qs[r] >> (8 * (c & 3) + 4 * (c >> 2))) & 15u;
-      const float w = (static_cast<float>(q) - 8.f) * d[r];
-      hi[r] = static_cast<_Float16>(w);
-      // w has at most 15 significant bits and is a multiple of 2^-24 like
-      // its scale, so the rest fits binary16 exactly
-      if constexpr (PARTS == 2) lo[r] = static_cast<_Float16>(w - static_cast<float>(hi[r]));
+  // The table's last two bytes, where its last row is one of these and even
+  // (after the loads have arrived, by the wave that reads them).
+  static __device__ __forceinline__ void last_codes(const uint8_t* __restrict__ W, int64_t N,
+                                                    int left, int rb, int kt, uint32_t* raw) {
+    if constexpr (ODD) {
+      const int at = most(rb, kt);
+      if ((left & 1) && at < 18) {
+        if ((threadIdx.x & 63) == 0)
+          raw[(left - 1) * ROW + at] = *reinterpret_cast<const uint16_t*>(W + N * rb - 2);
+        issued();
+      }
     }
-    const int64_t at = ((2 * kb + (c >> 2)) * NB + nb) * 64 + 4 * j + (c & 3) + 16 * g;
-    tfrag[at] = hi;
-    if constexpr (PARTS == 2) tfrag[part + at] = lo;
   }
-}
-
-// A wave's 32 rows x 72 bytes (128 columns from column 128 kt) to its own LDS,
-// as consecutive dwords: byte offsets of this lane's nine from the first row.
-// Rows past `rows` repeat the last one, dwords past the row (rb bytes) its last.
-__device__ __forceinline__ void raw_offsets(int64_t rows, int64_t rb, int kt, uint32_t (&off)[9]) {
-  const int lane = threadIdx.x & 63;
-  const int64_t most = rb / 4 - 1 - kt * 18;
-#pragma unroll
-  for (int u = 0; u < 9; ++u) {
-    const int e = u * 64 + lane;
-    off[u] = static_cast<uint32_t>(min<int64_t>(e / 18, rows - 1) * rb + min<int64_t>(e % 18, most) * 4);
-  }
-}
-constexpr int RAW = 32 * 18 + 16;  // dwords of it, and what the last row's pair of reads touches
+};
 
 // Lane (i, g): dword i % 4 of the codes of block i / 4 and that block's scale
 // in rows 8 g .. 8 g + 7.  A block starts at byte 18 (i / 4) of a row: its
 // scale in either half of a dword, its codes from the next half on.
+template <bool ODD>
 struct RawCodes {
   uint32_t q[8];
   f16x2 d[4];
-  __device__ __forceinline__ explicit RawCodes(const uint32_t* raw) {
+  // `live` rows (ODD: the scales of those past them, which may be any bytes,
+  // are zero).
+  __device__ __forceinline__ RawCodes(const uint32_t* raw, int live) {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const int first = 18 * (i >> 2), code = first + 2 + 4 * (i & 3);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const uint32_t* p = raw + (8 * g + r) * 18;
+      const int first = 18 * (i >> 2) + (ODD ? 2 * (r & 1) : 0), code = first + 2 + 4 * (i & 3);
+      const uint32_t* p = raw + (8 * g + r) * Raw<ODD>::ROW;
       const uint32_t* c = p + (code >> 2);
       q[r] = __builtin_amdgcn_alignbit(c[1], c[0], 8 * (code & 2));
-      d[r >> 1][r & 1] = reinterpret_cast<const _Float16*>(p)[first >> 1];
+      const _Float16 v = reinterpret_cast<const _Float16*>(p)[first >> 1];
+      d[r >> 1][r & 1] = !ODD || 8 * g + r < live ? v : static_cast<_Float16>(0.f);
     }
   }
   // Low (h = 0) or high codes of every byte.
@@ -307,15 +298,17 @@ struct RawCodes {
   }
 };
 
-// K % 64 == 0: a wave takes 32 rows x 128 columns, turned in registers, put
-// together in LDS and written as whole fragments (16-byte pieces 64 bytes
-// apart, as above, take 1.9 times as long on 32768 rows of 3072).
-template <int PARTS>
-__global__ __launch_bounds__(256) void prep_transpose64_kernel(const uint8_t* __restrict__ W,
+// The transposed weights: a wave takes 32 rows x 128 columns, turned in
+// registers, put together in LDS and written as whole fragments (one thread
+// per dword, its 16-byte pieces 64 bytes apart, takes 1.9 times as long on
+// 32768 rows of 3072).
+template <int PARTS, bool ODD>
+__global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __restrict__ W,
                                                                int64_t n0, int64_t N, int64_t K,
                                                                int64_t NB, int ktiles,
                                                                f16x8* __restrict__ tfrag) {
-  __shared__ uint32_t raw[4][RAW];
+  using R = Raw<ODD>;
+  __shared__ uint32_t raw[4][R::SIZE];
   __shared__ f16x8 tile[4][8][64];  // [wave][fragment][swizzled lane]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -325,14 +318,17 @@ __global__ __launch_bounds__(256) void prep_transpose64_kernel(const uint8_t* __
   const int kt = static_cast<int>(item - nb * ktiles);
   if (nb >= NB) return;
   const int64_t rb = K / 32 * BLOCK_BYTES, n = n0 + nb * 32;
-  const int64_t rows = max<int64_t>(1, min<int64_t>(32, N - n));
-  uint32_t off[9];
-  raw_offsets(rows, rb, kt, off);
-  const uint8_t* base = W + min(n, N - 1) * rb + static_cast<int64_t>(kt) * 72;
+  // a block past the matrix (its weights are zero) loads its last even row
+  const int64_t from = min(n, (N - 1) & ~int64_t(1));
+  const int left = static_cast<int>(min<int64_t>(32, N - from)), row_bytes = static_cast<int>(rb);
+  uint32_t off[R::LOADS];
+  R::offsets(left, row_bytes, kt, off);
+  const uint8_t* base = W + from * rb + static_cast<int64_t>(kt) * 72;
 #pragma unroll
-  for (int u = 0; u < 9; ++u) to_lds<4>(base + off[u], raw[wave] + u * 64);
+  for (int u = 0; u < R::LOADS; ++u) to_lds<4>(base + off[u], raw[wave] + u * 64);
   arrived();
-  RawCodes codes(raw[wave]);
+  R::last_codes(W, N, left, row_bytes, kt, raw[wave]);
+  RawCodes<ODD> codes(raw[wave], 32);
   // rows past the matrix: weights of zero
 #pragma unroll
   for (int r = 0; r < 8; ++r)
@@ -347,7 +343,7 @@ __global__ __launch_bounds__(256) void prep_transpose64_kernel(const uint8_t* __
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         f16x8 hi, lo;
-        codes.column<PARTS>(nib, b, hi, lo);
+        codes.template column<PARTS>(nib, b, hi, lo);
         // fragment 2 (i / 4) + h, its lane 4 (i % 4) + b + 16 g; the low bits
         // are mixed with g so that the lanes of a store spread over the banks
         tile[wave][2 * (i >> 2) + h][4 * (i & 3) + (b ^ g) + 16 * g] = p ? lo : hi;
@@ -701,12 +697,15 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
 // row) and the rows' fragments go to LDS by DMA while the previous chunk is
 // multiplied.  A lane (i, g) of a wave reads dword g of a block's codes of
 // weight row i: the operand of the exact codes q - 8, the block scale applied
-// to the product (as in gemm_logits_kernel).  K % 64 == 0 (rows start on a
-// dword).
+// to the product (as in gemm_logits_kernel).
+//
+// ANY: K is no multiple of 128.  A row takes 19 dwords from the one it starts
+// in: with K an odd multiple of 32, odd rows start in the middle of it.  The
+// last chunk has one to three blocks; the scales of the others are zero.
 // ---------------------------------------------------------------------------
 constexpr int DW = 8;  // waves
 
-template <int RT, int PA, bool STATS, bool HALF>
+template <int RT, int PA, bool STATS, bool ANY>
 __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict__ W,
                           const float* __restrict__ inv, int64_t M, int64_t cols, int64_t K,
@@ -715,33 +714,41 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
                           float* __restrict__ tsum, float* __restrict__ tlogit, int64_t ld,
                           int64_t tld) {
   constexpr int FA = RT * PA * 4, PER = (FA + DW - 1) / DW;  // fragments of a chunk, per wave
+  constexpr int ROW = ANY ? 19 : 18;                         // dwords of a row in LDS
   __shared__ f16x8 a0[FA][64], a1[FA][64];                   // [part][row tile][block]
-  __shared__ uint32_t raw0[DW][64 * 18], raw1[DW][64 * 18];
+  __shared__ uint32_t raw0[DW][64 * ROW], raw1[DW][64 * ROW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int64_t rb = K / 32 * BLOCK_BYTES, CB = K / 32, rta = (M + 15) / 16;
+  const int64_t AB = (CB + 1) / 2 * 2;  // blocks of a row of A (blocks32)
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (64 * DW) + 64 * wave;
 
-  // this lane's 18 dwords of the wave's 64 rows; rows past the matrix repeat
-  // its last one (their logits are dropped)
+  // this lane's dwords of the wave's 64 rows; rows past the matrix repeat its
+  // last one (their logits are dropped)
+  auto start = [&](int64_t row) { return row * rb & ~int64_t(3); };
   const int64_t row0 = min(n0 + c0, N - 1);
-  const uint8_t* base = W + row0 * rb;
-  uint32_t off[18];
+  const uint8_t* base = W + start(row0);
+  uint32_t off[ROW];
 #pragma unroll
-  for (int u = 0; u < 18; ++u) {
+  for (int u = 0; u < ROW; ++u) {
     const int e = u * 64 + lane;
-    off[u] = static_cast<uint32_t>((min(n0 + c0 + e / 18, N - 1) - row0) * rb + e % 18 * 4);
+    off[u] = static_cast<uint32_t>(start(min(n0 + c0 + e / ROW, N - 1)) - start(row0) + e % ROW * 4);
   }
-  const int64_t chunks = (K + (HALF ? 127 : 0)) / 128;
+  // the last dword of a row that lies in the table
+  auto most = [&](int64_t row) { return ((min((row + 1) * rb + 3, N * rb) - start(row)) >> 2) - 1; };
+  const int64_t chunks = (CB + 3) / 4;
   auto issue = [&](f16x8 (*a)[64], uint32_t* raw, int64_t chunk) {
-    // HALF, K % 128 == 64: the last chunk is half one; the second half's places are
-    // filled with its first again, and not used
-    const bool half = HALF && (chunk + 1) * 128 > K;
+    if (ANY && chunk == chunks - 1) {
 #pragma unroll
-    for (int u = 0; u < 18; ++u) {
-      const uint32_t back = half && (u * 64 + lane) % 18 >= 9 ? 36u : 0u;
-      to_lds<4>(base + chunk * 72 + off[u] - back, raw + u * 64);
+      for (int u = 0; u < ROW; ++u) {
+        const int e = u * 64 + lane;
+        const int64_t over = chunk * 18 + e % ROW - most(min(n0 + c0 + e / ROW, N - 1));
+        to_lds<4>(base + chunk * 72 + off[u] - 4 * max<int64_t>(0, over), raw + u * 64);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < ROW; ++u) to_lds<4>(base + chunk * 72 + off[u], raw + u * 64);
     }
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
@@ -749,8 +756,19 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
       if (FA % DW != 0 && f >= FA) break;  // wave-uniform
       const int p = f / (RT * 4), t = f / 4 % RT, b = f % 4;
       const int64_t rt = min<int64_t>(t, rta - 1);
-      to_lds<16>(A + ((p * rta + rt) * CB + (HALF ? min(chunk * 4 + b, CB - 1) : chunk * 4 + b)) * 64 + lane, &a[f][0]);
+      const int64_t block = ANY ? min(chunk * 4 + b, CB - 1) : chunk * 4 + b;
+      to_lds<16>(A + ((p * rta + rt) * AB + block) * 64 + lane, &a[f][0]);
     }
+    issued();
+  };
+  // the last chunk's bytes, once they have arrived: a lane per row
+  auto finish = [&](uint32_t* raw) {
+    const int64_t n = n0 + c0 + lane;
+    uint16_t* h = reinterpret_cast<uint16_t*>(raw + lane * ROW) + (CB & lane & 1);
+    for (int b = static_cast<int>(CB % 4); b < 4; ++b) h[9 * b] = 0;
+    // an even last row of the table may end in the middle of a dword
+    if (n == N - 1 && (N * rb & 3) != 0)
+      raw[lane * ROW + most(n) + 1 - (chunks - 1) * 18] = *reinterpret_cast<const uint16_t*>(W + N * rb - 2);
     issued();
   };
 
@@ -763,18 +781,26 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
   // 16 steps: block b = s / 4, weight rows 16 j .. of j = s % 4; a step's
   // codes are read one step ahead, and its scaled sums are taken while the
   // next step's products run
-  auto compute = [&](auto steps, const f16x8 (*a)[64], const uint32_t* raw) {
-    constexpr int STEPS = decltype(steps)::value;
+  const int odd = static_cast<int>(CB & i & 1);  // ANY: this lane's rows start at byte 2
+  const int at0 = i * ROW + g;
+  auto compute = [&](const f16x8 (*a)[64], const uint32_t* raw) {
     uint32_t lo[2], hi[2];
     uint32_t dw[3];
     f16x8 x[RT][PA];
     f32x4 t[2][RT];
     auto codes = [&](int s) {
       const int b = s / 4, j = s % 4, at = 18 * b + 2;  // byte of the block's codes in a row
-      const uint32_t* p = raw + (16 * j + i) * 18;
-      lo[s & 1] = p[at / 4 + g];
-      if (at & 2) hi[s & 1] = p[at / 4 + g + 1];
-      dw[s % 3] = p[18 * b / 4];
+      const uint32_t* p = raw + 16 * j * ROW + at0 + at / 4;
+      if constexpr (ANY) {
+        if (at & 2) p += odd;
+        lo[s & 1] = p[0];
+        hi[s & 1] = p[1];
+        dw[s % 3] = reinterpret_cast<const uint16_t*>(raw + 16 * j * ROW + i * ROW)[9 * b + odd];
+      } else {
+        lo[s & 1] = p[0];
+        if (at & 2) hi[s & 1] = p[1];
+        dw[s % 3] = raw[(16 * j + i) * ROW + 18 * b / 4];
+      }
     };
     auto acts = [&](int b) {
 #pragma unroll
@@ -784,7 +810,8 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
     };
     auto products = [&](int s) {
       const int b = s / 4, at = 18 * b + 2;
-      const f16x8 q = codes8(at & 2 ? shift16(hi[s & 1], lo[s & 1]) : lo[s & 1]);
+      const f16x8 q = codes8(ANY ? __builtin_amdgcn_alignbit(hi[s & 1], lo[s & 1], at & 2 ? 16 - 16 * odd : 16 * odd)
+                             : at & 2 ? shift16(hi[s & 1], lo[s & 1]) : lo[s & 1]);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
@@ -798,14 +825,14 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
     codes(1);
     products(0);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      if (s + 2 < STEPS) codes(s + 2);
-      if (s + 1 < STEPS) {
+    for (int s = 0; s < 16; ++s) {
+      if (s + 2 < 16) codes(s + 2);
+      if (s + 1 < 16) {
         if ((s + 1) % 4 == 0) acts((s + 1) / 4);
         products(s + 1);
       }
       const int b = s / 4, j = s % 4;
-      const float d = half_bits_to_float((18 * b) & 2 ? dw[s % 3] >> 16 : dw[s % 3] & 0xFFFFu);
+      const float d = half_bits_to_float(ANY ? dw[s % 3] : (18 * b) & 2 ? dw[s % 3] >> 16 : dw[s % 3] & 0xFFFFu);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         acc[r][j].x = __builtin_fmaf(d, t[s & 1][r].x, acc[r][j].x);
@@ -816,33 +843,24 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
       }
     }
   };
-  const std::integral_constant<int, 16> whole;
-  const std::integral_constant<int, 8> halved;
-  const int64_t full = K / 128;
   issue(a0, raw0[wave], 0);
   arrived();
   __syncthreads();
   int64_t c = 0;
-  for (; c + 2 <= full; c += 2) {
+  for (; c + 2 <= chunks; c += 2) {
     issue(a1, raw1[wave], c + 1);
-    compute(whole, a0, raw0[wave]);
+    compute(a0, raw0[wave]);
     arrived();
     __syncthreads();
     if (c + 2 < chunks) issue(a0, raw0[wave], c + 2);
-    compute(whole, a1, raw1[wave]);
+    if (ANY && c + 2 == chunks) finish(raw1[wave]);
+    compute(a1, raw1[wave]);
     arrived();
     __syncthreads();
   }
-  if (c < full) {
-    if constexpr (HALF) issue(a1, raw1[wave], c + 1);
-    compute(whole, a0, raw0[wave]);
-    if constexpr (HALF) {
-      arrived();
-      __syncthreads();
-      compute(halved, a1, raw1[wave]);
-    }
-  } else if constexpr (HALF) {
-    compute(halved, a0, raw0[wave]);
+  if (c < chunks) {
+    if constexpr (ANY) finish(raw0[wave]);
+    compute(a0, raw0[wave]);
   }
   logits_out<STATS>(acc, 0, c0, cols, inv, M, n0, N, targets, logits, tmax, tsum, tlogit, ld, tld);
 }
@@ -866,7 +884,7 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 // ---------------------------------------------------------------------------
 constexpr int TW = 8;  // waves
 
-template <int RT, int PA, int PB, typename T>
+template <int RT, int PA, int PB, typename T, bool ODD>
 __global__ __launch_bounds__(64 * TW) __attribute__((amdgpu_waves_per_eu(2, RT <= 1 ? 4 : 2)))
 void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restrict__ W, int64_t n0,
                             int64_t N, int64_t M, int64_t K, int64_t CB, int mtiles, int tiles,
@@ -875,7 +893,8 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
   constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time
   __shared__ f32x4 red[4][RP * 8][64];
   // two arrays: reading one does not have to wait for loads into the other
-  __shared__ uint32_t raw0[TW][RAW], raw1[TW][RAW];
+  using R = Raw<ODD>;
+  __shared__ uint32_t raw0[TW][R::SIZE], raw1[TW][R::SIZE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -888,17 +907,19 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
 
   // rows past the matrix repeat its last one (G is zero there), columns past it
   // its last dword (their results are dropped)
-  uint32_t off[9];
-  raw_offsets(min<int64_t>(32, N - n0), rb, kt, off);
+  uint32_t off[R::LOADS];
+  const int row_bytes = static_cast<int>(rb);
+  auto left = [&](int64_t nb) { return static_cast<int>(min<int64_t>(32, N - n0 - nb * 32)); };
+  R::offsets(left(0), row_bytes, kt, off);
 
   struct Acts {
     f16x8 a[RT][PA];
   };
   auto load = [&](int64_t nb, uint32_t* raw, Acts& x) {
-    if (n0 + nb * 32 + 32 > N) raw_offsets(N - n0 - nb * 32, rb, kt, off);  // the last, partial block
+    if (left(nb) < 32) R::offsets(left(nb), row_bytes, kt, off);  // the last, partial block
     const uint8_t* base = W + (n0 + nb * 32) * rb + static_cast<int64_t>(kt) * 72;
 #pragma unroll
-    for (int u = 0; u < 9; ++u) to_lds<4>(base + off[u], raw + u * 64);
+    for (int u = 0; u < R::LOADS; ++u) to_lds<4>(base + off[u], raw + u * 64);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -915,8 +936,9 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const uint32_t* raw, const Acts& x) {
-    const RawCodes codes(raw);
+  auto compute = [&](int64_t nb, uint32_t* raw, const Acts& x) {
+    R::last_codes(W, N, left(nb), row_bytes, kt, raw);
+    const RawCodes<ODD> codes(raw, left(nb));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t nib[8];
@@ -946,11 +968,11 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
     arrived();
     const bool two = nb + TW < b1;
     if (two) load(nb + TW, raw1[wave], x1);
-    compute(raw0[wave], x0);
+    compute(nb, raw0[wave], x0);
     if (two) {
       arrived();
       if (nb + 2 * TW < b1) load(nb + 2 * TW, raw0[wave], x0);
-      compute(raw1[wave], x1);
+      compute(nb + TW, raw1[wave], x1);
     }
   }
 
@@ -1063,23 +1085,12 @@ hipError_t prep_weights(const uint8_t* w, int64_t n0, int64_t rows, int64_t N, i
   if (qfrag)
     hipLaunchKernelGGL(prep_codes_kernel, dim3(static_cast<unsigned>(rows / 16), gy), dim3(256), 0,
                        s, w, n0, N, kblocks, KB, qfrag, scale);
-  if (tfrag && K % 64 == 0) {
+  if (tfrag) {
     const int ktiles = static_cast<int>((K + 127) / 128);
     const dim3 grid(static_cast<unsigned>((rows / 32 * ktiles + 3) / 4));
-    if (parts == 2)
-      hipLaunchKernelGGL(prep_transpose64_kernel<2>, grid, dim3(256), 0, s, w, n0, N, K, rows / 32,
-                         ktiles, tfrag);
-    else
-      hipLaunchKernelGGL(prep_transpose64_kernel<1>, grid, dim3(256), 0, s, w, n0, N, K, rows / 32,
-                         ktiles, tfrag);
-  } else if (tfrag) {
-    const dim3 grid(static_cast<unsigned>(rows / 32), gy);
-    if (parts == 2)
-      hipLaunchKernelGGL(prep_transpose_kernel<2>, grid, dim3(256), 0, s, w, n0, N, kblocks,
-                         rows / 32, tfrag);
-    else
-      hipLaunchKernelGGL(prep_transpose_kernel<1>, grid, dim3(256), 0, s, w, n0, N, kblocks,
-                         rows / 32, tfrag);
+    auto* kernel = K % 64 == 0 ? (parts == 2 ? prep_transpose_kernel<2, false> : prep_transpose_kernel<1, false>)
+                               : (parts == 2 ? prep_transpose_kernel<2, true> : prep_transpose_kernel<1, true>);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, w, n0, N, K, rows / 32, ktiles, tfrag);
   }
   return hipGetLastError();
 }
@@ -1144,9 +1155,10 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   const int64_t span = (p.CB + p.splits - 1) / p.splits;
   auto go = [&](auto rtc, auto pa, auto pb, auto type) {
     using T = decltype(type);
-    hipLaunchKernelGGL((gemm_transposed_kernel<decltype(rtc)::value, decltype(pa)::value,
-                                               decltype(pb)::value, T>),
-                       dim3(static_cast<unsigned>(static_cast<int64_t>(tiles) * p.splits)),
+    constexpr int RT = decltype(rtc)::value, PA = decltype(pa)::value, PB = decltype(pb)::value;
+    auto* kernel = p.K % 64 == 0 ? gemm_transposed_kernel<RT, PA, PB, T, false>
+                                 : gemm_transposed_kernel<RT, PA, PB, T, true>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(tiles) * p.splits)),
                        dim3(64 * TW), 0, s, p.g, p.w, p.n0, p.N, p.M, p.K, p.CB, mtiles, tiles, span,
                        p.part, p.alpha, p.inv, static_cast<T*>(p.out));
   };
@@ -1195,9 +1207,9 @@ hipError_t launch_logits_direct(const uint8_t* w, const LogitGemm& p, hipStream_
   auto go = [&](auto rt, auto pa, auto stats) {
     constexpr int RT = decltype(rt)::value, PA = decltype(pa)::value;
     constexpr bool STATS = decltype(stats)::value;
-    auto* kernel = p.CB % 4 == 0 ? logits_direct_kernel<RT, PA, STATS, false>
+    auto* kernel = p.K % 128 == 0 ? logits_direct_kernel<RT, PA, STATS, false>
                                  : logits_direct_kernel<RT, PA, STATS, true>;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * DW), 0, s, p.a, w, p.inv, p.M, p.cols, p.CB * 32, p.n0, p.N,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * DW), 0, s, p.a, w, p.inv, p.M, p.cols, p.K, p.n0, p.N,
                        p.targets, p.logits, p.tmax, p.tsum, p.tlogit, p.ld, p.tld);
   };
   using std::integral_constant;
@@ -1268,7 +1280,7 @@ DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   // the transposed copy: written and read at about 3 TB/s, and its launch
   best += 2.0 * N * K * p.pb * 2 / 3e6 + 3;
   const TransposedPlan d = transposed_plan(M, N, K, units, cus);
-  p.direct = K % 64 == 0 && d.us < best;
+  p.direct = d.us < best;
   p.splits = p.direct ? d.splits : even_splits(p.rows / 32, p.splits);
   Carver c;
   p.dy = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * p.pa);

@@ -16,8 +16,8 @@
 // small gradient and loss.
 //
 // Up to 64 rows read the table at its Q4_0 size instead, for the logits and for
-// the gradient (K % 64 == 0); a few rows without a gradient go through the
-// matvec-accuracy kernels.
+// the gradient; a few rows without a gradient go through the matvec-accuracy
+// kernels.
 
 #include <algorithm>
 
@@ -287,13 +287,13 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
 // (131072 x 3072, one row: 49 us against the direct kernel's 69, four 57
 // against 71), and up to 16 of a table that gives few of the direct kernel's
 // 512-row workgroups long rows to walk (16 rows of 8192 x 3072: 43 against 57;
-// of 8192 x 1280 34 against 32).  Otherwise the table would
-// have to be unpacked: one row of 65392 x 1248 takes 55 us against 109, eight
-// of 2000 24 against 40; from two rows on, 65392 take 110 either way, and more
-// here at five.
+// of 8192 x 1280 34 against 32).  Otherwise those kernels are slower, and only
+// small products go there (1248 columns: one row of 16384 23 us against 36, of
+// 65392 55 against 40, eight of 2000 24 against 37; of 160 columns 25 against
+// 19).
 bool few_rows(int64_t M, int64_t N, int64_t K) {
   if (K % 64 == 0) return M <= (N <= 16384 && K >= 2048 ? 16 : 4);
-  return M == 1 || (M <= 16 && M * N * K <= int64_t(1) << 25);
+  return K >= 1024 && M <= 16 && M * N * K <= int64_t(1) << 25;
 }
 
 struct XentPlan {
@@ -309,7 +309,7 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus
   XentPlan p = {};
   Carver c;
   p.few = !grad && few_rows(M, N, K);
-  p.direct = !p.few && M <= DIRECT_ROWS && K % 64 == 0;
+  p.direct = !p.few && M <= DIRECT_ROWS;
   p.run_max = c.take(M * 4);
   p.run_sum = c.take(M * 4);
   p.tlogit = c.take(M * 4);
@@ -440,6 +440,7 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, 
     lg.inv = f32(p.inv);
     lg.M = M;
     lg.cols = cols;
+    lg.K = K;
     lg.CB = blocks32(K);
     lg.n0 = n0;
     lg.N = N;

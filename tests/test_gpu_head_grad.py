@@ -365,8 +365,21 @@ def test_xent_pieces_unpacked(dtype):
 
 @pytest.mark.parametrize("m,n,k", [(4, 1000, 2048), (5, 1000, 2048), (16, 16384, 2112), (16, 16385, 2048),
                                    (17, 500, 2048), (16, 300, 1984), (1, 40000, 96), (2, 40000, 96),
-                                   (16, 21845, 96), (16, 21846, 96)])
+                                   (16, 21845, 96), (16, 21846, 96), (16, 1985, 1056), (16, 1986, 1056),
+                                   (3, 500, 1056), (3, 500, 992)])
 def test_xent_loss_routes(m, n, k):
     """Losses alone on both sides of the sizes that choose between the kernels."""
     for dtype in (F32, BF16):
         xent_case(m, n, k, dtype, 5400 + m, grad=False, targets=ODD if m > 5 else None)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("m,n,k", [(2, 1, 32), (2, 3, 96), (5, 31, 32), (17, 33, 160), (33, 63, 224), (49, 65, 288),
+                                   (64, 129, 352), (64, 128, 416), (20, 2001, 1056), (70, 301, 160), (16, 515, 480)])
+def test_odd_blocks(m, n, k, dtype):
+    """K an odd multiple of 32 (every other row of the weights starts in the middle of a
+    dword), with an odd or even last row: the head's loss and gradient, and dx."""
+    xent_case(m, n, k, dtype, 5500 + m + n, targets=ODD if m > 5 else None)
+    xent_case(m, n, k, dtype, 5600 + m + n, grad=False, targets=ODD if m > 5 else None)
+    dx_case(m, n, k, dtype, 5700 + m + n)
+    dx_case(300, n, k, dtype, 5800 + m + n)
