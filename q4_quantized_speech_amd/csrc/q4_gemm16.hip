@@ -719,8 +719,8 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
 // ---------------------------------------------------------------------------
 constexpr int DW = 8;  // waves
 
-// Measured: 38 x 131072 x 3072 float32 116 us (61 GFLOP of binary16 in two parts:
-// 530 TFLOP/s; the table at 2 TB/s), bound by decoding, scaling and the latency of
+// Measured: 38 x 131072 x 3072 float32 114 us (61 GFLOP of binary16 in two parts:
+// 540 TFLOP/s; the table at 2 TB/s), bound by decoding, scaling and the latency of
 // one chunk in flight; 8 rows of 65392 x 1280 bfloat16 36 us in all.
 template <int RT, int PA, bool STATS, bool ANY>
 __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(2, 2)))
@@ -832,9 +832,14 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        if constexpr (PA == 2)
-          t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][1], q, t[s & 1][r], 0, 0, 0);
         asm volatile("" : "+v"(t[s & 1][r])::"memory");
+      }
+      if constexpr (PA == 2) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          t[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[r][1], q, t[s & 1][r], 0, 0, 0);
+          asm volatile("" : "+v"(t[s & 1][r])::"memory");
+        }
       }
     };
     codes(0);
