@@ -383,3 +383,11 @@ def test_odd_blocks(m, n, k, dtype):
     xent_case(m, n, k, dtype, 5600 + m + n, grad=False, targets=ODD if m > 5 else None)
     dx_case(m, n, k, dtype, 5700 + m + n)
     dx_case(300, n, k, dtype, 5800 + m + n)
+
+
+@pytest.mark.parametrize("n", [(1 << 20) + 777, (1 << 20) + 2048])
+def test_odd_blocks_pieces(n):
+    """K an odd multiple of 32 and more columns than one piece of the direct form."""
+    t = [0, n - 1, (n + 1) // 2 // 256 * 256, n // 2, -1]
+    xent_case(64, n, 96, BF16, 5900, ramp=True, targets=t)
+    xent_case(64, n, 96, F32, 5900, ramp=True, grad=False, targets=t)
