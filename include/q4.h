@@ -362,10 +362,13 @@ q4_status q4_matmul_dx(const void* w_q4, const void* dy, void* dx, int32_t type,
  *           bytes of device scratch; its contents do not matter.  Calls that
  *           share it must be ordered.
  * Logits, maxima and sums are float32 over exact weights.  1 - softmax at the
- * target is taken as the sum of the others, so small losses and gradients
- * keep their relative precision.  For float16 and bfloat16 the gradient's
- * probabilities and weights are rounded to binary16 (float32 keeps two parts
- * of each; |deq(T)| must stay below 65504 for dx).  Deterministic; a row that
+ * target is taken as the sum of the others, and the gradient's probabilities
+ * are kept relative to the largest of the others, so small losses and
+ * gradients keep their relative precision however far the target is above
+ * them.  For float16 and bfloat16 the gradient's probabilities and weights are
+ * rounded to binary16 (2^-11 of each, or 2^-39 of the largest probability but
+ * the target's); float32 keeps two parts of each (2^-22, or the same 2^-39).
+ * |deq(T)| must stay below 65504 for dx.  Deterministic; a row that
  * holds an infinity or NaN gives non-finite values in that row only, and
  * loss 0 and dx 0 if it is padding.
  */

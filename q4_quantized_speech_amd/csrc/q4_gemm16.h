@@ -106,8 +106,9 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s);
 // Logits of weight rows n0 .. n0 + cols: l[m][n] = inv[m] sum_b scale[n][b]
 // (A[m, block b] . (q - 8)[n, block b]), float32 over exact products.  With
 // `logits`, [M][ld] floats are written and tmax[m][n / 64 cols] holds the
-// maxima; else tmax and tsum hold the maximum and the sum of exp(l - maximum)
-// of each 64 columns without the target's, and tlogit[m] the target's.
+// maxima of the others than the target; else tmax and tsum hold the maximum
+// (the target among them) and the sum of exp(l - maximum) of each 64 columns
+// without the target's, and tlogit[m] the target's.
 struct LogitGemm {
   const f16x8 *a, *q;
   int pa;

@@ -557,15 +557,15 @@ __device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0
       const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
       const bool live = m < M;
       const float is = live ? inv[m] : 0.f;
+      const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 - nl : -1;
       float l[4], top = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         l[j] = n0 + nl + 16 * j < N ? acc[i][j][v] * is : -__builtin_inff();
-        top = fmaxf(top, l[j]);
+        if (STATS || t != 16 * j) top = fmaxf(top, l[j]);
       }
       top = row16_max(top);
       if constexpr (STATS) {
-        const int64_t t = live ? static_cast<int64_t>(targets[m]) - n0 - nl : -1;
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

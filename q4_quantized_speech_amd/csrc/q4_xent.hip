@@ -12,8 +12,10 @@
 // codes, the running maximum and sum of the softmax updated, and, for the
 // gradient, the piece's probabilities multiplied by the transposed piece into
 // a float32 accumulator that is rescaled when the maximum grows.  1 - p_t is
-// the sum of the other probabilities, so a row the model is sure of keeps its
-// small gradient and loss.
+// the sum of the other probabilities, and the gradient's probabilities are
+// taken relative to the largest logit but the target's, brought to the row's
+// scale once at the end: a row the model is sure of keeps its small gradient
+// and loss, however far the target is above the others.
 //
 // Up to 64 rows read the table at its Q4_0 size instead, for the logits and for
 // the gradient; a few rows without a gradient go through the matvec-accuracy
@@ -27,7 +29,7 @@
 namespace q4 {
 namespace {
 
-constexpr float P_SCALE = 0x1p14f;  // probabilities relative to the row's maximum, scaled into binary16
+constexpr float P_SCALE = 0x1p14f;  // probabilities relative to the largest but the target's, scaled into binary16
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -66,8 +68,8 @@ __device__ __forceinline__ void row_loss(float top, float rest, float et, float 
   loss = !valid ? 0.f : et >= rest ? log1pf(rest / et) : logf(rest + et) + (top - target_logit);
 }
 
-// Per row, one workgroup each.  GRAD: the new running maximum, alpha = the
-// factor that moves sums and gradients to it, and the running sum with the
+// Per row, one workgroup each.  GRAD: the new running maximum (of the logits
+// but the target's, as tmax is), alpha = the factor that moves sums and gradients to it, and the running sum with the
 // previous piece's partial sums (psum [chunks][M]).  Else: the piece's own
 // (tmax, tsum) entries folded into the running pair, and after the last piece
 // (loss not null) the results.
@@ -133,9 +135,12 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(
   }
 }
 
-// Probabilities of a piece relative to the running maximum, as operand
-// fragments (NATURAL over the columns), 16 rows x `chunk` columns per
-// workgroup; the target's is left out.  psum[chunk][m] their float32 sums.
+// Probabilities of a piece relative to the running maximum of the logits but
+// the target's, as operand fragments (NATURAL over the columns), 16 rows x
+// `chunk` columns per workgroup; the target's is left out.  psum[chunk][m]
+// their float32 sums.  Scaled by 2^14, a value is stored to 2^-11 (one part) or
+// 2^-22 of it, and to 2^-39 of the largest of the others (binary16's smallest
+// step is the same for both parts).
 constexpr int PC_CHUNK = 2048;
 // Measured per piece of 32768 columns: 375 rows in two parts 27 us (98 MB), 1500
 // in one 62 us (295 MB, 4.8 TB/s); bound by bytes.
@@ -197,7 +202,10 @@ __global__ __launch_bounds__(256) void xent_prob_kernel(const float* __restrict_
   }
 }
 
-// loss, lse and the gradient: one workgroup per row.
+// loss, lse and the gradient: one workgroup per row.  With d the target's logit
+// less the largest of the others, top, and rest = sum exp(l - top) without the
+// target: p_n = f exp(l[n] - top), f = 1 / (rest + e^d) = e^-d / (rest e^-d + 1),
+// the one whose exponential is at most 1.
 // Measured: 375 x 3072 float32 20 us, 1500 bfloat16 28 us.
 template <typename T>
 __global__ __launch_bounds__(256) void xent_final_kernel(
@@ -210,13 +218,18 @@ __global__ __launch_bounds__(256) void xent_final_kernel(
   const int64_t m = blockIdx.x;
   const int64_t t = targets[m];
   const bool valid = t >= 0 && t < N;
-  float rest = run_sum[m];  // exp sum without the target, relative to the maximum
+  float rest = run_sum[m];
   for (int c = 0; c < chunks; ++c) rest += psum[static_cast<int64_t>(c) * M + m];
-  const float top = run_max[m];
-  const float et = valid ? exp_below(tlogit[m], top) : 0.f;
-  if (threadIdx.x == 0) row_loss(top, rest, et, tlogit[m], valid, loss[m], lse[m]);
+  const float top = run_max[m];  // -inf where the target is the only column: d is inf
+  const float d = valid ? tlogit[m] - top : -__builtin_inff();
+  const float ed = expf(-fabsf(d));
+  const float f = d > 0.f ? ed / __builtin_fmaf(rest, ed, 1.f) : 1.f / (rest + ed);
+  if (threadIdx.x == 0) {
+    const float over = d > 0.f ? log1pf(rest * ed) : logf(rest + ed);  // of lse over the larger of the two
+    lse[m] = (d > 0.f ? tlogit[m] : top) + over;
+    loss[m] = !valid ? 0.f : d > 0.f ? over : over - d;
+  }
   const float g = valid ? (dloss ? dloss[m] : 1.f) : 0.f;
-  const float f = 1.f / (rest + et);
   T* o = dx + m * K;
   for (int64_t k = 4 * threadIdx.x; k < K; k += 1024) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -225,12 +238,12 @@ __global__ __launch_bounds__(256) void xent_final_kernel(
       for (int p = 0; p < splits; ++p)
         s += *reinterpret_cast<const f32x4*>(part + (static_cast<int64_t>(p) * M + m) * K + k);
       const uint8_t* blk = W + (t * (K / 32) + k / 32) * BLOCK_BYTES;
-      const float d = half_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
+      const float ws = half_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
       const int j = static_cast<int>(k & 31);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t b = blk[2 + ((j + e) & 15)];
-        const float w = (static_cast<float>(j < 16 ? b & 15u : b >> 4) - 8.f) * d;
+        const float w = (static_cast<float>(j < 16 ? b & 15u : b >> 4) - 8.f) * ws;
         v[e] = g * (f * (s[e] * (1.f / P_SCALE) - rest * w));
       }
     }
