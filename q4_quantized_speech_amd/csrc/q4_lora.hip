@@ -12,9 +12,11 @@
 // step the two dependent launches.  Products run on the matrix cores as
 // bfloat16 with float32 sums, in a fixed order: a value enters as one, two or
 // three bfloat16 parts (bfloat16, float16, float32: the leading 8 bits of
-// what is left, exact), and the products of parts below 2^-24 of the whole are
-// dropped.  One v_mfma_f32_16x16x32_bf16 takes the reduction steps of eight
-// float32 MFMAs in a sixteenth of their time, so six of them are still faster.
+// what is left, exact), of which the second is below 2^-7 of the whole and the
+// third below 2^-15.  Of the products of parts only that of two third ones is
+// left out (below 2^-30).  One v_mfma_f32_16x16x32_bf16 takes the reduction
+// steps of eight float32 MFMAs in a sixteenth of their time, so eight of them
+// are still twice as fast.
 //
 // A first launch contracts the long axis ("down": rank vectors h and g),
 // split over workgroups into slices that the next launch adds.  Rows are
@@ -85,7 +87,7 @@ __device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mfma_parts(const Parts<NA>& a, const Parts<NB>& b, f32x4 c) {
 #pragma unroll
-  for (int s = 2; s >= 0; --s)  // small products first
+  for (int s = 3; s >= 0; --s)  // small products first; (2, 2) is left out
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       if (s - i >= 0 && s - i < NB)
