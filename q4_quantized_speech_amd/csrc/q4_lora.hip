@@ -64,7 +64,9 @@ __device__ __forceinline__ uint32_t pack_high(float a, float b) {  // the high h
 }
 
 // Leading 8 significant bits, then the rest's (truncation: exact remainders).
-template <int NP>
+// NEAREST: the last part takes all that is left, rounded to nearest (a value
+// that has more bits than its parts: 2^-16 of it with two, without a bias).
+template <int NP, bool NEAREST = false>
 __device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
   Parts<NP> out;
   float r[8];
@@ -72,6 +74,13 @@ __device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
   for (int e = 0; e < 8; ++e) r[e] = v[e];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
+    if constexpr (NEAREST) {
+      if (p == NP - 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out.p[p][e] = static_cast<__bf16>(r[e]);
+        break;
+      }
+    }
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = pack_high(r[2 * e], r[2 * e + 1]);
@@ -401,7 +410,7 @@ __device__ __forceinline__ void load_rank(const float* __restrict__ P, int split
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] *= scale;
     }
-    const Parts<NP> q = split8<NP>(v);
+    const Parts<NP> q = split8<NP, NP == 2>(v);
 #pragma unroll
     for (int u = 0; u < NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + u8) * ld + j) = q.p[u];
   }
@@ -415,8 +424,8 @@ __device__ __forceinline__ Parts<NP> rank_parts(const uint16_t* hs, int ld, int 
   return q;
 }
 
-// Parts of a rank vector that a result of type T needs: 16 bits of it are far
-// below a 16-bit result's rounding.
+// Parts of a float32 rank vector for a result of type T: two hold it to 2^-16,
+// 32 times below float16's rounding and 256 times below bfloat16's.
 template <typename T>
 constexpr int rank_np = sizeof(T) == 4 ? 3 : 2;
 

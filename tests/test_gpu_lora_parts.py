@@ -7,7 +7,9 @@ any run (u = 2^-24, half a step of float32):
   float32 results  one product v v and sums with zeros: the rounding of the last sum (u), the
                    roundings of the small sums before it (2^-6 u each, at most eight), the
                    dropped product of the two smallest parts (2^-30), the residual's sum
-                   (exact here: zeros): 2 u v v."""
+                   (exact here: zeros): 2 u v v.
+  16-bit results   the rank vector enters as two bfloat16 parts, the second rounded to
+                   nearest: 2^-16 of it, + the smallest step of the type."""
 
 import pytest
 import torch
@@ -49,3 +51,24 @@ def test_float32(m, na, atype):
         b[:, 7, 3] = va if first else 1.0
         dx = q4.lora_grad(x, dy, a, b, ids)[0][:, 5].double()
         assert ((dx - want).abs() <= 2 * U * want).all(), float(((dx - want) / want / U).abs().max())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("m", [40, 300])
+def test_rank_vectors_of_16_bit_results(m, dtype):
+    """The residual takes all but the last bits of the result away, so its rounding is small."""
+    n, k, r, na = 72, 64, 16, 2
+    x, dy, a, b, ids = one_hot(m, n, k, r, na, dtype, F32)
+    x[:, 5], dy[:, 7] = 1.0, 1.0
+    a[:, 3, 5], b[:, 7, 3] = V, 1.0
+    res = torch.zeros((m, n), device="cuda", dtype=dtype)
+    res[:, 7] = -(1 + 2.0 ** -7)  # V - 1 - 2^-7 = -2^-23
+    step = torch.finfo(dtype).tiny * torch.finfo(dtype).eps
+    announce(f"rank vectors {m} {dtype}")
+    y = q4.lora(x, a, b, ids, r=res)[:, 7].double()
+    assert ((y + 2.0 ** -23).abs() <= 2.0 ** -16 * V + step).all(), float(y.abs().max()) * 2 ** 16
+    a[:, 3, 5], b[:, 7, 3] = 1.0, V
+    res = torch.zeros((m, k), device="cuda", dtype=dtype)
+    res[:, 5] = -(1 + 2.0 ** -7)
+    dx = q4.lora_grad(x, dy, a, b, ids, r=res)[0][:, 5].double()
+    assert ((dx + 2.0 ** -23).abs() <= 2.0 ** -16 * V + step).all(), float(dx.abs().max()) * 2 ** 16
