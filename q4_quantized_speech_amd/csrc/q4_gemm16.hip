@@ -1193,11 +1193,12 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   const integral_constant<int, 1> one;
   const integral_constant<int, 2> two;
   auto parts = [&](auto rtc) {
-    // float32 has two parts of both, float16 and bfloat16 one of G
+    // float32 has two parts of both, float16 and bfloat16 one of G; the head's
+    // gradient, which writes slices whatever its type, one of both there
     if (p.pa == 2) go(rtc, two, two, float{});
-    else if (p.pb == 2) go(rtc, one, two, _Float16{});
-    else if (p.type == TYPE_F16) go(rtc, one, one, _Float16{});
-    else go(rtc, one, one, __bf16{});
+    else if (p.pb == 1) go(rtc, one, one, float{});
+    else if (p.type == TYPE_F16) go(rtc, one, two, _Float16{});
+    else go(rtc, one, two, __bf16{});
   };
   if (rt == 1) parts(one);
   else if (rt == 2) parts(two);
@@ -1288,9 +1289,7 @@ struct DxPlan {
 DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   DxPlan p;
   p.pa = type == TYPE_F32 ? 2 : 1;
-  // bfloat16: the weight's rounding to binary16 (2^-11) is well below the
-  // result's (2^-8); float16 and float32 results keep the weight exact
-  p.pb = type == TYPE_BF16 ? 1 : 2;
+  p.pb = 2;  // the weights are exact, as the plain form's
   const int units = p.pa + p.pb - 1;
   p.rows = (N + 63) / 64 * 64;
   double best = 1e30;
