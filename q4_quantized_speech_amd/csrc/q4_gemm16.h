@@ -43,7 +43,7 @@ hipError_t prep_weights(const uint8_t* w, int64_t n0, int64_t rows, int64_t N, i
                         f16x8* qfrag, float* scale, f16x8* tfrag, int parts, hipStream_t s);
 
 // Tile shapes.
-enum class Tile { T256x256, T128x128, T32x256 };
+enum class Tile { T256x256, T128x128 };
 struct TileDim {
   int m, n;
 };

@@ -380,7 +380,6 @@ struct Shape {
 };
 using S256 = Shape<2, 4, 8, 4>;
 using S128 = Shape<2, 2, 4, 4>;
-using S32 = Shape<1, 4, 2, 4>;
 
 template <typename S, int PA, int PB, int KS>
 struct Stage {
@@ -1084,11 +1083,10 @@ __global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ par
 
 template <typename F>
 hipError_t with_tile(Tile t, F f) {
-  switch (t) {
-    case Tile::T256x256: f(S256{}); break;
-    case Tile::T128x128: f(S128{}); break;
-    default: f(S32{}); break;
-  }
+  if (t == Tile::T256x256)
+    f(S256{});
+  else
+    f(S128{});
   return hipGetLastError();
 }
 
@@ -1123,14 +1121,14 @@ hipError_t prep_weights(const uint8_t* w, int64_t n0, int64_t rows, int64_t N, i
 }
 
 TileDim tile_dim(Tile t) {
-  return t == Tile::T256x256 ? TileDim{256, 256} : t == Tile::T128x128 ? TileDim{128, 128} : TileDim{32, 256};
+  return t == Tile::T256x256 ? TileDim{256, 256} : TileDim{128, 128};
 }
 
 double tile_time_us(Tile t, int64_t M, int64_t N, int64_t C, int units, int splits, int cus) {
   const TileDim d = tile_dim(t);
   const int64_t items = ((M + d.m - 1) / d.m) * ((N + d.n - 1) / d.n) * splits;
   const int per_cu = t == Tile::T256x256 ? 1 : 2;
-  const double eff = t == Tile::T256x256 ? 0.45 : t == Tile::T128x128 ? 0.30 : 0.12;
+  const double eff = t == Tile::T256x256 ? 0.45 : 0.30;
   const double cu_rate = 2.5e9 / 256 * eff;  // flops per microsecond of one CU
   const double rounds = static_cast<double>((items + per_cu * cus - 1) / (static_cast<int64_t>(per_cu) * cus));
   const double gemm = rounds * per_cu * 2.0 * d.m * d.n * (static_cast<double>(C) / splits) * units / cu_rate;
@@ -1293,7 +1291,7 @@ DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   const int units = p.pa + p.pb - 1;
   p.rows = (N + 63) / 64 * 64;
   double best = 1e30;
-  for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
+  for (Tile t : {Tile::T256x256, Tile::T128x128}) {
     for (int s = 1; s <= 16 && (s == 1 || p.rows / s >= 128); ++s) {
       const double us = tile_time_us(t, M, K, p.rows, units, s, cus);
       if (us < best) {

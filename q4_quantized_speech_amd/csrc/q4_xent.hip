@@ -362,7 +362,7 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus
     p.splits = transposed_plan(M, p.piece, K, p.pp + p.pb - 1, cus).splits;
   } else {
     double best1 = 1e30, best2 = 1e30;
-    for (Tile t : {Tile::T256x256, Tile::T128x128, Tile::T32x256}) {
+    for (Tile t : {Tile::T256x256, Tile::T128x128}) {
       const double us = tile_time_us(t, M, p.piece, K, p.pa, 1, cus);
       if (us < best1) {
         best1 = us;
