@@ -392,13 +392,11 @@ q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets
  *   4194304, R a multiple of 8 from 8 to 128, 1 <= adapters <= 65535.
  *   workspace : q4_lora_workspace_bytes(M, N, K, R) bytes of device scratch;
  *           its contents do not matter.  Calls that share it must be ordered.
- * Two launches, three for more than 256 rows; A_a x is kept in float32 (float16
- * and bfloat16 activations: 2^-16 of it may be lost where a row shares its
- * adapter with more than eight of its 64 rows).  Deterministic; the order of a
- * row's float32 sums depends on the sizes and on how many rows share its
- * adapter.  An infinity or NaN in a row gives non-finite values in that row
- * only (an infinity may come out as NaN); the rows of other adapters do not
- * see an adapter's.
+ * Two launches, three for more than 256 rows; A_a x is kept in float32.
+ * Deterministic; the order of a row's float32 sums depends on the sizes and on
+ * how many rows share its adapter.  An infinity or NaN in a row gives
+ * non-finite values in that row only (an infinity may come out as NaN); the
+ * rows of other adapters do not see an adapter's.
  */
 size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 q4_status q4_lora(const void* x, const void* a, const void* b, const float* scale,
@@ -420,8 +418,7 @@ q4_status q4_lora(const void* x, const void* a, const void* b, const float* scal
  *   Rows without an adapter: dx = r, nothing to da and db, whatever they hold.
  *   s_a is a constant.
  *   Ranges as for q4_lora, and adapters * (ceil(K/64) + ceil(N/64)) <= 2^21.
- * Three launches.  Deterministic.  For float16 and bfloat16 activations dx takes
- * g to 2^-16 of it.
+ * Three launches.  Deterministic.
  */
 size_t q4_lora_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 q4_status q4_lora_grad(const void* x, const void* dy, const void* a, const void* b,

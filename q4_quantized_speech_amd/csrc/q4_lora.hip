@@ -64,9 +64,7 @@ __device__ __forceinline__ uint32_t pack_high(float a, float b) {  // the high h
 }
 
 // Leading 8 significant bits, then the rest's (truncation: exact remainders).
-// NEAREST: the last part takes all that is left, rounded to nearest (a value
-// that has more bits than its parts: 2^-16 of it with two, without a bias).
-template <int NP, bool NEAREST = false>
+template <int NP>
 __device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
   Parts<NP> out;
   float r[8];
@@ -74,13 +72,6 @@ __device__ __forceinline__ Parts<NP> split8(const float (&v)[8]) {
   for (int e = 0; e < 8; ++e) r[e] = v[e];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    if constexpr (NEAREST) {
-      if (p == NP - 1) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) out.p[p][e] = static_cast<__bf16>(r[e]);
-        break;
-      }
-    }
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = pack_high(r[2 * e], r[2 * e + 1]);
@@ -381,14 +372,15 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(
   }
 }
 
-// Rank vectors of a group as NP bfloat16 parts in LDS, hs[part][member][ld]:
+// Rank vectors of a group as three bfloat16 parts (exact: two would leave up to
+// 2^-15 of them out, 1500 rows of rank 64 in bfloat16 25.1 us against 25.5) in
+// LDS, hs[part][member][ld]:
 // scale * (the slices' sum); zero past the last member and for j in [R, R
 // rounded up to 32).  ld = that + 8: rows 16-byte aligned, on different banks.
 __device__ __forceinline__ int rank_ld(int R) { return ((R + 31) & ~31) + 8; }
-template <int NP>
-constexpr size_t rank_lds(int64_t R) { return static_cast<size_t>(NP) * LT * (((R + 31) & ~31) + 8) * 2; }
+constexpr int RANK_NP = 3;
+constexpr size_t rank_lds(int64_t R) { return static_cast<size_t>(RANK_NP) * LT * (((R + 31) & ~31) + 8) * 2; }
 
-template <int NP>
 __device__ __forceinline__ void load_rank(const float* __restrict__ P, int splits, int64_t M, int R,
                                           int64_t m0, const Group& group, float scale,
                                           uint16_t* hs) {
@@ -410,24 +402,18 @@ __device__ __forceinline__ void load_rank(const float* __restrict__ P, int split
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] *= scale;
     }
-    const Parts<NP> q = split8<NP, NP == 2>(v);
+    const Parts<RANK_NP> q = split8<RANK_NP>(v);
 #pragma unroll
-    for (int u = 0; u < NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + u8) * ld + j) = q.p[u];
+    for (int u = 0; u < RANK_NP; ++u) *reinterpret_cast<bf16x8*>(hs + (u * LT + u8) * ld + j) = q.p[u];
   }
 }
 
-template <int NP>
-__device__ __forceinline__ Parts<NP> rank_parts(const uint16_t* hs, int ld, int row, int j) {
-  Parts<NP> q;
+__device__ __forceinline__ Parts<RANK_NP> rank_parts(const uint16_t* hs, int ld, int row, int j) {
+  Parts<RANK_NP> q;
 #pragma unroll
-  for (int u = 0; u < NP; ++u) q.p[u] = *reinterpret_cast<const bf16x8*>(hs + (u * LT + row) * ld + j);
+  for (int u = 0; u < RANK_NP; ++u) q.p[u] = *reinterpret_cast<const bf16x8*>(hs + (u * LT + row) * ld + j);
   return q;
 }
-
-// Parts of a float32 rank vector for a result of type T: two hold it to 2^-16,
-// 32 times below float16's rounding and 256 times below bfloat16's.
-template <typename T>
-constexpr int rank_np = sizeof(T) == 4 ? 3 : 2;
 
 // y[m, n] = r[m, n] + sum_j hs[m][j] B_a[n, j] for one tile of rows and the
 // columns [n0, n1).
@@ -448,8 +434,7 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
     const float* __restrict__ P, const TA* __restrict__ B, const float* __restrict__ scale,
     const int32_t* __restrict__ ids, const T* R_, T* Y, int64_t M, int64_t N, int R, int adapters,
     int splits, int chunks, int64_t chunk) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t hs[];  // rank_lds<NP>(R) bytes
-  constexpr int NP = rank_np<T>;
+  extern __shared__ __attribute__((aligned(16))) uint16_t hs[];  // rank_lds(R) bytes
   const int ld = rank_ld(R);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
@@ -549,7 +534,7 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
       }
       return;
     }
-    load_rank<NP>(P, splits, M, R, m0, group, sc, hs);
+    load_rank(P, splits, M, R, m0, group, sc, hs);
     __syncthreads();
     for (int64_t base = n0 + 64 * wave; base < n1; base += 64 * WAVES) {
       const TA* brow[4];
@@ -570,7 +555,7 @@ __global__ __launch_bounds__(64 * WAVES, NS == 1 ? 4 : 2) void lora_up_kernel(
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
             if (NS > 1 && s >= group.blocks()) break;
-            const Parts<NP> h = rank_parts<NP>(hs, ld, 16 * (s0 + s) + i, j0 + 8 * g);
+            const Parts<RANK_NP> h = rank_parts(hs, ld, 16 * (s0 + s) + i, j0 + 8 * g);
 #pragma unroll
             for (int t = 0; t < 4; ++t) acc[s][t] = mfma_parts(w[t], h, acc[s][t]);
           }
@@ -612,7 +597,6 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
                                         const int32_t* __restrict__ ids, const T* R_, T* DX,
                                         int64_t M, int64_t K, int R, int adapters, int64_t tile,
                                         int64_t k0, int64_t k1, int mine, int of, uint16_t* hs) {
-  constexpr int NP = rank_np<T>;
   const int ld = rank_ld(R);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
@@ -637,7 +621,7 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
   };
   for_groups(ids, m0, M, adapters, mine, of, [&](const Group& group, int a) {
     __syncthreads();
-    load_rank<NP>(G, 1, M, R, m0, group, 1.f, hs);
+    load_rank(G, 1, M, R, m0, group, 1.f, hs);
     __syncthreads();
     const TA* ad = A + static_cast<int64_t>(a) * R * K;
     // blocks of 16 rows at a time: two leave the registers for two workgroups on
@@ -664,9 +648,9 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
             v[e] = piece{};
             if (j < R) v[e] = *reinterpret_cast<const piece*>(ad + static_cast<int64_t>(j + e) * K + k);  // R % 8 == 0
           }
-          Parts<NP> h[NS];
+          Parts<RANK_NP> h[NS];
 #pragma unroll
-          for (int s = 0; s < NS; ++s) h[s] = rank_parts<NP>(hs, ld, 16 * (s0 + s) + i, j);
+          for (int s = 0; s < NS; ++s) h[s] = rank_parts(hs, ld, 16 * (s0 + s) + i, j);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             Parts<parts_of<TA>> w;
@@ -851,7 +835,7 @@ __global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) vo
     unsigned ablocks, int achunks, int bchunks) {
   __shared__ __attribute__((aligned(16))) union {
     f32x4 red[G_WAVES][4][64];
-    uint16_t hs[rank_lds<rank_np<T>>(16 * RT) / 2];
+    uint16_t hs[rank_lds(16 * RT) / 2];
   } sh;
   const unsigned bid = blockIdx.x;
   if (bid < dxblocks) {
@@ -941,7 +925,7 @@ hipError_t lora_rt(const LoraArgs& p, int cus) {
   auto up = [&](auto ns) {
     hipLaunchKernelGGL((lora_up_kernel<T, TA, WAVES, decltype(ns)::value>),
                        dim3(static_cast<unsigned>(tiles * chunks), gy), dim3(64 * WAVES),
-                       rank_lds<rank_np<T>>(p.R), p.stream, H, static_cast<const TA*>(p.b), scale,
+                       rank_lds(p.R), p.stream, H, static_cast<const TA*>(p.b), scale,
                        p.ids, static_cast<const T*>(p.r), static_cast<T*>(p.y), p.M, p.N,
                        static_cast<int>(p.R), static_cast<int>(p.adapters), slices, chunks,
                        per * unit);
