@@ -494,7 +494,8 @@ def lmhead_xent(w_q4: torch.Tensor, x: torch.Tensor, targets: torch.Tensor, grad
     """(loss, lse, dx): per row of x, lse = logsumexp(deq(T) x), loss = lse - the target's
     logit (float32), and with ``grad`` (or a ``dx`` to write) the gradient of
     sum(dloss * loss) with respect to x, in x's type; dx is None otherwise.  Rows whose
-    target is outside [0, N) have loss 0 and dx 0.  The logits are never kept whole."""
+    target is outside [0, N) have loss 0 and dx 0.  Logits are kept in pieces of the
+    vocabulary, at most 256 MiB of them (512 MiB for more than 32768 rows)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return lmhead_xent(w_q4, x, targets, grad, dloss, loss, lse, dx, workspace)

@@ -307,6 +307,8 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
   }
 }
 
+constexpr int64_t LOGITS = int64_t(1) << 26;  // kept at a time (256 MiB)
+
 // Losses alone (no gradient) that go through the matvec-accuracy kernels, four
 // rows at a time, instead of the matrix cores.  K % 64 == 0: up to four rows
 // (131072 x 3072, one row: 49 us against the direct kernel's 69, four 57
@@ -315,8 +317,10 @@ __global__ __launch_bounds__(256) void widen_kernel(const T* __restrict__ x, flo
 // of 8192 x 1280 34 against 32).  Otherwise those kernels are slower, and only
 // small products go there (1248 columns: one row of 16384 23 us against 36, of
 // 65392 55 against 40, eight of 2000 24 against 37; of 160 columns 25 against
-// 19).
+// 19).  They keep all logits, which the direct kernel takes in pieces: at most
+// as many as one of its pieces.
 bool few_rows(int64_t M, int64_t N, int64_t K) {
+  if (M * N > LOGITS) return false;
   if (K % 64 == 0) return M <= (N <= 16384 && K >= 2048 ? 16 : 4);
   return K >= 1024 && M <= 16 && M * N * K <= int64_t(1) << 25;
 }
@@ -350,8 +354,10 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus
   p.pa = type == TYPE_F32 ? 2 : 1;
   p.pp = p.pa;  // probabilities and weights: binary16's 11 bits below a 16-bit result's rounding
   p.pb = p.pa;
-  // pieces of equal size, their logits up to 256 MiB, their unpacked weights too
-  int64_t cap = std::max<int64_t>(2048, (int64_t(1) << 26) / M / 256 * 256);
+  // pieces of equal size, of up to LOGITS logits in rows padded to 16 as the
+  // probabilities' are (2048 columns for more than 32768 rows, 512 MiB at
+  // 65536), 32768 columns where they are unpacked
+  int64_t cap = std::max<int64_t>(2048, LOGITS / ((M + 15) / 16 * 16) / 256 * 256);
   if (!p.direct) cap = std::min<int64_t>(cap, 32768);
   const int64_t pieces = (N + cap - 1) / cap;
   p.piece = ((N + pieces - 1) / pieces + 255) / 256 * 256;

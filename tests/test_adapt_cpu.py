@@ -121,3 +121,18 @@ def test_dx_and_xent_binding_refusals():
                 dict(dx=x.half()), dict(lse=torch.zeros(4, 1)), {}):
         with pytest.raises(ValueError):
             q4.lmhead_xent(**{**dict(w_q4=w, x=x, targets=t), **bad})
+
+
+@pytest.mark.parametrize("grad", [0, 1])
+@pytest.mark.parametrize("m,n,k", [(1, 1 << 28, 32), (1, 1 << 27, 64), (4, 1 << 27, 64), (3, 1 << 24, 512), (16, 1 << 24, 96),
+                                   (64, 1 << 26, 128), (65, 1 << 20, 4096), (32768, 131072, 1280), (65536, 131072, 1280)])
+def test_xent_workspace_holds_pieces(m, n, k, grad):
+    """However large the table, the workspace holds pieces of at most 2^26 logits (2048 columns
+    where a row's share is less) in float32 and as two parts, their maxima and sums per 64
+    columns, a piece's unpacked weights (32768 rows) and x and dx a few times over."""
+    logits = max(1 << 26, 2048 * m)
+    most = logits * (8 if grad else 0) + logits // 4 * (0 if m <= 64 else 1) + 32768 * (k + 32) * 8 + 80 * m * k + (1 << 24)
+    if not grad and m <= 64:
+        most += logits * 4 + logits // 4  # a few rows may keep them all
+    need = _need("q4_lmhead_xent", 0, grad=grad, M=m, N=n, K=k)
+    assert 0 < need <= most, (need, most)
