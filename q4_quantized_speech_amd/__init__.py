@@ -458,6 +458,15 @@ def _scratch(workspace, query: str, dev: int, *args):
     return workspace
 
 
+def _realigned(status: int, *vectors):
+    """After a call refused for its alignment: the vectors it reads, copied on the current
+    stream where they start inside a 16-byte word (as the targets tokens[1:] do), or None if
+    none does and the call stays refused."""
+    if status != Q4_ERR_ALIGN or not any(v is not None and v.data_ptr() % 16 for v in vectors):
+        return None
+    return [v.clone() if v is not None and v.data_ptr() % 16 else v for v in vectors]
+
+
 def _raw_stream(dev: int) -> int:
     """The current stream's handle."""
     return torch._C._cuda_getCurrentRawStream(dev)
@@ -519,9 +528,13 @@ def lmhead_xent(w_q4: torch.Tensor, x: torch.Tensor, targets: torch.Tensor, grad
     if grad and dx is None:
         dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
     ws = _scratch(workspace, "q4_lmhead_xent_workspace_bytes", dev, t, int(bool(grad)), m, n, k)
-    _check(lib().q4_lmhead_xent(w_q4.data_ptr(), x.data_ptr(), targets.data_ptr(), _addr(dloss),
-                                loss.data_ptr(), lse.data_ptr(), _addr(dx), t, m, n, k,
-                                ws.data_ptr(), ws.numel(), _raw_stream(dev)), "q4_lmhead_xent")
+    status = lib().q4_lmhead_xent(w_q4.data_ptr(), x.data_ptr(), targets.data_ptr(), _addr(dloss),
+                                  loss.data_ptr(), lse.data_ptr(), _addr(dx), t, m, n, k,
+                                  ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    again = _realigned(status, targets, dloss)
+    if again:
+        return lmhead_xent(w_q4, x, again[0], grad, again[1], loss, lse, dx, ws)
+    _check(status, "q4_lmhead_xent")
     return loss, lse, dx
 
 
@@ -565,9 +578,13 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
     if out is None:
         out = torch.empty((m, n), dtype=x.dtype, device=x.device)
     ws = _scratch(workspace, "q4_lora_workspace_bytes", dev, m, n, k, rank)
-    _check(lib().q4_lora(x.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), ids.data_ptr(),
-                         _addr(r), out.data_ptr(), t, ta, m, n, k, rank, na, ws.data_ptr(),
-                         ws.numel(), _raw_stream(dev)), "q4_lora")
+    status = lib().q4_lora(x.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), ids.data_ptr(),
+                           _addr(r), out.data_ptr(), t, ta, m, n, k, rank, na, ws.data_ptr(),
+                           ws.numel(), _raw_stream(dev))
+    again = _realigned(status, ids, scale)
+    if again:
+        return lora(x, a, b, again[0], again[1], r, out, ws)
+    _check(status, "q4_lora")
     return out
 
 
@@ -600,10 +617,14 @@ def lora_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tenso
     if db is None:
         db = torch.empty((na, n, rank), dtype=torch.float32, device=x.device)
     ws = _scratch(workspace, "q4_lora_grad_workspace_bytes", dev, m, n, k, rank)
-    _check(lib().q4_lora_grad(x.data_ptr(), dy.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale),
-                              ids.data_ptr(), _addr(r), dx.data_ptr(), da.data_ptr(), db.data_ptr(),
-                              t, ta, m, n, k, rank, na, ws.data_ptr(), ws.numel(),
-                              _raw_stream(dev)), "q4_lora_grad")
+    status = lib().q4_lora_grad(x.data_ptr(), dy.data_ptr(), a.data_ptr(), b.data_ptr(),
+                                _addr(scale), ids.data_ptr(), _addr(r), dx.data_ptr(),
+                                da.data_ptr(), db.data_ptr(), t, ta, m, n, k, rank, na,
+                                ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    again = _realigned(status, ids, scale)
+    if again:
+        return lora_grad(x, dy, a, b, again[0], again[1], r, dx, da, db, ws)
+    _check(status, "q4_lora_grad")
     return dx, da, db
 
 
