@@ -86,9 +86,10 @@ def case(m, n, k, dtype, seed, shared, targets=()):
     err = (dx.double() - want).abs()
     assert (err <= tol).all(), float((err / tol).max())
     size = 2.0 ** -21 * (1 + l.abs().amax(1))
-    assert ((loss.double() - ref_loss).abs()
-            <= rest * (2 * tl + 4096 * U + size) + 2.0 ** -21 * ref_loss + n * 2.0 ** -126).all()
-    assert ((lse.double() - ref_lse).abs() <= tl + 4096 * U + size).all()
+    for loss, lse in ((loss, lse), q4.lmhead_xent(wq, x, t)[:2]):  # with the gradient, and alone
+        assert ((loss.double() - ref_loss).abs()
+                <= rest * (2 * tl + 4096 * U + size) + 2.0 ** -21 * ref_loss + n * 2.0 ** -126).all()
+        assert ((lse.double() - ref_lse).abs() <= tl + 4096 * U + size).all()
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
