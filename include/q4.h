@@ -334,7 +334,7 @@ enum { Q4_TYPE_F32 = 0, Q4_TYPE_F16 = 1, Q4_TYPE_BF16 = 30 };
  * On the matrix cores with float32 sums.  Each row of dy is scaled by a power
  * of two into binary16 (float32 rows as two parts), so gradients of any
  * magnitude keep their precision: per element the error of an operand is at
- * most 2^-22 of it or 2^-40 of its row's largest magnitude.  Weights are exact
+ * most 2^-22 of it or 2^-39 of its row's largest magnitude.  Weights are exact
  * (two parts).  |deq(W)| must stay below 65504.
  * Deterministic; a row that holds an infinity or NaN gives non-finite values
  * in that row only.

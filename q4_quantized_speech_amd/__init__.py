@@ -476,7 +476,9 @@ def matmul_dx(w_q4: torch.Tensor, dy: torch.Tensor, out: torch.Tensor | None = N
               workspace: torch.Tensor | None = None, stream=None):
     """dX = dY deq(W), the gradient of ``matmul`` with respect to x: dy is [M, N] of float32,
     float16 or bfloat16, the result [M, K] of its type.  Without ``workspace`` one is
-    allocated (several times the decoded weights' size for float32)."""
+    allocated: dy's operands and, for split sums, float32 copies of the result (42 MB for
+    375 x 18432 x 3072 in float32); very many rows of a small matrix also keep the
+    decoded weights."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return matmul_dx(w_q4, dy, out, workspace)
@@ -565,7 +567,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
     requests at once.  x is [M, K] (float32, float16 or bfloat16), a [adapters, R, K] and
     b [adapters, N, R] (x's type, or float32; with a float32 x any of the three), ids int32
     [M]; an id outside [0, adapters) leaves y = r.  r (zeros if None) may be ``out``.
-    With ``matmul_residual(w, x, y, out=y)`` after it, y is the adapted projection."""
+    With ``matmul_residual(w, x, y, out=y)`` after it, which takes float32, y is the
+    adapted projection."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return lora(x, a, b, ids, scale, r, out, workspace)

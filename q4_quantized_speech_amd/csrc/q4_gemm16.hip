@@ -418,7 +418,7 @@ struct Stage {
 };
 
 // Measured, 256 x 256 tiles: 375 x 3072 over 32768 with three products per pair
-// 236 us (956 TFLOP/s of binary16), 1500 with one 304 us (993); the matrix cores
+// 227 us (998 TFLOP/s of binary16), 1500 with one 296 us (1020); the matrix cores
 // are busy 43 % of the time, the rest waits on LDS and on the loads of the next
 // stage.
 template <typename S, int PA, int PB, int KS>
@@ -586,8 +586,8 @@ __device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0
   }
 }
 
-// Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 182 us, 1500 in
-// one 361 us (830 and 836 TFLOP/s of binary16).  The block scale's FMAs keep the
+// Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 179 us, 1500 in
+// one 354 us (845 and 853 TFLOP/s of binary16).  The block scale's FMAs keep the
 // vector unit busy 48 % of the time beside the matrix cores' 33 %.
 template <typename S, int PA, int KS, bool STATS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
@@ -894,7 +894,8 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 //
 // A block's 32 rows x 72 bytes go to the wave's own LDS as they are, by DMA of
 // consecutive dwords (each lane's codes straight from memory, 20 loads of four
-// rows a block: 39.9 us against 38.7 at 1500 x 5120 x 1280 bfloat16).  A lane
+// rows a block: 39.9 us against 38.7 at 1500 x 5120 x 1280 bfloat16 with one
+// part of the weights).  A lane
 // (i, g) takes one dword of codes of block i / 4 of the 128 columns from each
 // of the rows 8 g .. 8 g + 7: eight rows of eight columns, turned
 // in registers into the operands of the columns k = 32 (i / 4) + 4 (i % 4) +
@@ -905,8 +906,9 @@ void logits_direct_kernel(const f16x8* __restrict__ A, const uint8_t* __restrict
 // ---------------------------------------------------------------------------
 constexpr int TW = 8;  // waves
 
-// Measured: 1500 x 5120 x 1280 bfloat16 39 us (503 TFLOP/s), 375 x 1280 x 5120
-// float32 23 us (three products per pair: 640), 16 x 3072 x 4096 float32 8.1 us.
+// Measured: 1500 x 5120 x 1280 bfloat16 49 us (two products per pair: 800
+// TFLOP/s; one, with the weights rounded, 39), 375 x 1280 x 5120 float32 23.9 us
+// (three: 620), 16 x 3072 x 4096 float32 8.2 us.
 // Waves wait 41 to 44 % of their cycles, mostly for a block's bytes: two per SIMD
 // do not cover them.
 template <int RT, int PA, int PB, typename T, bool ODD>
@@ -1287,7 +1289,7 @@ struct DxPlan {
 DxPlan dx_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   DxPlan p;
   p.pa = type == TYPE_F32 ? 2 : 1;
-  p.pb = 2;  // the weights are exact, as the plain form's
+  p.pb = 2;  // exact weights: rounded ones show where a sum's terms cancel
   const int units = p.pa + p.pb - 1;
   p.rows = (N + 63) / 64 * 64;
   double best = 1e30;

@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(
 }
 
 // Rank vectors of a group as three bfloat16 parts (exact: two would leave up to
-// 2^-15 of them out, 1500 rows of rank 64 in bfloat16 25.1 us against 25.5) in
+// 2^-15 of them out, 1500 rows of rank 64 in bfloat16 25.5 us against 26.1) in
 // LDS, hs[part][member][ld]:
 // scale * (the slices' sum); zero past the last member and for j in [R, R
 // rounded up to 32).  ld = that + 8: rows 16-byte aligned, on different banks.
@@ -625,7 +625,8 @@ __device__ __forceinline__ void dx_body(const float* __restrict__ G, const TA* _
     __syncthreads();
     const TA* ad = A + static_cast<int64_t>(a) * R * K;
     // blocks of 16 rows at a time: two leave the registers for two workgroups on
-    // a CU (1500 x 5120 x 1280, rank 32: 30.6 -> 18.0 us for the kernel)
+    // a CU (1500 x 5120 x 1280, rank 32: 30.6 -> 18.0 us for the kernel, with two
+    // parts of the rank vectors)
     constexpr int NS = sizeof(T) == 2 ? 2 : SUB;
     for (int64_t base = k0 + 64 * wave; base < k1; base += 64 * WAVES) {
       const int64_t k = min(base + 4 * i, K - 4);
@@ -823,8 +824,8 @@ __device__ __forceinline__ void outer_body(const float* __restrict__ L, const T*
 // Last launch of the backward pass: workgroups [0, dxblocks) dx, the next
 // adapters * achunks dA, the rest dB.
 constexpr int G_WAVES = 8;
-// Measured: 76 rows, rank 8 float32 10 us; 1500 rows, rank 32 bfloat16 18 us (34 MB,
-// 1.9 TB/s).  Each adapter's workgroups look through all rows' ids for theirs.
+// Measured: 76 rows, rank 8 float32 10 us; 1500 rows, rank 32 bfloat16 19 us (34 MB,
+// 1.8 TB/s).  Each adapter's workgroups look through all rows' ids for theirs.
 template <typename T, typename TA, int RT>
 __global__ __launch_bounds__(64 * G_WAVES, RT <= 2 && sizeof(T) == 2 ? 4 : 2) void lora_grad_kernel(
     const float* __restrict__ H, const float* __restrict__ G, const uint16_t* __restrict__ HT,
