@@ -428,6 +428,66 @@ q4_status q4_lora_grad(const void* x, const void* dy, const void* a, const void*
                        void* stream);
 
 /*
+ * Operators of a draft model (section "Architecture": the decoder generates
+ * one token at a time, each pass reading every weight): a small draft with the
+ * same kind of blocks proposes tokens, which the large model verifies several
+ * at a time.  The gated block is what both are made of, forward and backward;
+ * distillation trains the draft on the large model's best logits.  Element
+ * types as above: activations and their gradients share one.
+ */
+enum { Q4_ACT_SILU = 0, Q4_ACT_GELU = 1 };  /* g * sigmoid(g); gelu in its tanh form */
+
+/*
+ * q4_gated_ffn -- the first half of a gated feed-forward block: both
+ * projections, the activation and the product,
+ *   g = r[m, n] + sum_k deq(Wg)[n, k] x[m, k],
+ *   u = r[m, N + n] + sum_k deq(Wu)[n, k] x[m, k],   h[m, n] = act(g) u.
+ *   w_gate, w_up : N rows of Q4_0 each (of one tensor, or of two).
+ *   x : [M, K].   h : [M, N] (written).
+ *   r : [M, 2 N], gate then up, or NULL (zeros): what adapters add to the two
+ *       projections (q4_lora's y with N = 2 N).
+ *   z : [M, 2 N] or NULL: (g, u), rounded, for q4_gated_ffn_grad.  h is
+ *       computed from g and u before that rounding.  z may be r.
+ *   1 <= M <= 2^20, 1 <= N <= 2097152, K a positive multiple of 32 up to
+ *   4194304, M*N and M*K below 2^33, N*K below 2^33.
+ *   workspace : q4_gated_ffn_workspace_bytes(type, M, N, K) bytes of device
+ *           scratch (0 for few rows: NULL allowed); its contents do not
+ *           matter.  Calls that share it must be ordered.
+ * Exact codes on the matrix cores, each block's scale applied in float32,
+ * float32 sums.  x enters exactly (float32 as bfloat16 parts), or above 64 rows
+ * scaled per row by a power of two into binary16 (float32 rows as two parts):
+ * to 2^-22 of an element or 2^-39 of its row's largest.  Deterministic; an
+ * infinity or NaN in a row of x gives non-finite values in that row only.
+ */
+size_t q4_gated_ffn_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);
+q4_status q4_gated_ffn(const void* w_gate, const void* w_up, const void* x, const void* r, void* h,
+                       void* z, int32_t act, int32_t type, int64_t M, int64_t N, int64_t K,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * q4_gated_ffn_grad -- the gradient of q4_gated_ffn for dh, the gradient of
+ * its h, with z = (g, u) as q4_gated_ffn wrote it:
+ *   dg = dh u act'(g),   du = dh act(g),   dx = dg deq(Wg) + du deq(Wu).
+ *   z  : [M, 2 N].   dh : [M, N].
+ *   dx : [M, K] or NULL (written).
+ *   dz : [M, 2 N] or NULL: (dg, du), the gradient of r and of adapters beside
+ *        the projections (q4_lora_grad's dy).  At least one of dx, dz is
+ *        given.  dz may be z.
+ *   Ranges as for q4_gated_ffn.
+ *   workspace : q4_gated_ffn_grad_workspace_bytes(type, M, N, K) bytes; as
+ *           above.  Without dx none is needed.
+ * dx: exact weights, float32 sums, dg and du before their rounding to dz's
+ * type, scaled per row by a power of two into binary16: to 2^-22 in float32
+ * (two parts), 2^-12 in the 16-bit types (one, half of a binary16 step), or
+ * 2^-33 of max|dh| max|z| of the row.  Deterministic; a row that holds an
+ * infinity or NaN gives non-finite values in that row only.
+ */
+size_t q4_gated_ffn_grad_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);
+q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z, const void* dh,
+                            void* dx, void* dz, int32_t act, int32_t type, int64_t M, int64_t N,
+                            int64_t K, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * GGUF reader (host code, no GPU) -- the container of the pages' quantised
  * model (section "Architecture": a GGUF Q4_0 file; section "Préparation du
  * modèle et sharding": the file is cut into byte pieces of at most 512 MB).

@@ -16,6 +16,8 @@ Entry points (same names as the C ABI, minus the ``q4_`` prefix):
     lmhead_xent(w_q4, x, targets, grad=False)    cross entropy of the head, and its gradient
     lora(x, a, b, ids, scale=None, r=None, ...)  y = r + s_a B_a (A_a x), a = ids[row]
     lora_grad(x, dy, a, b, ids, ...)             its gradient: dx, da, db
+    gated_ffn(w_gate, w_up, x, act, r, ...)      h = act(g) u, the gated block's projections
+    gated_ffn_grad(w_gate, w_up, z, dh, ...)     its gradient: dx, dz
 
 Q4_0 tensors are ``torch.uint8`` of shape [N, 18*K/32] (rows of 32-weight
 blocks: binary16 scale + 16 bytes of nibbles, as stored in GGUF).
@@ -81,6 +83,10 @@ _SIGS = {
     "q4_lora": ([_P] * 7 + [ctypes.c_int32] * 2 + [_I64] * 5 + [_P, _SZ, _P], ctypes.c_int),
     "q4_lora_grad_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
     "q4_lora_grad": ([_P] * 10 + [ctypes.c_int32] * 2 + [_I64] * 5 + [_P, _SZ, _P], ctypes.c_int),
+    "q4_gated_ffn_workspace_bytes": ([ctypes.c_int32] + [_I64] * 3, _SZ),
+    "q4_gated_ffn": ([_P] * 6 + [ctypes.c_int32] * 2 + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
+    "q4_gated_ffn_grad_workspace_bytes": ([ctypes.c_int32] + [_I64] * 3, _SZ),
+    "q4_gated_ffn_grad": ([_P] * 6 + [ctypes.c_int32] * 2 + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
     "q4_gguf_open": ([_P, _I64, _P], ctypes.c_int),
     "q4_gguf_close": ([_P], None),
     "q4_gguf_version": ([_P], ctypes.c_uint32),
@@ -629,6 +635,84 @@ def lora_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tenso
         return lora_grad(x, dy, a, b, again[0], again[1], r, dx, da, db, ws)
     _check(status, "q4_lora_grad")
     return dx, da, db
+
+
+# Activations of the gated block (Q4_ACT_* of the ABI).
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _gated(w_gate: torch.Tensor, w_up: torch.Tensor, act: str):
+    """(activation code, N, K) of a gated block's projections."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(map(repr, _ACTS))}, got {act!r}")
+    n, k = q4_shape(w_gate)
+    if q4_shape(w_up) != (n, k):
+        raise ValueError("w_gate and w_up must have the same shape")
+    return _ACTS[act], n, k
+
+
+def gated_ffn(w_gate: torch.Tensor, w_up: torch.Tensor, x: torch.Tensor, act: str = "silu",
+              r: torch.Tensor | None = None, keep: bool = False, out: torch.Tensor | None = None,
+              z: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(h, z): h = act(g) u with (g, u) = r + x (deq(Wg), deq(Wu))^T, the first half of a gated
+    feed-forward block.  x is [M, K] of float32, float16 or bfloat16, the others of its type:
+    r [M, 2 N] (zeros if None) what adapters add to the two projections, as
+    ``lora(x, a, b, ids)`` with b of 2 N rows gives it; h [M, N]; z [M, 2 N], with ``keep`` (or
+    a ``z`` to write, which may be r), (g, u) for ``gated_ffn_grad``, else None.  act is "silu"
+    or "gelu" (its tanh form).  Above 64 rows the workspace holds the unpacked codes of both
+    projections, 2 bytes each (113 MB for 9216 x 3072)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_ffn(w_gate, w_up, x, act, r, keep, out, z, workspace)
+    code, n, k = _gated(w_gate, w_up, act)
+    t = _activations(x, "x")
+    m, k2 = x.shape
+    if k2 != k:
+        raise ValueError(f"x must be [M, {k}]")
+    for v, name, width in ((r, "r", 2 * n), (out, "out", n), (z, "z", 2 * n)):
+        if v is not None:
+            _matrix(v, name, (m, width), x.dtype)
+    dev = _gpu(w_gate, w_up, x, r, out, z)
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    if keep and z is None:
+        z = torch.empty((m, 2 * n), dtype=x.dtype, device=x.device)
+    ws = _scratch(workspace, "q4_gated_ffn_workspace_bytes", dev, t, m, n, k)
+    _check(lib().q4_gated_ffn(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), _addr(r),
+                              out.data_ptr(), _addr(z), code, t, m, n, k, ws.data_ptr(), ws.numel(),
+                              _raw_stream(dev)), "q4_gated_ffn")
+    return out, z
+
+
+def gated_ffn_grad(w_gate: torch.Tensor, w_up: torch.Tensor, z: torch.Tensor, dh: torch.Tensor,
+                   act: str = "silu", keep: bool = False, dx: torch.Tensor | None = None,
+                   dz: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None):
+    """(dx, dz): the gradient of ``gated_ffn`` for dh [M, N], the gradient of its h, from the z
+    it kept.  dx is [M, K]; dz [M, 2 N], with ``keep`` (or a ``dz`` to write, which may be z),
+    the gradient of r and the dy of ``lora_grad`` for adapters beside the projections, else
+    None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_ffn_grad(w_gate, w_up, z, dh, act, keep, dx, dz, workspace)
+    code, n, k = _gated(w_gate, w_up, act)
+    t = _activations(z, "z")
+    m, n2 = z.shape
+    if n2 != 2 * n:
+        raise ValueError(f"z must be [M, {2 * n}]")
+    for v, name, width in ((dh, "dh", n), (dx, "dx", k), (dz, "dz", 2 * n)):
+        if v is not None:
+            _matrix(v, name, (m, width), z.dtype)
+    dev = _gpu(w_gate, w_up, z, dh, dx, dz)
+    if dx is None:
+        dx = torch.empty((m, k), dtype=z.dtype, device=z.device)
+    if keep and dz is None:
+        dz = torch.empty((m, 2 * n), dtype=z.dtype, device=z.device)
+    ws = _scratch(workspace, "q4_gated_ffn_grad_workspace_bytes", dev, t, m, n, k)
+    _check(lib().q4_gated_ffn_grad(w_gate.data_ptr(), w_up.data_ptr(), z.data_ptr(), dh.data_ptr(),
+                                   dx.data_ptr(), _addr(dz), code, t, m, n, k, ws.data_ptr(),
+                                   ws.numel(), _raw_stream(dev)), "q4_gated_ffn_grad")
+    return dx, dz
 
 
 GGUF_F32, GGUF_F16, GGUF_Q4_0, GGUF_Q8_0, GGUF_BF16 = 0, 1, 2, 8, 30

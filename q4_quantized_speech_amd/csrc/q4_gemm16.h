@@ -94,6 +94,10 @@ struct TransposedGemm {
   float* part;
   const float *alpha, *inv;
   void* out;
+  // w2 (nullable): a second matrix of N rows with its own G; its slices follow
+  // the first one's in part
+  const f16x8* g2;
+  const uint8_t* w2;
 };
 struct TransposedPlan {
   double us;  // estimate

@@ -84,6 +84,32 @@ size_t matmul_dx_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int 
 hipError_t launch_matmul_dx(const uint8_t* w, const void* dy, void* dx, int type, int64_t M,
                             int64_t N, int64_t K, void* ws, int cus, hipStream_t s);
 
+// The gated feed-forward block (arguments as in q4_gated_ffn and
+// q4_gated_ffn_grad).
+constexpr int ACT_SILU = 0, ACT_GELU = 1;
+struct FfnArgs {
+  const uint8_t *gate, *up;
+  const void *x, *r;
+  void *h, *z;
+  int act, type;
+  int64_t M, N, K;
+  void* ws;
+  hipStream_t stream;
+};
+size_t ffn_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_ffn(const FfnArgs& a, int cus);
+struct FfnGradArgs {
+  const uint8_t *gate, *up;
+  const void *z, *dh;
+  void *dx, *dz;
+  int act, type;
+  int64_t M, N, K;
+  void* ws;
+  hipStream_t stream;
+};
+size_t ffn_grad_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus);
+
 // Cross entropy of the head; dx null: the loss alone.
 size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, const float* dloss,
