@@ -488,6 +488,85 @@ q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z,
                             int64_t K, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * q4_lmhead_distill -- distillation of a teacher's best logits through the
+ * Q4_0 LM head, and its gradient, in pieces of the vocabulary as in
+ * q4_lmhead_xent.  With l[n] = sum_k deq(T)[n, k] x[m, k] / temperature,
+ * p = softmax(l) and q the softmax of the row's top_logits / temperature:
+ *   lse[m]  = log sum_n exp l[n],
+ *   loss[m] = temperature^2 sum_j q_j (log q_j - log p[top_ids[m, j]]),
+ *   dx[m]   = dloss[m] temperature (sum_n p[n] deq(T)[n, :]
+ *                                   - sum_j q_j deq(T)[top_ids[m, j], :]).
+ *   w_q4    : N rows of Q4_0.   x : [M, K].
+ *   top_ids, top_logits : [M, top] int32 and float32 (device).  An entry whose
+ *             id is outside [0, N) is absent (whatever its logit), so rows may
+ *             hold fewer; the probabilities of entries with one id add up.  A
+ *             row without an entry, or with logits of -inf alone, has loss 0
+ *             and dx 0.
+ *   temperature : from 2^-60 to 2^60 (Q4_ERR_SHAPE otherwise).
+ *   loss, lse, dloss, dx : as for q4_lmhead_xent.
+ *   1 <= top <= 256; the other ranges are q4_lmhead_xent's.
+ *   workspace : q4_lmhead_distill_workspace_bytes(type, dx != NULL, M, N, K,
+ *           top) bytes of device scratch; its contents do not matter.  Calls
+ *           that share it must be ordered.
+ * Logits, maxima and sums are float32 over exact weights.  In the gradient the
+ * teacher's tokens are taken out of the sum over the vocabulary and p - q is
+ * formed for each of them in float32, so a student near its teacher keeps the
+ * precision of the difference; the other probabilities are kept relative to
+ * their largest and rounded as in q4_lmhead_xent.  |deq(T)| must stay below
+ * 65504 for dx.  Deterministic; a row of x that holds an infinity or NaN, or
+ * one of top_logits that holds NaN or +inf in a present entry, gives
+ * non-finite values in that row only.
+ */
+size_t q4_lmhead_distill_workspace_bytes(int32_t type, int32_t grad, int64_t M, int64_t N,
+                                         int64_t K, int64_t top);
+q4_status q4_lmhead_distill(const void* w_q4, const void* x, const int32_t* top_ids,
+                            const float* top_logits, double temperature, const float* dloss,
+                            float* loss, float* lse, void* dx, int32_t type, int64_t M, int64_t N,
+                            int64_t K, int64_t top, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * q4_verify_draft -- how many of a draft's tokens stand, and the token after
+ * them, for many sequences at once, from given random numbers.  With
+ * p_i = softmax(logits[s, i] / temperature), the large model's distribution
+ * after i drafted tokens, and q_i the draft's own:
+ *   token i stands if all before it do, i < lens[s] and
+ *       u[s, i] q_i(draft[s, i]) < p_i(draft[s, i]);
+ *   accepted[s] = a, the number that stand;
+ *   the next token is drawn from max(p_a - q_a, 0) if a < lens[s], from p_a
+ *       otherwise: the lowest n with c_n > u[s, D] c_(N-1), c_n the sum of the
+ *       entries 0 .. n of that distribution (not normalised).
+ * Tokens so drawn have the large model's distribution, whatever the draft.
+ *   logits : [S, D + 1, N].
+ *   draft  : [S, D] int32 (NULL allowed for D = 0: a plain draw).  An id
+ *            outside [0, N) does not stand.
+ *   probs  : [S, D, N], the draft's probabilities, of logits' type, or NULL:
+ *            the draft was certain of its tokens (q_i is 1 at draft[s, i]).
+ *   u      : [S, D + 1] float32 uniform numbers in [0, 1).
+ *   lens   : S int32, drafted tokens of each sequence, or NULL (D); values
+ *            outside [0, D] count as the nearer end.
+ *   temperature : 0, or from 2^-60 to 2^60 (Q4_ERR_SHAPE otherwise); 0: p_i
+ *            is 1 at the lowest index of the largest logit (greedy).
+ *   tokens : [S, D + 1] int32: the tokens that stand, the next one, -1s.
+ *   accepted : S int32.
+ *   1 <= S <= 2^20, 0 <= D <= 63, 1 <= N < 2^31, S*(D + 1)*N below 2^40.
+ *   workspace : q4_verify_draft_workspace_bytes(S, D, N) bytes of device
+ *            scratch; its contents do not matter.  Calls that share it must be
+ *            ordered.
+ * Probabilities and sums are float64 from the logits on, so the tokens do not
+ * depend on the order of the sums but for draws within about 1e-13 of a border.
+ * Logits of -inf are masked tokens.  Where a row of logits holds NaN or its
+ * largest is infinite there is no distribution: no token stands there, and the
+ * next token is -1 if it is drawn there.  A distribution of zeros (nothing of p
+ * is above q) is replaced by p_a.  Deterministic.
+ */
+size_t q4_verify_draft_workspace_bytes(int64_t S, int64_t D, int64_t N);
+q4_status q4_verify_draft(const void* logits, const int32_t* draft, const void* probs,
+                          const float* u, const int32_t* lens, double temperature, int32_t* tokens,
+                          int32_t* accepted, int32_t type, int64_t S, int64_t D, int64_t N,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * GGUF reader (host code, no GPU) -- the container of the pages' quantised
  * model (section "Architecture": a GGUF Q4_0 file; section "Préparation du
  * modèle et sharding": the file is cut into byte pieces of at most 512 MB).

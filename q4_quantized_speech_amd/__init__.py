@@ -18,6 +18,8 @@ Entry points (same names as the C ABI, minus the ``q4_`` prefix):
     lora_grad(x, dy, a, b, ids, ...)             its gradient: dx, da, db
     gated_ffn(w_gate, w_up, x, act, r, ...)      h = act(g) u, the gated block's projections
     gated_ffn_grad(w_gate, w_up, z, dh, ...)     its gradient: dx, dz
+    lmhead_distill(w_q4, x, top_ids, ...)        loss of the head against a teacher's best logits
+    verify_draft(logits, draft, u, probs, ...)   drafted tokens that stand, and the next one
 
 Q4_0 tensors are ``torch.uint8`` of shape [N, 18*K/32] (rows of 32-weight
 blocks: binary16 scale + 16 bytes of nibbles, as stored in GGUF).
@@ -87,6 +89,12 @@ _SIGS = {
     "q4_gated_ffn": ([_P] * 6 + [ctypes.c_int32] * 2 + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
     "q4_gated_ffn_grad_workspace_bytes": ([ctypes.c_int32] + [_I64] * 3, _SZ),
     "q4_gated_ffn_grad": ([_P] * 6 + [ctypes.c_int32] * 2 + [_I64] * 3 + [_P, _SZ, _P], ctypes.c_int),
+    "q4_lmhead_distill_workspace_bytes": ([ctypes.c_int32] * 2 + [_I64] * 4, _SZ),
+    "q4_lmhead_distill": ([_P] * 4 + [ctypes.c_double] + [_P] * 4 + [ctypes.c_int32] + [_I64] * 4
+                          + [_P, _SZ, _P], ctypes.c_int),
+    "q4_verify_draft_workspace_bytes": ([_I64] * 3, _SZ),
+    "q4_verify_draft": ([_P] * 5 + [ctypes.c_double] + [_P] * 2 + [ctypes.c_int32] + [_I64] * 3
+                        + [_P, _SZ, _P], ctypes.c_int),
     "q4_gguf_open": ([_P, _I64, _P], ctypes.c_int),
     "q4_gguf_close": ([_P], None),
     "q4_gguf_version": ([_P], ctypes.c_uint32),
@@ -713,6 +721,107 @@ def gated_ffn_grad(w_gate: torch.Tensor, w_up: torch.Tensor, z: torch.Tensor, dh
                                    dx.data_ptr(), _addr(dz), code, t, m, n, k, ws.data_ptr(),
                                    ws.numel(), _raw_stream(dev)), "q4_gated_ffn_grad")
     return dx, dz
+
+
+def lmhead_distill(w_q4: torch.Tensor, x: torch.Tensor, top_ids: torch.Tensor,
+                   top_logits: torch.Tensor, temperature: float = 1.0, grad: bool = False,
+                   dloss: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """(loss, lse, dx): per row of x, temperature^2 times the divergence of the student's
+    p = softmax(deq(T) x / temperature) from the teacher's q, the softmax of the row's
+    top_logits / temperature (float32 [M, top], 1 to 256) at the tokens top_ids (int32
+    [M, top]): sum q (log q - log p); lse = logsumexp(deq(T) x / temperature); and with
+    ``grad`` (or a ``dx`` to write) the gradient of sum(dloss * loss) with respect to x, in
+    x's type; dx is None otherwise.  Entries whose token is outside [0, N) are absent, those of
+    one token add up; rows without any have loss 0 and dx 0.  Memory as for ``lmhead_xent``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lmhead_distill(w_q4, x, top_ids, top_logits, temperature, grad, dloss, loss, lse,
+                                  dx, workspace)
+    n, k = q4_shape(w_q4)
+    t = _activations(x, "x")
+    m, k2 = x.shape
+    if k2 != k:
+        raise ValueError(f"x must be [M, {k}]")
+    if top_ids.dim() != 2:
+        raise ValueError("top_ids must be [M, top]")
+    top = top_ids.shape[1]
+    _matrix(top_ids, "top_ids", (m, top), torch.int32)
+    _matrix(top_logits, "top_logits", (m, top), torch.float32)
+    for v, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
+        if v is not None:
+            _matrix(v, name, (m,), torch.float32)
+    if dx is not None:
+        _matrix(dx, "dx", (m, k), x.dtype)
+        grad = True
+    dev = _gpu(w_q4, x, top_ids, top_logits, dloss, loss, lse, dx)
+    if loss is None:
+        loss = torch.empty(m, dtype=torch.float32, device=x.device)
+    if lse is None:
+        lse = torch.empty(m, dtype=torch.float32, device=x.device)
+    if grad and dx is None:
+        dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+    ws = _scratch(workspace, "q4_lmhead_distill_workspace_bytes", dev, t, int(bool(grad)), m, n, k,
+                  top)
+    status = lib().q4_lmhead_distill(w_q4.data_ptr(), x.data_ptr(), top_ids.data_ptr(),
+                                     top_logits.data_ptr(), temperature, _addr(dloss),
+                                     loss.data_ptr(), lse.data_ptr(), _addr(dx), t, m, n, k, top,
+                                     ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    again = _realigned(status, top_ids, top_logits, dloss)
+    if again:
+        return lmhead_distill(w_q4, x, again[0], again[1], temperature, grad, again[2], loss, lse,
+                              dx, ws)
+    _check(status, "q4_lmhead_distill")
+    return loss, lse, dx
+
+
+def verify_draft(logits: torch.Tensor, draft: torch.Tensor, u: torch.Tensor,
+                 probs: torch.Tensor | None = None, lens: torch.Tensor | None = None,
+                 temperature: float = 1.0, tokens: torch.Tensor | None = None,
+                 accepted: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None):
+    """(tokens, accepted): for each of S sequences, how many of its drafted tokens stand
+    (int32 [S]), and those tokens, the one after them and -1s (int32 [S, D + 1]).  logits is
+    [S, D + 1, N] (float32, float16 or bfloat16), the large model's after 0 .. D drafted tokens,
+    as ``matmul`` with the head gives them; draft int32 [S, D]; probs [S, D, N] of logits' type
+    the draft's probabilities, or None: it was certain of its tokens; u float32 [S, D + 1] in
+    [0, 1), column i for drafted token i and the last for the draw; lens int32 [S], drafted
+    tokens of each sequence (D if None); temperature 0 is greedy."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_draft(logits, draft, u, probs, lens, temperature, tokens, accepted,
+                                workspace)
+    t = _TYPES.get(logits.dtype)
+    if t is None or logits.dim() != 3 or not logits.is_contiguous() or logits.shape[1] < 1:
+        raise ValueError("logits must be a contiguous [S, D + 1, N] tensor of float32, float16 or "
+                         "bfloat16")
+    s, d, n = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+    _matrix(draft, "draft", (s, d), torch.int32)
+    _matrix(u, "u", (s, d + 1), torch.float32)
+    if probs is not None:
+        _matrix(probs, "probs", (s, d, n), logits.dtype)
+    if lens is not None:
+        _matrix(lens, "lens", (s,), torch.int32)
+    if tokens is not None:
+        _matrix(tokens, "tokens", (s, d + 1), torch.int32)
+    if accepted is not None:
+        _matrix(accepted, "accepted", (s,), torch.int32)
+    dev = _gpu(logits, draft, u, probs, lens, tokens, accepted)
+    if tokens is None:
+        tokens = torch.empty((s, d + 1), dtype=torch.int32, device=logits.device)
+    if accepted is None:
+        accepted = torch.empty(s, dtype=torch.int32, device=logits.device)
+    ws = _scratch(workspace, "q4_verify_draft_workspace_bytes", dev, s, d, n)
+    status = lib().q4_verify_draft(logits.data_ptr(), draft.data_ptr(), _addr(probs), u.data_ptr(),
+                                   _addr(lens), temperature, tokens.data_ptr(), accepted.data_ptr(),
+                                   t, s, d, n, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    again = _realigned(status, draft, u, lens)
+    if again:
+        return verify_draft(logits, again[0], again[1], probs, again[2], temperature, tokens,
+                            accepted, ws)
+    _check(status, "q4_verify_draft")
+    return tokens, accepted
 
 
 GGUF_F32, GGUF_F16, GGUF_Q4_0, GGUF_Q8_0, GGUF_BF16 = 0, 1, 2, 8, 30

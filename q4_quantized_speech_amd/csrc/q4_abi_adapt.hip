@@ -68,7 +68,7 @@ q4_status q4_matmul_dx(const void* w_q4, const void* dy, void* dx, int32_t type,
 size_t q4_lmhead_xent_workspace_bytes(int32_t type, int32_t grad, int64_t M, int64_t N,
                                       int64_t K) {
   if (!type_ok(type) || !xent_shape_ok(M, N, K)) return 0;
-  return xent_workspace_bytes(type, grad != 0, M, N, K, device_info().cu_count);
+  return xent_workspace_bytes(type, grad != 0, M, N, K, 0, device_info().cu_count);
 }
 
 q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets,
@@ -82,10 +82,10 @@ q4_status q4_lmhead_xent(const void* w_q4, const void* x, const int32_t* targets
       !aligned16(loss) || !aligned16(lse) || !aligned16(dx) || !aligned16(workspace))
     return Q4_ERR_ALIGN;
   const int cus = device_info().cu_count;
-  if (!workspace || ws_bytes < xent_workspace_bytes(type, dx != nullptr, M, N, K, cus))
+  if (!workspace || ws_bytes < xent_workspace_bytes(type, dx != nullptr, M, N, K, 0, cus))
     return Q4_ERR_WORKSPACE;
-  return hip_status(launch_xent(static_cast<const uint8_t*>(w_q4), x, targets, dloss, loss, lse, dx,
-                                type, M, N, K, workspace, cus, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_xent(static_cast<const uint8_t*>(w_q4), x, targets, nullptr, dloss, loss,
+                                lse, dx, type, M, N, K, workspace, cus, static_cast<hipStream_t>(stream)));
 }
 
 size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {

@@ -563,12 +563,6 @@ using std::integral_constant;
 template <int V>
 using Int = integral_constant<int, V>;
 
-template <typename F>
-void with_type(int type, F f) {
-  if (type == TYPE_F32) f(float{});
-  else if (type == TYPE_F16) f(_Float16{});
-  else f(__bf16{});
-}
 
 #define Q4_TRY(expr)                          \
   do {                                        \

@@ -110,10 +110,35 @@ struct FfnGradArgs {
 size_t ffn_grad_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus);
 
-// Cross entropy of the head; dx null: the loss alone.
-size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int cus);
-hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets, const float* dloss,
-                       float* loss, float* lse, void* dx, int type, int64_t M, int64_t N, int64_t K,
+// Cross entropy of the head against targets, or (teacher not null, targets
+// null) against a teacher's softmax over `top` entries a row; dx null: the loss
+// alone.
+struct TeacherArgs {
+  const int32_t* ids;
+  const float* logits;
+  int64_t top;
+  double temperature;
+};
+size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int64_t top, int cus);
+hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
+                       const TeacherArgs* teacher, const float* dloss, float* loss, float* lse, void* dx, int type, int64_t M, int64_t N, int64_t K,
                        void* ws, int cus, hipStream_t s);
+
+// Verification of drafted tokens (arguments as in q4_verify_draft).
+struct VerifyArgs {
+  const void* logits;
+  const int32_t* draft;
+  const void* probs;
+  const float* u;
+  const int32_t* lens;
+  double temperature;
+  int32_t *tokens, *accepted;
+  int type;
+  int64_t S, D, N;
+  void* ws;
+  hipStream_t stream;
+};
+size_t verify_workspace_bytes(int64_t S, int64_t D, int64_t N);
+hipError_t launch_verify(const VerifyArgs& v);
 
 }  // namespace q4

@@ -16,6 +16,14 @@ constexpr int TYPE_F32 = 0, TYPE_F16 = 1, TYPE_BF16 = 30;
 inline bool type_ok(int t) { return t == TYPE_F32 || t == TYPE_F16 || t == TYPE_BF16; }
 inline int type_bytes(int t) { return t == TYPE_F32 ? 4 : 2; }
 
+// f called with a value of the type's C++ type.
+template <typename F>
+void with_type(int t, F f) {
+  if (t == TYPE_F32) f(float{});
+  else if (t == TYPE_F16) f(_Float16{});
+  else f(__bf16{});
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(_Float16 v) { return static_cast<float>(v); }
 __device__ __forceinline__ float to_f32(__bf16 v) { return static_cast<float>(v); }
