@@ -21,6 +21,9 @@
 namespace q4 {
 namespace {
 
+template <int V>
+using Int = std::integral_constant<int, V>;
+
 // ---------------------------------------------------------------------------
 // Activations.  With s = sigmoid(a), 1 - s from the exponential as well: the
 // derivative keeps its precision on both sides.
@@ -83,19 +86,16 @@ __device__ __forceinline__ void finish(const Out& o, int64_t m, int64_t n, float
 
 // ---------------------------------------------------------------------------
 // Few rows, straight from the Q4_0 bytes.  A workgroup owns 16 NT columns of
-// each projection; its eight waves share them and take every eighth chunk of
-// 128 k, and their sums are added in LDS at the end: all of a short matrix's
-// bytes are requested at once, whatever its height.
+// each projection; its waves share them and take every nw-th chunk of 256 k,
+// and their sums are added in LDS at the end: most of a matrix's bytes are
+// requested at once, whatever its height.
 //
-// Lane (i, g) loads block g of the chunk of weight row i: a 16-bit scale and 16
-// bytes of codes, at any even address.  A 4 x 4 transposition over the lane
-// groups gives it dword g of each of the four blocks, the operand of the exact
-// codes q - 8, and the scales of all four.
+// Lane (i, g) loads the block pair g of the chunk of weight row i: 36 bytes.
+// 4 x 4 transpositions over the lane groups give it dword g of each of the
+// eight blocks, the operand of the exact codes q - 8.
 // ---------------------------------------------------------------------------
-constexpr int FW = 8;            // waves
+constexpr int FW = 8;            // waves at most
 constexpr int64_t FEW_ROWS = 64; // rows of x this route takes
-
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // Row g (lanes 16 g .. 16 g + 15) of r[t] holds X[g][t]; afterwards row g of
 // r[p] holds X[p][g].
@@ -110,6 +110,17 @@ __device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
   r[3] = d[1];
 }
 
+// The power of two that brings `top` to [2^14, 2^15) (at most 2^126: for zero and
+// the smallest numbers), and its inverse.
+struct PowerOfTwo {
+  float s, inv;
+  __device__ __forceinline__ explicit PowerOfTwo(float top) {
+    const int e = min(268 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+    s = __uint_as_float(static_cast<uint32_t>(e) << 23);
+    inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  }
+};
+
 // The largest over the four lane groups, in all of them.
 __device__ __forceinline__ float groups_max(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -120,83 +131,150 @@ __device__ __forceinline__ float groups_max(float v) {
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// This lane's blocks of a chunk, one of each of the workgroup's row tiles.
-template <int TILES>
+// The largest over LANES (32 or 64) neighbours, in all of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, dpp_f32<0xB1>(v));
+  v = fmaxf(v, dpp_f32<0x4E>(v));
+  v = fmaxf(v, dpp_f32<0x141>(v));
+  v = fmaxf(v, dpp_f32<0x140>(v));
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  if constexpr (LANES == 64) {
+    const uint32_t w = __float_as_uint(v);
+    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    v = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  }
+  return v;
+}
+
+// This lane's block pairs of a chunk, one of each of the workgroup's row tiles.
+// ODD: K is an odd multiple of 32; rows start at any even address and end with
+// half a pair, the other half of which may lie outside the matrix.
+typedef uint32_t u32x4_at __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32_at __attribute__((aligned(2)));
+template <int TILES, bool ODD>
 struct RawChunk {
-  uint32_t q[TILES][4];
-  int d[TILES];  // bits of the scale
-  __device__ __forceinline__ void load(const uint8_t* const (&row)[TILES], int64_t c, int g, int64_t CB) {
-    const int64_t off = min(4 * c + g, CB - 1) * BLOCK_BYTES;
+  uint32_t w[TILES][9];
+  // row: this lane's pair of each tile; half: it is half a pair
+  __device__ __forceinline__ void load_pair(const uint8_t* const (&row)[TILES], bool half) {
+    if (ODD && half) {
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(row[t]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[t][e] = h[2 * e] | static_cast<uint32_t>(h[2 * e + 1]) << 16;
+        w[t][4] = h[8];  // the second block's scale: 0
+#pragma unroll
+        for (int e = 5; e < 9; ++e) w[t][e] = 0;
+      }
+      return;
+    }
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      const u32x4 v = *reinterpret_cast<const u32x4_any*>(row[t] + off + 2);
-      d[t] = *reinterpret_cast<const uint16_t*>(row[t] + off);
-      q[t][0] = v.x; q[t][1] = v.y; q[t][2] = v.z; q[t][3] = v.w;
+      const u32x4 a = *reinterpret_cast<const u32x4_at*>(row[t]);
+      const u32x4 b = *reinterpret_cast<const u32x4_at*>(row[t] + 16);
+      w[t][8] = *reinterpret_cast<const u32_at*>(row[t] + 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[t][e] = a[e];
+        w[t][4 + e] = b[e];
+      }
     }
+  }
+  __device__ __forceinline__ void load(const uint8_t* const (&row)[TILES], int64_t c, int g, int64_t K) {
+    const int64_t pairs = (K + 32) / 64, p = min(4 * c + g, pairs - 1);
+    const uint8_t* at[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) at[t] = row[t] + p * PAIR_BYTES;
+    load_pair(at, ODD && p == pairs - 1);
   }
 };
 
-// The activations of a chunk, up to 16 rows, read and split here: a row's chunk
-// is scaled by a power of two into binary16 (float16 as it is).  Row a of the
-// operand is row (a >> 2) + 4 (a & 3) of x, so that up to four rows lie in the
-// first of a result's registers.  (More rows come as fragments from prep_rows.)
-template <int PA, typename T>
+// Up to 16 rows of x: a wave reads its chunk of each of them once, scales the
+// row's XB blocks by a power of two into binary16 (float16 as it is), splits
+// them and puts them into LDS in operand order, so the split costs by the rows
+// there are.  Row a of the operand is row (a >> 2) + 4 (a & 3) of x: up to 4 VR
+// rows lie in the first VR of a result's registers.
+template <int PA, int VR, typename T>
 struct Acts {
+  static constexpr int ROWS = 4 * VR;
+  static constexpr int XB = VR == 4 ? 4 : 8;      // blocks staged at a time
+  static constexpr int LANES = 8 * XB;            // per row
+  static constexpr int LOADS = ROWS * LANES / 64; // per stage
+  static constexpr int BLOCK = ROWS * 64 + 64;    // bytes; the padding spreads a store over the banks
+  static constexpr int BYTES = PA * XB * BLOCK + ROWS * 4;  // of a wave
   typedef T vec __attribute__((ext_vector_type(4)));
-  vec v[4][2];
-  const T* row;
-  __device__ __forceinline__ Acts(const void* x, int64_t M, int64_t K, int lane) {
-    const int a = lane & 15;
-    row = static_cast<const T*>(x) + min<int64_t>((a >> 2) + 4 * (a & 3), M - 1) * K + 4 * (lane >> 4);
-  }
-  __device__ __forceinline__ void load(int64_t c, int64_t CB) {
+  vec v[LOADS];
+
+  // stage s: blocks XB s .. of the operand's blocks
+  __device__ __forceinline__ void load(const T* x, int64_t M, int64_t K, int64_t s, int lane) {
+    const int64_t k = s * XB * 32 + 4 * (lane % LANES);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const T* p = row + min(4 * c + b, CB - 1) * 32;
-      v[b][0] = *reinterpret_cast<const vec*>(p);
-      v[b][1] = *reinterpret_cast<const vec*>(p + 16);
+    for (int u = 0; u < LOADS; ++u) {
+      const int r = u * (64 / LANES) + lane / LANES;
+      v[u] = vec{};
+      if (LANES == 64 ? u < M : u * (64 / LANES) < M)  // uniform
+        if (k < K) v[u] = *reinterpret_cast<const vec*>(x + min<int64_t>(r, M - 1) * K + k);
     }
   }
-  // The power of two that brings the chunk's largest magnitude to binary16's
-  // range.
-  __device__ __forceinline__ float scale() {
+  __device__ __forceinline__ void store(char* lds, int64_t M, int lane) const {
+    const int l = lane % LANES;
+    char* to = lds + (l >> 3) * BLOCK + (l & 3) * 16 + (l & 4) * 2;
+    float* scales = reinterpret_cast<float*>(lds + PA * XB * BLOCK);
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) {
+      if (!(LANES == 64 ? u < M : u * (64 / LANES) < M)) continue;  // uniform
+      const int r = u * (64 / LANES) + lane / LANES;
+      float f[4], s = 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = to_f32(static_cast<T>(v[u][e]));
+      if constexpr (!__is_same(T, _Float16)) {
+        const PowerOfTwo p(
+            lanes_max<LANES>(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])))));
+        s = p.s;
+        if (l == 0) scales[r] = p.inv;
+      }
+      typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+      f16x4 hi, lo;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = f[e] * s;
+        hi[e] = static_cast<_Float16>(y);
+        if constexpr (PA == 2) lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
+      }
+      *reinterpret_cast<f16x4*>(to + r * 64) = hi;
+      if constexpr (PA == 2) *reinterpret_cast<f16x4*>(to + XB * BLOCK + r * 64) = lo;
+    }
+  }
+  static __device__ __forceinline__ f16x8 fragment(const char* lds, int b, int part, int64_t M, int lane) {
+    const int a = lane & 15, r = static_cast<int>(min<int64_t>((a >> 2) + 4 * (a & 3), M - 1));
+    return *reinterpret_cast<const f16x8*>(lds + (part * XB + b) * BLOCK + r * 64 + (lane >> 4) * 16);
+  }
+  // of the row in register v of a result
+  static __device__ __forceinline__ float inverse(const char* lds, int v, int64_t M, int lane) {
     if constexpr (__is_same(T, _Float16)) return 1.f;
-    float top = 0.f;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f32(static_cast<T>(v[b][e >> 2][e & 3]))));
-    top = row_scale(groups_max(top));
-    // the values stay packed until their fragment is made
-#pragma unroll
-    for (int b = 0; b < 4; ++b) asm volatile("" : "+v"(v[b][0]), "+v"(v[b][1]));
-    return top;
-  }
-  __device__ __forceinline__ void fragment(int b, float s, f16x8 (&a)[1][PA]) const {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = to_f32(static_cast<T>(v[b][e >> 2][e & 3])) * s;
-      a[0][0][e] = static_cast<_Float16>(x);
-      if constexpr (PA == 2) a[0][1][e] = static_cast<_Float16>(x - static_cast<float>(a[0][0][e]));
-    }
+    return reinterpret_cast<const float*>(lds + PA * XB * BLOCK)[min<int64_t>((lane >> 4) + 4 * v, M - 1)];
   }
 };
 
-template <int RT, int PA, int NT, int VR, typename T>
-__global__ __launch_bounds__(64 * FW) __attribute__((amdgpu_waves_per_eu(RT == 1 ? 4 : 2)))
+template <int RT, int PA, int NT, int VR, typename T, bool ODD>
+__global__ __launch_bounds__(64 * FW) __attribute__((amdgpu_waves_per_eu(RT > 1 || NT > 1 ? 2 : VR > 2 ? 3 : 4)))
 void ffn_few_kernel(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu,
                     const void* __restrict__ X, const float* __restrict__ inv, int64_t K, Out o) {
   constexpr int TILES = 2 * NT;  // gate's, then up's
-  __shared__ float red[FW][TILES][VR][64];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = static_cast<int>(blockDim.x) >> 6;
   const int i = lane & 15, g = lane >> 4;
-  const int64_t CB = K / 32, chunks = (CB + 3) / 4, AB = (CB + 1) / 2 * 2;
+  const int64_t pairs = (K + 32) / 64, chunks = (pairs + 3) / 4, AB = 2 * pairs, M = o.M;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT);
   const uint8_t* row[TILES];
 #pragma unroll
   for (int t = 0; t < TILES; ++t)
-    row[t] = (t < NT ? Wg : Wu) + min(n0 + 16 * (t % NT) + i, o.N - 1) * CB * BLOCK_BYTES;
+    row[t] = (t < NT ? Wg : Wu) + min(n0 + 16 * (t % NT) + i, o.N - 1) * (K / 32) * BLOCK_BYTES;
 
   f32x4 acc[RT][TILES];
 #pragma unroll
@@ -204,27 +282,45 @@ void ffn_few_kernel(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ 
 #pragma unroll
     for (int t = 0; t < TILES; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // A chunk: step 4-block-major, codes of block s / TILES of tile s % TILES
-  // against a(b); a step's scaled sums are taken while the next one's products
-  // run.  The empty volatile asm keeps that order: regrouped, all products
-  // first, their results would spill.
-  auto chunk = [&](RawChunk<TILES>& w, int64_t c, const float (&is)[VR], auto&& acts) {
-    constexpr int STEPS = 4 * TILES;
-    f16x8 a[2][RT][PA];
-    f32x4 p[2][RT];
-    int from = 4 * i;  // of the scale's lane, in bytes
-    asm volatile("" : "+v"(from));
+  // codes in place of the loaded bytes: q[t][o][p] is this lane's dword of block
+  // 2 p + o of the chunk, dd[t] the two scales of its own pair
+  struct Codes {
+    uint32_t q[TILES][2][4], dd[TILES];
+  };
+  auto decode = [&](const RawChunk<TILES, ODD>& w, int64_t c) {
+    Codes k;
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      transpose4(w.q[t]);
-      if (4 * c + g >= CB) w.d[t] = 0;  // blocks past the row have no weight
+      const uint32_t* r = w.w[t];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        k.q[t][0][e] = shift16(r[e + 1], r[e]);
+        k.q[t][1][e] = r[5 + e];
+      }
+      // pairs past the row have no weight
+      k.dd[t] = 4 * c + g < pairs ? __builtin_amdgcn_perm(r[4], r[0], 0x07060100u) : 0u;
+      transpose4(k.q[t][0]);
+      transpose4(k.q[t][1]);
     }
-    float d[2];
+    return k;
+  };
+  // blocks B0 .. B0 + NB - 1 of a chunk: step s is block s / TILES against tile
+  // s % TILES; a step's scaled sums are taken while the next one's products run.
+  // The empty volatile asm keeps that order: regrouped, all products first,
+  // their results would spill.
+  auto blocks = [&](const Codes& k, auto b0, auto nb, const float (&is)[VR], auto&& acts) {
+    constexpr int B0 = decltype(b0)::value, NB = decltype(nb)::value, STEPS = NB * TILES;
+    f16x8 a[2][RT][PA];
+    f32x4 p[2][RT];
+    uint32_t d[2][TILES];
+    int from = 4 * i;  // of the scale's lane, in bytes
+    asm volatile("" : "+v"(from));
     auto products = [&](int s) {
-      const int b = s / TILES, t = s % TILES;
-      if (t == 0 && b + 1 < 4) acts(b + 1, a[(b + 1) & 1]);
-      d[s & 1] = half_bits_to_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from + 64 * b, w.d[t])));
-      const f16x8 q = codes8(w.q[t][b]);
+      const int b = B0 + s / TILES, t = s % TILES;
+      if (t == 0 && s + TILES < STEPS) acts(b + 1, a[(b + 1) & 1]);
+      if ((b & 1) == 0)
+        d[(b >> 1) & 1][t] = __builtin_amdgcn_ds_bpermute(from + 64 * (b >> 1), k.dd[t]);
+      const f16x8 q = codes8(k.q[t][b & 1][b >> 1]);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
         p[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b & 1][r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
@@ -236,89 +332,273 @@ void ffn_few_kernel(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ 
 #pragma unroll
       for (int r = 0; r < RT; ++r) asm volatile("" : "+v"(p[s & 1][r])::"memory");
     };
-    acts(0, a[0]);
+    acts(B0, a[B0 & 1]);
     products(0);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       if (s + 1 < STEPS) products(s + 1);
-      const int t = s % TILES;
+      const int b = B0 + s / TILES, t = s % TILES;
+      const uint32_t pair = d[(b >> 1) & 1][t];
+      const float ds = half_bits_to_float(b & 1 ? pair >> 16 : pair & 0xFFFFu);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
 #pragma unroll
         for (int v = 0; v < VR; ++v)
-          acc[r][t][v] = __builtin_fmaf(RT == 1 ? d[s & 1] * is[v] : d[s & 1], p[s & 1][r][v], acc[r][t][v]);
+          acc[r][t][v] = __builtin_fmaf(RT == 1 && !__is_same(T, _Float16) ? ds * is[v] : ds, p[s & 1][r][v], acc[r][t][v]);
         asm volatile("" : "+v"(acc[r][t]));
       }
     }
   };
 
   // one chunk is multiplied while the next one's bytes are in flight
-  RawChunk<TILES> w0, w1;
-  auto all = [&](auto&& one) {
-    int64_t c = wave;
-    if (c < chunks) w0.load(row, c, g, CB);
-    for (; c < chunks; c += 2 * FW) {
-      const bool two = c + FW < chunks;
-      if (two) w1.load(row, c + FW, g, CB);
-      one(w0, c);
-      if (two) {
-        if (c + 2 * FW < chunks) w0.load(row, c + 2 * FW, g, CB);
-        one(w1, c + FW);
-      }
-    }
-  };
+  RawChunk<TILES, ODD> w;
+  int64_t c = wave;
   if constexpr (RT == 1) {
-    Acts<PA, T> x(X, o.M, K, lane);
-    all([&](RawChunk<TILES>& w, int64_t c) {
-      x.load(c, CB);
-      const float s = x.scale();
+    using X1 = Acts<PA, VR, T>;
+    const T* x = static_cast<const T*>(X);
+    char* mine = lds + wave * X1::BYTES;
+    X1 xa;
+    if (c < chunks) {
+      xa.load(x, M, K, c * (8 / X1::XB), lane);
+      w.load(row, c, g, K);
+    }
+    for (; c < chunks; c += waves) {
+      const int64_t next = c + waves;
+      auto stage = [&](int64_t following) {
+        xa.store(mine, M, lane);
+        issued();
+        if (following >= 0) xa.load(x, M, K, following, lane);
+      };
+      stage(X1::XB == 4 ? 2 * c + 1 : next < chunks ? next : -1);
+      const Codes k = decode(w, c);
+      if (next < chunks) w.load(row, next, g, K);
       float is[VR];
+      auto acts = [&](int b, f16x8 (&a)[1][PA]) {
 #pragma unroll
-      for (int v = 0; v < VR; ++v) is[v] = __is_same(T, _Float16) ? 1.f : 1.f / __shfl(s, 4 * g + v);
-      chunk(w, c, is, [&](int b, f16x8 (&a)[1][PA]) { x.fragment(b, s, a); });
-    });
+        for (int p = 0; p < PA; ++p) a[0][p] = X1::fragment(mine, b % X1::XB, p, M, lane);
+      };
+#pragma unroll
+      for (int v = 0; v < VR; ++v) is[v] = X1::inverse(mine, v, M, lane);
+      blocks(k, Int<0>{}, Int<X1::XB>{}, is, acts);
+      if constexpr (X1::XB == 4) {
+        issued();
+        stage(next < chunks ? 2 * next : -1);
+#pragma unroll
+        for (int v = 0; v < VR; ++v) is[v] = X1::inverse(mine, v, M, lane);
+        blocks(k, Int<4>{}, Int<4>{}, is, acts);
+      }
+      issued();
+    }
   } else {
     const f16x8* A = static_cast<const f16x8*>(X) + lane;
-    const int64_t rta = (o.M + 15) / 16;
-    const float one[VR] = {};
-    all([&](RawChunk<TILES>& w, int64_t c) {
-      chunk(w, c, one, [&](int b, f16x8 (&a)[RT][PA]) {
-        const f16x8* at = A + min(4 * c + b, CB - 1) * 64;
+    const int64_t rta = (M + 15) / 16;
+    const float none[VR] = {};
+    if (c < chunks) w.load(row, c, g, K);
+    for (; c < chunks; c += waves) {
+      const Codes k = decode(w, c);
+      if (c + waves < chunks) w.load(row, c + waves, g, K);
+      blocks(k, Int<0>{}, Int<8>{}, none, [&](int b, f16x8 (&a)[RT][PA]) {
+        const f16x8* at = A + min(8 * c + b, AB - 1) * 64;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int p = 0; p < PA; ++p) a[r][p] = at[(p * rta + min<int64_t>(r, rta - 1)) * AB * 64];
       });
-    });
+    }
   }
 
   // the waves' sums in a fixed order; a thread takes one column of both
   // projections in one row
+  float(*red)[TILES][VR][64] = reinterpret_cast<float(*)[TILES][VR][64]>(lds);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    if (r) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
 #pragma unroll
       for (int v = 0; v < VR; ++v) red[wave][t][v][lane] = acc[r][t][v];
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < (NT * VR + FW - 1) / FW; ++u) {
-      const int item = u * FW + wave;
-      if (item >= NT * VR) break;  // wave-uniform
+    for (int item = wave; item < NT * VR; item += waves) {
       const int t = item / VR, v = item % VR;
       const int64_t m = RT == 1 ? g + 4 * v : 16 * r + 4 * g + v, n = n0 + 16 * t + i;
-      if (m >= o.M || n >= o.N) continue;
+      if (m >= M || n >= o.N) continue;
       float sg = red[0][t][v][lane], su = red[0][NT + t][v][lane];
-#pragma unroll
-      for (int w = 1; w < FW; ++w) {
-        sg += red[w][t][v][lane];
-        su += red[w][NT + t][v][lane];
+      for (int u = 1; u < waves; ++u) {
+        sg += red[u][t][v][lane];
+        su += red[u][NT + t][v][lane];
       }
       const float f = RT == 1 ? 1.f : inv[m];
       finish<T>(o, m, n, f * sg, f * su);
     }
   }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 rows of up to 4096 columns: persistent workgroups, a wave per chunk of
+// 256 k, which it keeps of every row of x in registers, as matrix-core operands.
+// A pass is eight columns of each projection, gate's in the low half of the
+// operand's sixteen; two passes' bytes are in flight.
+// ---------------------------------------------------------------------------
+constexpr int STREAM_K = 4096;
+
+template <int PA, int VR, typename T, bool ODD>
+__global__ __launch_bounds__(1024) void ffn_stream_kernel(const uint8_t* __restrict__ Wg,
+                                                          const uint8_t* __restrict__ Wu,
+                                                          const T* __restrict__ X, int K, int passes,
+                                                          Out o) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = static_cast<int>(blockDim.x) >> 6;
+  float(*red)[VR][64] = reinterpret_cast<float(*)[VR][64]>(lds);  // [2 waves][VR][64]
+  const int i = lane & 15, g = lane >> 4;
+  const int pairs = (K + 32) / 64, pair = 4 * wave + g;
+  const int64_t rb = static_cast<int64_t>(K / 32) * BLOCK_BYTES;
+  const uint8_t* base = (i < 8 ? Wg : Wu) + min(pair, pairs - 1) * PAIR_BYTES;
+  RawChunk<1, ODD> w0, w1;
+  auto load = [&](int u, RawChunk<1, ODD>& w) {
+    w.load_pair({base + min<int64_t>(8 * static_cast<int64_t>(u) + (i & 7), o.N - 1) * rb},
+                ODD && pair >= pairs - 1);
+  };
+
+  // x, its rows as Acts has them.  Up to four are split once and reach the
+  // operands through LDS (one row straight into operands, each of its values
+  // split by sixteen lanes: 12.9 us against 10.8); more are read as operands.
+  f16x8 a[8][PA];
+  float is[VR];
+  auto start = [&]() {
+    load(blockIdx.x, w0);
+    if (static_cast<int>(blockIdx.x + gridDim.x) < passes) load(blockIdx.x + gridDim.x, w1);
+  };
+  if constexpr (VR <= 2) {
+    using X1 = Acts<PA, VR, T>;
+    char* mine = lds + 2 * waves * VR * 256 + wave * X1::BYTES;
+    X1 x;
+    x.load(X, o.M, K, wave, lane);
+    start();
+    x.store(mine, o.M, lane);
+    issued();
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int p = 0; p < PA; ++p) a[b][p] = X1::fragment(mine, b, p, o.M, lane);
+#pragma unroll
+    for (int v = 0; v < VR; ++v) is[v] = X1::inverse(mine, v, o.M, lane);
+  } else {
+    typedef T vec __attribute__((ext_vector_type(4)));
+    vec v[8][2];
+    const int row = (i >> 2) + 4 * (i & 3);
+    const T* x = X + static_cast<int64_t>(min<int64_t>(row, o.M - 1)) * K + 4 * g;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const int k = 256 * wave + 32 * b;
+      const T* p = x + min(k, K - 32);
+      v[b][0] = *reinterpret_cast<const vec*>(p);
+      v[b][1] = *reinterpret_cast<const vec*>(p + 16);
+      if (k >= K) v[b][0] = v[b][1] = vec{};
+    }
+    start();
+    float s = 1.f, back = 1.f;
+    if constexpr (!__is_same(T, _Float16)) {
+      float top = 0.f;
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f32(static_cast<T>(v[b][e >> 2][e & 3]))));
+      const PowerOfTwo p(groups_max(top));
+      s = p.s;
+      back = p.inv;
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = to_f32(static_cast<T>(v[b][e >> 2][e & 3])) * s;
+        a[b][0][e] = static_cast<_Float16>(y);
+        if constexpr (PA == 2) a[b][1][e] = static_cast<_Float16>(y - static_cast<float>(a[b][0][e]));
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < VR; ++v) is[v] = __is_same(T, _Float16) ? 1.f : __shfl(back, 4 * g + v);
+  }
+
+  auto compute = [&](const RawChunk<1, ODD>& w, f32x4& acc) {
+    uint32_t q[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[0][e] = shift16(w.w[0][e + 1], w.w[0][e]);
+      q[1][e] = w.w[0][5 + e];
+    }
+    const uint32_t dd = pair < pairs ? __builtin_amdgcn_perm(w.w[0][4], w.w[0][0], 0x07060100u) : 0u;
+    transpose4(q[0]);
+    transpose4(q[1]);
+    uint32_t d[4];
+    int from = 4 * i;
+    asm volatile("" : "+v"(from));
+#pragma unroll
+    for (int p = 0; p < 4; ++p) d[p] = __builtin_amdgcn_ds_bpermute(from + 64 * p, dd);
+    f32x4 t[2];
+    auto products = [&](int b) {
+      const f16x8 c = codes8(q[b & 1][b >> 1]);
+      t[b & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b][0], c, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      if constexpr (PA == 2) t[b & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b][1], c, t[b & 1], 0, 0, 0);
+      asm volatile("" : "+v"(t[b & 1])::"memory");
+    };
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    products(0);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b + 1 < 8) products(b + 1);
+      const float s = half_bits_to_float(b & 1 ? d[b >> 1] >> 16 : d[b >> 1] & 0xFFFFu);
+#pragma unroll
+      for (int v = 0; v < VR; ++v) acc[v] = __builtin_fmaf(s, t[b & 1][v], acc[v]);
+      asm volatile("" : "+v"(acc));
+    }
+  };
+  // the waves' sums in a fixed order, by the waves in turn
+  int turn = wave;
+  auto put = [&](int u, const f32x4& acc, int q) {
+#pragma unroll
+    for (int v = 0; v < VR; ++v) red[q * waves + wave][v][lane] = acc[v] * is[v];
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VR; ++v) {
+      if (turn != v % waves) continue;  // (wave-uniform)
+      const int64_t m = g + 4 * v, n = 8 * static_cast<int64_t>(u) + (i & 7);
+      float s = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < waves; k += 4) {  // four in flight
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = k + e < waves ? red[q * waves + k + e][v][lane] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += p[e];
+      }
+      const float up = dpp_f32<0x128>(s);  // row_ror:8
+      if (i < 8 && m < o.M && n < o.N) finish<T>(o, m, n, s, up);
+    }
+    if (VR < waves) turn = turn + VR < waves ? turn + VR : turn + VR - waves;
+  };
+  const int step = gridDim.x;
+  for (int u = blockIdx.x; u < passes; u += 2 * step) {
+    f32x4 acc;
+    compute(w0, acc);
+    if (u + 2 * step < passes) load(u + 2 * step, w0);
+    __builtin_amdgcn_sched_barrier(0);
+    put(u, acc, 0);
+    if (u + step >= passes) break;
+    compute(w1, acc);
+    if (u + 3 * step < passes) load(u + 3 * step, w1);
+    __builtin_amdgcn_sched_barrier(0);
+    put(u + step, acc, 1);
+  }
+}
+
+// Bytes of LDS per wave.
+template <int RT, int PA, int NT, int VR, typename T>
+constexpr int few_lds() {
+  const int sums = 2 * NT * VR * 256;
+  return RT == 1 && Acts<PA, VR, T>::BYTES > sums ? Acts<PA, VR, T>::BYTES : sums;
 }
 
 // ---------------------------------------------------------------------------
@@ -493,8 +773,8 @@ __global__ __launch_bounds__(256) void ffn_dz_kernel(const T* z, const T* __rest
 }
 
 struct FfnPlan {
-  bool few;
-  int rt, nt, pa;
+  bool stream, few;
+  int rt, nt, pa, waves, grid;
   Tile tile;
   int64_t cols;  // rows of both projections, padded
   size_t x, inv, codes, scale, total;
@@ -506,18 +786,22 @@ FfnPlan ffn_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   p.pa = type == TYPE_F32 ? 2 : 1;
   p.few = M <= FEW_ROWS;
   p.rt = static_cast<int>((M + 15) / 16);
+  if (p.rt == 1 && K <= STREAM_K) {
+    p.stream = true;
+    p.waves = static_cast<int>((K + 255) / 256);
+    // a workgroup per CU, more of fewer waves
+    p.grid = static_cast<int>(std::min<int64_t>((N + 7) / 8, static_cast<int64_t>(cus) * std::max(1, 8 / p.waves)));
+    return p;
+  }
   if (p.few) {
-    // the tile that keeps the busiest CU's columns fewest; a workgroup's x is
-    // read whatever its columns, so the wider of equals
-    int64_t best = INT64_MAX;
-    for (int nt = p.rt == 1 || p.rt > 3 ? 2 : 3; nt >= 1; --nt) {
-      const int64_t groups = (N + 16 * nt - 1) / (16 * nt);
-      const int64_t most = (groups + cus - 1) / cus * nt;
-      if (most < best) {
-        best = most;
-        p.nt = nt;
-      }
-    }
+    // short matrices: the wider tile once a CU has more than one of the narrow
+    // (x is read per workgroup)
+    p.nt = (N + 15) / 16 > cus ? 2 : 1;
+    // a wave per chunk while a workgroup has no more than eight of them; else
+    // eight waves for up to 16 rows and four above, whose registers let two
+    // workgroups share a CU (9216 x 3072, 38 rows: 33.6 us against 42.9 with six)
+    const int64_t chunks = (K + 255) / 256;
+    p.waves = static_cast<int>(chunks <= FW ? chunks : p.rt == 1 ? FW : 4);
     if (p.rt == 1) return p;
   }
   p.x = c.take(static_cast<size_t>(frag_elems(M, K)) * 16 * p.pa);
@@ -559,10 +843,6 @@ GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   return p;
 }
 
-using std::integral_constant;
-template <int V>
-using Int = integral_constant<int, V>;
-
 
 #define Q4_TRY(expr)                          \
   do {                                        \
@@ -583,6 +863,24 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
   float* inv = reinterpret_cast<float*>(base + p.inv);
   const Out o = {a.r, a.h, a.z, a.M, a.N, a.act};
   if (!p.few || p.rt > 1) Q4_TRY(prep_rows(a.x, a.type, Order::NIBBLE, xa, inv, a.M, a.K, a.stream));
+  if (p.stream) {
+    with_type(a.type, [&](auto type) {
+      using T = decltype(type);
+      constexpr int PA = sizeof(T) == 4 ? 2 : 1;
+      auto go = [&](auto vr) {
+        constexpr int VR = decltype(vr)::value;
+        auto* kernel = a.K % 64 == 0 ? ffn_stream_kernel<PA, VR, T, false> : ffn_stream_kernel<PA, VR, T, true>;
+        const unsigned lds = p.waves * (2 * VR * 256 + (VR <= 2 ? Acts<PA, VR, T>::BYTES : 0));
+        hipLaunchKernelGGL(kernel, dim3(p.grid), dim3(64 * p.waves), lds, a.stream, a.gate, a.up,
+                           static_cast<const T*>(a.x), static_cast<int>(a.K),
+                           static_cast<int>((a.N + 7) / 8), o);
+      };
+      if (a.M <= 4) go(Int<1>{});
+      else if (a.M <= 8) go(Int<2>{});
+      else go(Int<4>{});
+    });
+    return hipGetLastError();
+  }
   if (p.few) {
     with_type(a.type, [&](auto type) {
       using T = decltype(type);
@@ -590,13 +888,14 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
       auto launch = [&](auto rt, auto nt, auto vr) {
         constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value, VR = decltype(vr)::value;
         const unsigned grid = static_cast<unsigned>((a.N + 16 * NT - 1) / (16 * NT));
-        hipLaunchKernelGGL((ffn_few_kernel<RT, PA, NT, VR, T>), dim3(grid), dim3(64 * FW), 0, a.stream,
-                           a.gate, a.up, RT == 1 ? a.x : static_cast<const void*>(xa), inv, a.K, o);
+        auto* kernel = a.K % 64 == 0 ? ffn_few_kernel<RT, PA, NT, VR, T, false> : ffn_few_kernel<RT, PA, NT, VR, T, true>;
+        const unsigned lds = p.waves * few_lds<RT, PA, NT, VR, T>();
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * p.waves), lds, a.stream, a.gate, a.up,
+                           RT == 1 ? a.x : static_cast<const void*>(xa), inv, a.K, o);
       };
       auto cols = [&](auto rt, auto vr) {
         if (p.nt == 1) launch(rt, Int<1>{}, vr);
-        else if (p.nt == 2) launch(rt, Int<2>{}, vr);
-        else launch(rt, Int<(decltype(rt)::value == 1 || decltype(rt)::value > 3) ? 2 : 3>{}, vr);
+        else launch(rt, Int<2>{}, vr);
       };
       if (a.M <= 4) cols(Int<1>{}, Int<1>{});
       else if (a.M <= 8) cols(Int<1>{}, Int<2>{});
