@@ -623,14 +623,14 @@ __global__ __launch_bounds__(256) void ffn_codes_kernel(const uint8_t* __restric
   scale[f * 16 + i] = half_bits_to_float(d);
 }
 
-template <typename S, int PA, int KS, typename T>
+template <typename S, int PA, typename T>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_gemm_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
                      const float* __restrict__ scale, const float* __restrict__ inv, int64_t cols,
                      int64_t CB, int tiles_m, Out o) {
   f32x4 acc[S::FM][S::FN];
   int64_t m0, c0;
-  scaled_tile<S, PA, KS>(A, Q, scale, o.M, cols, CB, tiles_m, acc, m0, c0);
+  scaled_tile<S, PA>(A, Q, scale, o.M, cols, CB, tiles_m, acc, m0, c0);
   if (c0 >= cols) return;
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -917,10 +917,10 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
   const int tm = static_cast<int>((a.M + d.m - 1) / d.m), tn = static_cast<int>((p.cols + d.n - 1) / d.n);
   with_type(a.type, [&](auto type) {
     using T = decltype(type);
-    constexpr int PA = sizeof(T) == 4 ? 2 : 1, KS = PA == 1 ? 2 : 1;
+    constexpr int PA = sizeof(T) == 4 ? 2 : 1;
     auto go = [&](auto shape) {
       using S = decltype(shape);
-      hipLaunchKernelGGL((ffn_gemm_kernel<S, PA, KS, T>),
+      hipLaunchKernelGGL((ffn_gemm_kernel<S, PA, T>),
                          dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn)), dim3(S::THREADS), 0,
                          a.stream, xa, codes, scale, inv, p.cols, KB, tm, o);
     };

@@ -320,10 +320,42 @@ __global__ __launch_bounds__(256) void prep_transpose_kernel(const uint8_t* __re
   }
 }
 
-// Measured, 256 x 256 tiles: 375 x 3072 over 32768 with three products per pair
-// 227 us (998 TFLOP/s of binary16), 1500 with one 296 us (1020); the matrix cores
-// are busy 43 % of the time, the rest waits on LDS and on the loads of the next
-// stage.
+// Writes (alpha: adds to) a tile's slice: fragments (i, j) from fragment row m0 and
+// fragment column n0 on.
+template <int FM, int FN>
+__device__ __forceinline__ void plain_out(const f32x4 (&acc)[FM][FN], int64_t m0, int64_t n0, int split,
+                                          int64_t M, int64_t N, float* __restrict__ out, int64_t ld,
+                                          const float* __restrict__ alpha) {
+  const int lane = threadIdx.x & 63;
+  // lane (i, g): row i of a fragment row, columns 4 g .. 4 g + 3 (N % 16 == 0)
+  float* o = out + static_cast<int64_t>(split) * M * ld;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = (m0 + i) * 16 + (lane & 15);
+    if (m >= M) continue;
+    const float al = alpha ? alpha[m] : 0.f;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t n = (n0 + j) * 16 + 4 * (lane >> 4);
+      if (n >= N) continue;
+      f32x4* p = reinterpret_cast<f32x4*>(o + m * ld + n);
+      f32x4 v = acc[i][j];
+      if (alpha) {
+        const f32x4 q = *p;
+        v.x = __builtin_fmaf(al, q.x, v.x);
+        v.y = __builtin_fmaf(al, q.y, v.y);
+        v.z = __builtin_fmaf(al, q.z, v.z);
+        v.w = __builtin_fmaf(al, q.w, v.w);
+      }
+      *p = v;
+    }
+  }
+}
+
+// Operands of which one has two parts.  Measured, 256 x 256 tiles: 375 x 3072 over
+// 32768 with three products per pair 227 us (998 TFLOP/s of binary16); the matrix
+// cores are busy 43 % of the time, the rest waits on LDS and on the loads of the
+// next stage.
 template <typename S, int PA, int PB, int KS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_plain_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B, int64_t M,
@@ -405,29 +437,115 @@ void gemm_plain_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B,
     __syncthreads();
   }
   if (c < c1) compute(buf0);
-  // lane (i, g): row i of a fragment row, columns 4 g .. 4 g + 3 (N % 16 == 0)
-  float* o = out + static_cast<int64_t>(split) * M * ld;
+  plain_out(acc, ma + wm * S::FM, mb + wn * S::FN, split, M, N, out, ld, alpha);
+}
+
+// Operands of one part each.  Measured, 256 x 256 tiles: 1500 x 3072 over 32768
+// 272 us (1110 TFLOP/s; 296 on gemm_plain_kernel's two buffers, whose LDS reads
+// wait for every load in flight; two-part operands gain nothing from the ring,
+// 113 us against 101 for 375 x 1280 over 32768: a stage of theirs fills the LDS
+// of two here).
+template <typename S>
+__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gemm_ring_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ B, int64_t M,
+                       int64_t N, int64_t CB, int tiles_m, int tiles, int64_t span,
+                       float* __restrict__ out, int64_t ld, const float* __restrict__ alpha) {
+  using St = Stage<S, 1, 1, 1>;
+  constexpr int FM = S::FM, FN = S::FN;
+  static_assert(St::NF % St::WAVES == 0 && FM % 4 == 0, "");
+  // arrays of their own rather than one of all: the compiler then knows that
+  // reading one does not have to wait for loads into the others
+  __shared__ f16x8 buf0[St::NF][64], buf1[St::NF][64], buf2[St::NF][64], buf3[St::NF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = xcd_order(blockIdx.x, gridDim.x);
+  const int split = item / tiles, tile = item % tiles;
+  const int tm = tile % tiles_m, tn = tile / tiles_m;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int64_t ma = static_cast<int64_t>(tm) * (S::M / 16), mb = static_cast<int64_t>(tn) * (S::N / 16);
+  const int64_t rta = (M + 15) / 16, rtb = (N + 15) / 16;
+  const int64_t c0 = split * span, c1 = min(CB, c0 + span);
+
+  f32x4 acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i) {
-    const int64_t m = (ma + wm * S::FM + i) * 16 + (lane & 15);
-    if (m >= M) continue;
-    const float al = alpha ? alpha[m] : 0.f;
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < S::FN; ++j) {
-      const int64_t n = (mb + wn * S::FN + j) * 16 + 4 * (lane >> 4);
-      if (n >= N) continue;
-      f32x4* p = reinterpret_cast<f32x4*>(o + m * ld + n);
-      f32x4 v = acc[i][j];
-      if (alpha) {
-        const f32x4 q = *p;
-        v.x = __builtin_fmaf(al, q.x, v.x);
-        v.y = __builtin_fmaf(al, q.y, v.y);
-        v.z = __builtin_fmaf(al, q.z, v.z);
-        v.w = __builtin_fmaf(al, q.w, v.w);
-      }
-      *p = v;
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const St st(A, B, ma, rta, mb, rtb, CB, wave);
+  __amdgpu_buffer_rsrc_t from[St::PER];
+#pragma unroll
+  for (int u = 0; u < St::PER; ++u) from[u] = buffer(st.at[u], CB * 1024);
+  auto buf = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if constexpr (K == 0) return buf0;
+    else if constexpr (K == 1) return buf1;
+    else if constexpr (K == 2) return buf2;
+    else return buf3;
+  };
+  // past the last stage: it again, so that the loads in flight can be counted
+  auto fill = [&](auto k, int64_t c) {
+    const int at = static_cast<int>(min(c, c1 - 1)) * 1024;
+#pragma unroll
+    for (int u = 0; u < St::PER; ++u) buffer_to_lds<16>(from[u], lane * 16, at, &buf(k)[wave * St::PER + u][0]);
+    issued();
+  };
+  f16x8 a[4], b[2][FN];
+  auto load_a = [&](const f16x8 (*src)[64], int i) { a[i % 4] = src[wm * FM + i % FM][lane]; };
+  auto load_b = [&](const f16x8 (*src)[64], int k) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b[k][j] = src[St::FA + wn * FN + j][lane];
+  };
+  // Stage c in buffer k (a ring as in scaled_tile), a row of fragments after the
+  // other; rows are read from LDS two ahead.
+  auto stage = [&](auto k, int64_t c) {
+    constexpr int K = decltype(k)::value, P = K & 1;
+    const std::integral_constant<int, (K + 1) % 4> next;
+    const std::integral_constant<int, (K + 3) % 4> last;
+    arrived_but<St::PER>();
+    meet();
+    fill(last, c + 3);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (i + 2 < FM) load_a(buf(k), i + 2);
+      else load_a(buf(next), i + 2);
+      if (i == FM / 2 - 1) load_b(buf(next), P ^ 1);
+      __builtin_amdgcn_sched_barrier(0);  // the reads stay ahead of the products
+      // D rows are B's (the columns of out), D columns A's (its rows)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[P][j], a[i % 4], acc[i][j], 0, 0, 0);
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3])::"memory");
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  if (c0 < c1) {  // a slice of a short reduction may be empty: its sum is zero
+    const std::integral_constant<int, 0> z0;
+    const std::integral_constant<int, 1> z1;
+    const std::integral_constant<int, 2> z2;
+    const std::integral_constant<int, 3> z3;
+    fill(z0, c0);
+    fill(z1, c0 + 1);
+    fill(z2, c0 + 2);
+    arrived();
+    meet();
+    load_b(buf0, 0);
+    load_a(buf0, 0);
+    load_a(buf0, 1);
+    int64_t c = c0;  // (slices have an even number of blocks)
+    for (; c + 4 <= c1; c += 4) {
+      stage(z0, c);
+      stage(z1, c + 1);
+      stage(z2, c + 2);
+      stage(z3, c + 3);
+    }
+    if (c < c1) {
+      stage(z0, c);
+      stage(z1, c + 1);
+    }
+    arrived();  // the loads in vain: LDS may be another workgroup's after this one
   }
+  plain_out(acc, ma + wm * FM, mb + wn * FN, split, M, N, out, ld, alpha);
 }
 
 // Maximum over the 16 lanes of a DPP row, in all of them.
@@ -492,7 +610,7 @@ __device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0
 // Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 179 us, 1500 in
 // one 354 us (845 and 853 TFLOP/s of binary16).  The block scale's FMAs keep the
 // vector unit busy 48 % of the time beside the matrix cores' 33 %.
-template <typename S, int PA, int KS, bool STATS>
+template <typename S, int PA, bool STATS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
                         const float* __restrict__ scale, const float* __restrict__ inv, int64_t M,
@@ -503,7 +621,7 @@ void gemm_logits_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q
   static_assert(S::FN == 4, "a wave's columns are one entry of tmax");
   f32x4 acc[S::FM][S::FN];
   int64_t m0, c0;
-  scaled_tile<S, PA, KS>(A, Q, scale, M, cols, CB, tiles_m, acc, m0, c0);
+  scaled_tile<S, PA>(A, Q, scale, M, cols, CB, tiles_m, acc, m0, c0);
   logits_out<STATS>(acc, m0, c0, cols, inv, M, n0, N, targets, logits, tmax, tsum, tlogit, ld, tld);
 }
 
@@ -970,18 +1088,14 @@ hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s) {
   const int64_t span = ((p.CB / 2 + p.splits - 1) / p.splits) * 2;
   return with_tile(t, [&](auto shape) {
     using S = decltype(shape);
-    auto go = [&](auto pa, auto pb, auto ks) {
-      hipLaunchKernelGGL((gemm_plain_kernel<S, decltype(pa)::value, decltype(pb)::value, decltype(ks)::value>),
-                         dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.splits)),
+    auto go = [&](auto* kernel) {
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn * p.splits)),
                          dim3(S::THREADS), 0, s, p.a, p.b, p.M, p.N, p.CB, tm, tm * tn, span, p.out,
                          p.ld, p.alpha);
     };
-    using std::integral_constant;
-    const integral_constant<int, 1> one;
-    const integral_constant<int, 2> two;
-    if (p.pa == 1 && p.pb == 1) go(one, one, two);
-    else if (p.pa == 1) go(one, two, one);
-    else go(two, two, one);
+    if (p.pa == 1 && p.pb == 1) go(gemm_ring_kernel<S>);
+    else if (p.pa == 1) go(gemm_plain_kernel<S, 1, 2, 1>);
+    else go(gemm_plain_kernel<S, 2, 2, 1>);
   });
 }
 
@@ -1022,8 +1136,8 @@ hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
   const int tm = static_cast<int>((p.M + d.m - 1) / d.m), tn = static_cast<int>((p.cols + d.n - 1) / d.n);
   return with_tile(t, [&](auto shape) {
     using S = decltype(shape);
-    auto go = [&](auto pa, auto ks, auto stats) {
-      hipLaunchKernelGGL((gemm_logits_kernel<S, decltype(pa)::value, decltype(ks)::value, decltype(stats)::value>),
+    auto go = [&](auto pa, auto stats) {
+      hipLaunchKernelGGL((gemm_logits_kernel<S, decltype(pa)::value, decltype(stats)::value>),
                          dim3(static_cast<unsigned>(static_cast<int64_t>(tm) * tn)), dim3(S::THREADS), 0, s,
                          p.a, p.q, p.scale, p.inv, p.M, p.cols, p.CB, tm, p.n0, p.N, p.targets, p.logits,
                          p.tmax, p.tsum, p.tlogit, p.ld, p.tld);
@@ -1034,9 +1148,9 @@ hipError_t launch_gemm_logits(Tile t, const LogitGemm& p, hipStream_t s) {
     const std::true_type yes;
     const std::false_type no;
     if (p.logits) {
-      if (p.pa == 1) go(one, two, no); else go(two, one, no);
+      if (p.pa == 1) go(one, no); else go(two, no);
     } else {
-      if (p.pa == 1) go(one, two, yes); else go(two, one, yes);
+      if (p.pa == 1) go(one, yes); else go(two, yes);
     }
   });
 }

@@ -106,20 +106,59 @@ struct Stage {
   }
 };
 
+// The wave's loads to LDS but the latest `N` are complete, and no LDS access moves
+// across.
+template <int N>
+__device__ __forceinline__ void arrived_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+// A barrier alone: what the waves have in flight to LDS stays in flight.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Memory to LDS as to_lds, from lane l's SIZE bytes at base + own + at of a
+// range-checked buffer (own: the lane's offset, at: the wave's).  Beside these
+// loads the compiler counts LDS reads one by one; beside to_lds it waits for all
+// of them each time.
+template <int SIZE>
+__device__ __forceinline__ void buffer_to_lds(__amdgpu_buffer_rsrc_t base, int own, int at, void* l) {
+  const auto lp = (__attribute__((address_space(3))) void*)l;
+  if constexpr (SIZE == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(base, lp, 16, own, at, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(base, lp, 4, own, at, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+
 // A tile of A Q^T with exact codes: sum over the blocks b of scale[n][b]
 // (A[m, block b] . Q[n, block b]), `cols` rows of Q.  Row 4 g + v and column
 // lane % 16 of the wave's fragments (i, j) in acc[i][j][v]; the wave's first row
 // of A and of Q in m0 and c0.
-template <typename S, int PA, int KS>
+//
+// A ring of NB stages of one block each.  When stage c begins, stage c + NB - 1
+// is asked for and stage c + 1 is already there, so its first operands are read
+// before c ends and a barrier finds work on both sides of it.
+template <typename S, int PA>
 __device__ __forceinline__ void scaled_tile(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
                                             const float* __restrict__ scale, int64_t M, int64_t cols,
                                             int64_t CB, int tiles_m, f32x4 (&acc)[S::FM][S::FN],
                                             int64_t& m0, int64_t& c0) {
-  using St = Stage<S, PA, 1, KS>;
-  constexpr int SC = S::N * KS;  // block scales of a stage, [row tile][block][16]
-  constexpr int SU = (SC / 64 + St::WAVES - 1) / St::WAVES;  // loads of 64 scales per wave
-  __shared__ f16x8 buf0[St::NF][64], buf1[St::NF][64];
-  __shared__ float sc0[SC], sc1[SC];
+  using St = Stage<S, PA, 1, 1>;
+  constexpr int NB = PA == 1 ? 4 : 3, FM = S::FM, FN = S::FN;
+  constexpr int SC = S::N;  // block scales of a stage, [row tile][16]
+  static_assert(St::NF % St::WAVES == 0 && SC / 64 <= St::WAVES && FM % 4 == 0, "");
+  // arrays of their own rather than one of all: the compiler then knows that
+  // reading one does not have to wait for loads into the others
+  __shared__ f16x8 buf0[St::NF][64], buf1[St::NF][64], buf2[St::NF][64], buf3[NB == 4 ? St::NF : 1][64];
+  // (the waves past SC / 64 load scales in vain, so that all have as many loads
+  // in flight)
+  constexpr int SL = 64 * St::WAVES;
+  __shared__ float sc0[SL], sc1[SL], sc2[SL], sc3[NB == 4 ? SL : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned item = xcd_order(blockIdx.x, gridDim.x);
@@ -129,93 +168,143 @@ __device__ __forceinline__ void scaled_tile(const f16x8* __restrict__ A, const f
   const int64_t rta = (M + 15) / 16, rtb = cols / 16;
 
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const St st(A, Q, ma, rta, mb, rtb, CB, wave);
-  auto issue = [&](f16x8 (*buf)[64], float* sc, int64_t c) {
-    st.issue(buf, c, wave, lane);
+  __amdgpu_buffer_rsrc_t from[St::PER];
 #pragma unroll
-    for (int u = 0; u < SU; ++u) {
-      const int first = (wave * SU + u) * 64;
-      if (SC / 64 % St::WAVES != 0 && first >= SC) break;
-      const int e = first + lane;
-      const int64_t rt = min(mb + e / (16 * KS), rtb - 1);
-      to_lds<4>(scale + (rt * CB + c) * 16 + e % (16 * KS), sc + first);
-    }
+  for (int u = 0; u < St::PER; ++u) from[u] = buffer(st.at[u], CB * 1024);
+  const int tiles = static_cast<int>(min<int64_t>(S::N / 16, rtb - mb));  // that have scales
+  const __amdgpu_buffer_rsrc_t scales = buffer(scale + mb * CB * 16, tiles * CB * 64);
+  const int own = min(wave * 4 + lane / 16, tiles - 1) * static_cast<int>(CB) * 64 + lane % 16 * 4;
+  auto buf = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if constexpr (K == 0) return buf0;
+    else if constexpr (K == 1) return buf1;
+    else if constexpr (K == 2) return buf2;
+    else return buf3;
+  };
+  auto sc = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if constexpr (K == 0) return sc0;
+    else if constexpr (K == 1) return sc1;
+    else if constexpr (K == 2) return sc2;
+    else return sc3;
+  };
+  // past the last stage: it again, so that the loads in flight can be counted
+  auto fill = [&](auto k, int64_t c) {
+    const int at = static_cast<int>(min(c, CB - 1)) * 1024;
+#pragma unroll
+    for (int u = 0; u < St::PER; ++u) buffer_to_lds<16>(from[u], lane * 16, at, &buf(k)[wave * St::PER + u][0]);
+    buffer_to_lds<4>(scales, own, at / 16, sc(k) + wave * 64);
     issued();
   };
-  // Row s + 1's products are started before row s's scaled sums are taken, so
-  // the matrix cores and the vector unit overlap within the wave, and operands
-  // are read from LDS two rows (B and its scales half a block) ahead.  The
-  // empty volatile asm keeps that order (pure arithmetic would otherwise be
-  // regrouped, all products first, whose temporaries then spill).
-  auto compute = [&](const f16x8 (*buf)[64], const float* sc) {
-    constexpr int STEPS = KS * S::FM;
-    f16x8 a[3][PA], b[2][S::FN];
-    float d[2][S::FN];
-    auto load_a = [&](int s) {
+  f16x8 a[4][PA], b[2][FN];
+  float d[2][FN];
+  f32x4 t[2][FN];
+  auto load_a = [&](const f16x8 (*from)[64], int i) {
 #pragma unroll
-      for (int p = 0; p < PA; ++p)
-        a[s % 3][p] = buf[(p * S::WM * S::FM + wm * S::FM + s % S::FM) * KS + s / S::FM][lane];
-    };
-    auto load_b = [&](int k) {
+    for (int p = 0; p < PA; ++p) a[i % 4][p] = from[p * S::WM * FM + wm * FM + i % FM][lane];
+  };
+  auto load_b = [&](const f16x8 (*from)[64], const float* s, int k) {
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j) {
-        b[k & 1][j] = buf[St::FA + (wn * S::FN + j) * KS + k][lane];
-        d[k & 1][j] = sc[((wn * S::FN + j) * KS + k) * 16 + (lane & 15)];
-      }
-    };
-    f32x4 t[2][S::FN];
-    auto products = [&](int s) {
-      const int k = s / S::FM;
+    for (int j = 0; j < FN; ++j) {
+      b[k][j] = from[St::FA + wn * FN + j][lane];
+      d[k][j] = s[(wn * FN + j) * 16 + (lane & 15)];
+    }
+  };
+  auto products = [&](int i, int k) {
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j) {
-        t[s & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[s % 3][0], b[k & 1][j],
-                                                             f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        if constexpr (PA == 2)
-          t[s & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[s % 3][1], b[k & 1][j], t[s & 1][j], 0, 0, 0);
-      }
-      asm volatile("" : "+v"(t[s & 1][0]), "+v"(t[s & 1][1]), "+v"(t[s & 1][2]), "+v"(t[s & 1][3])::"memory");
-    };
-    load_b(0);
-    load_a(0);
-    if constexpr (STEPS > 1) load_a(1);
-    products(0);
+    for (int j = 0; j < FN; ++j)
+      t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[i % 4][0], b[k][j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+    if constexpr (PA == 2)
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int i = s % S::FM, k = s / S::FM;
-      if (s + 2 < STEPS) load_a(s + 2);
-      if (i == S::FM / 2 - 1 && k + 1 < KS) load_b(k + 1);
-      if (s + 1 < STEPS) products(s + 1);
+      for (int j = 0; j < FN; ++j)
+        t[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[i % 4][1], b[k][j], t[i & 1][j], 0, 0, 0);
+    asm volatile("" : "+v"(t[i & 1][0]), "+v"(t[i & 1][1]), "+v"(t[i & 1][2]), "+v"(t[i & 1][3])::"memory");
+  };
+  // Stage c in buffer k: row i + 1's products are started before row i's scaled
+  // sums are taken, so the matrix cores and the vector unit overlap within the
+  // wave, and operands are read from LDS two rows (B and its scales half a
+  // stage) ahead, at a stage's end from the next one's buffer (past the last
+  // stage they are read in vain).  The empty volatile asm keeps that order (pure
+  // arithmetic would otherwise be regrouped, all products first, whose
+  // temporaries then spill).
+  auto stage = [&](auto k, auto par, int64_t c) {
+    constexpr int K = decltype(k)::value, P = decltype(par)::value;
+    const std::integral_constant<int, (K + 1) % NB> next;
+    const std::integral_constant<int, (K + NB - 1) % NB> last;
+    // stage c + 1 is there, and all waves are past stage c - 1
+    arrived_but<(NB - 3) * (St::PER + 1)>();
+    meet();
+    fill(last, c + NB - 1);
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j) {
-        acc[i][j].x = __builtin_fmaf(d[k & 1][j], t[s & 1][j].x, acc[i][j].x);
-        acc[i][j].y = __builtin_fmaf(d[k & 1][j], t[s & 1][j].y, acc[i][j].y);
-        acc[i][j].z = __builtin_fmaf(d[k & 1][j], t[s & 1][j].z, acc[i][j].z);
-        acc[i][j].w = __builtin_fmaf(d[k & 1][j], t[s & 1][j].w, acc[i][j].w);
+    for (int i = 0; i < FM; ++i) {
+      if (i + 3 < FM) load_a(buf(k), i + 3);
+      else load_a(buf(next), i + 3);
+      if (i == FM / 2 - 1) load_b(buf(next), sc(next), P ^ 1);
+      __builtin_amdgcn_sched_barrier(0);  // the reads stay ahead of the products
+      products(i + 1, i + 1 < FM ? P : P ^ 1);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        acc[i][j].x = __builtin_fmaf(d[P][j], t[i & 1][j].x, acc[i][j].x);
+        acc[i][j].y = __builtin_fmaf(d[P][j], t[i & 1][j].y, acc[i][j].y);
+        acc[i][j].z = __builtin_fmaf(d[P][j], t[i & 1][j].z, acc[i][j].z);
+        acc[i][j].w = __builtin_fmaf(d[P][j], t[i & 1][j].w, acc[i][j].w);
       }
       asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
     }
   };
-  issue(buf0, sc0, 0);
+  using std::integral_constant;
+  const integral_constant<int, 0> z0;
+  const integral_constant<int, 1> z1;
+  const integral_constant<int, 2> z2;
+  const integral_constant<int, 3> z3;
+  fill(z0, 0);
+  fill(z1, 1);
+  if constexpr (NB == 4) fill(z2, 2);
   arrived();
-  __syncthreads();
-  int64_t c = 0;
-  for (; c + 2 * KS <= CB; c += 2 * KS) {
-    issue(buf1, sc1, c + KS);
-    compute(buf0, sc0);
-    arrived();
-    __syncthreads();
-    if (c + 2 * KS < CB) issue(buf0, sc0, c + 2 * KS);
-    compute(buf1, sc1);
-    arrived();
-    __syncthreads();
+  meet();
+  load_b(buf0, sc0, 0);
+  load_a(buf0, 0);
+  load_a(buf0, 1);
+  load_a(buf0, 2);
+  products(0, 0);
+  int64_t c = 0;  // (CB is even)
+  if constexpr (NB == 4) {
+    for (; c + 4 <= CB; c += 4) {
+      stage(z0, z0, c);
+      stage(z1, z1, c + 1);
+      stage(z2, z0, c + 2);
+      stage(z3, z1, c + 3);
+    }
+    if (c < CB) {
+      stage(z0, z0, c);
+      stage(z1, z1, c + 1);
+    }
+  } else {
+    for (; c + 6 <= CB; c += 6) {
+      stage(z0, z0, c);
+      stage(z1, z1, c + 1);
+      stage(z2, z0, c + 2);
+      stage(z0, z1, c + 3);
+      stage(z1, z0, c + 4);
+      stage(z2, z1, c + 5);
+    }
+    if (c < CB) {
+      stage(z0, z0, c);
+      stage(z1, z1, c + 1);
+    }
+    if (c + 2 < CB) {
+      stage(z2, z0, c + 2);
+      stage(z0, z1, c + 3);
+    }
   }
-  if (c < CB) compute(buf0, sc0);
-  m0 = (ma + wm * S::FM) * 16;
-  c0 = (mb + wn * S::FN) * 16;
+  arrived();  // the loads in vain: LDS may be another workgroup's after this one
+  m0 = (ma + wm * FM) * 16;
+  c0 = (mb + wn * FN) * 16;
 }
 
 }  // namespace q4

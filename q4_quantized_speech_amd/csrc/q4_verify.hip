@@ -17,6 +17,8 @@
 // of each chunk of the distribution to draw from; the draw.  Bound by reading
 // the logits once; the row that is drawn from is read again.
 
+#include <algorithm>
+
 #include "q4_kernels.h"
 #include "q4_types.h"
 
@@ -27,31 +29,29 @@ constexpr int CHUNK = 4096;         // columns of a workgroup
 constexpr int PER = CHUNK / 256;    // per thread
 constexpr int MAX_ROWS = 64;        // D + 1
 
-// 2^t for t <= 0 (0 below the smallest subnormal): Taylor's series of exp(f ln 2),
-// |f| <= 1/2, to the 13th power; what is left out is below 5e-18.
+// 2^t for t <= 0, 0 below -1000: t = k + f, |f| <= 1/2, 2^f by the polynomial of
+// degree 9 through it at Chebyshev's nodes (computed in 60 digits; within
+// 1.9e-14 of 2^f), k from the last bits of t + 1.5 * 2^52 and added to the
+// exponent: full-rate instructions alone (conversions, ldexp and a Taylor series
+// of 13 terms: 58 us against XX for 384 rows of 131072 float32).
 __device__ __forceinline__ double exp2_64(double t) {
-  constexpr double LN2 = 0.693147180559945309417232121458;
-  constexpr double C1 = LN2, C2 = C1 * LN2 / 2, C3 = C2 * LN2 / 3, C4 = C3 * LN2 / 4,
-                   C5 = C4 * LN2 / 5, C6 = C5 * LN2 / 6, C7 = C6 * LN2 / 7, C8 = C7 * LN2 / 8,
-                   C9 = C8 * LN2 / 9, C10 = C9 * LN2 / 10, C11 = C10 * LN2 / 11,
-                   C12 = C11 * LN2 / 12, C13 = C12 * LN2 / 13;
-  t = fmax(t, -1100.0);
-  const double k = __builtin_rint(t), f = t - k;
-  double p = C13;
-  p = __builtin_fma(p, f, C12);
-  p = __builtin_fma(p, f, C11);
-  p = __builtin_fma(p, f, C10);
-  p = __builtin_fma(p, f, C9);
-  p = __builtin_fma(p, f, C8);
-  p = __builtin_fma(p, f, C7);
-  p = __builtin_fma(p, f, C6);
-  p = __builtin_fma(p, f, C5);
-  p = __builtin_fma(p, f, C4);
-  p = __builtin_fma(p, f, C3);
-  p = __builtin_fma(p, f, C2);
-  p = __builtin_fma(p, f, C1);
-  p = __builtin_fma(p, f, 1.0);
-  return __builtin_ldexp(p, static_cast<int>(k));
+  constexpr double BIG = 0x1.8p52;
+  const double c = fmax(t, -1001.0), sum = c + BIG, f = c - (sum - BIG);
+  double p = 0x1.b6571de2f2351p-24;
+  p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
+  p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
+  p = __builtin_fma(p, f, 0x1.43088e257f341p-13);
+  p = __builtin_fma(p, f, 0x1.5d87fe908f88ap-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab72b175eep-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
+  p = __builtin_fma(p, f, 0x1.000000000003dp+0);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+  const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, sum));
+  const uint32_t hi = static_cast<uint32_t>(bits >> 32) + (k << 20);
+  const double r = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | static_cast<uint32_t>(bits));
+  return t > -1000.0 ? r : 0.0;
 }
 
 struct Stat {
@@ -164,9 +164,9 @@ __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
     double sum = 0.0;
     // a chunk of masked columns has no sum (nor has one that spoils its row)
     if (top > -__builtin_inff() && top < __builtin_inff()) {
-      const double t = top;
-#pragma unroll 4
-      for (int e = 0; e < PER; ++e) sum += exp2_64((static_cast<double>(l[e]) - t) * a.scale);
+      const double t = -static_cast<double>(top) * a.scale;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) sum += exp2_64(__builtin_fma(static_cast<double>(l[e]), a.scale, t));
     }
     sum = wave_sum(sum);
     if (lane == 0) ssum[wave] = sum;
@@ -249,43 +249,44 @@ __device__ __forceinline__ void entries(const Args& a, int64_t s, const Decision
   const bool probs = left && a.probs;
   if (probs) load_columns<V>(static_cast<const T*>(a.probs) + (s * a.D + d.row) * a.N, n, a.N, 0.f, q);
   const int64_t t = left && !probs ? a.draft[s * a.D + d.row] : -1;
+  const double top = -static_cast<double>(d.top) * a.scale;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    w[e] = exp2_64((static_cast<double>(l[e]) - static_cast<double>(d.top)) * a.scale);
+    w[e] = exp2_64(__builtin_fma(static_cast<double>(l[e]), a.scale, top));
     if (probs) w[e] = fmax(__builtin_fma(-static_cast<double>(q[e]), d.z, w[e]), 0.0);
     if (t == n + e) w[e] = 0.0;
   }
 }
 
+// `per` workgroups a sequence, each every per-th chunk.
 template <typename T>
-__global__ __launch_bounds__(256) void verify_mass_kernel(Args a) {
+__global__ __launch_bounds__(256) void verify_mass_kernel(Args a, int per) {
   __shared__ double ssum[4];
   constexpr int V = 16 / sizeof(T);
-  const int64_t per = a.greedy ? 1 : a.chunks, s = blockIdx.x / per, c = blockIdx.x - s * per;
+  const int64_t s = blockIdx.x / per;
+  const int first = static_cast<int>(blockIdx.x - s * per);
   const Decision d = decide<T>(a, s);
-  if (c == 0) {
+  if (first == 0) {
     publish(a, s, d);
     if (threadIdx.x == 0) a.decision[s] = d;
   }
-  if (d.none || a.greedy) return;
-  double sum = 0.0;
-  if (!d.cut) {  // known from the first launch
-    const Stat st = a.stats[(s * (a.D + 1) + d.row) * a.chunks + c];
-    sum = st.sum * exp2_64((static_cast<double>(st.max) - static_cast<double>(d.top)) * a.scale);
-    if (threadIdx.x == 0) a.mass[s * a.chunks + c] = sum;
-    return;
-  }
-#pragma unroll 1
-  for (int u = 0; u < PER / V; ++u) {
-    double w[V];
-    entries<V, T>(a, s, d, true, c * CHUNK + V * (u * 256 + static_cast<int>(threadIdx.x)), w);
+  // (what is not cut is known from the first launch)
+  if (d.none || a.greedy || !d.cut) return;
+  for (int64_t c = first; c < a.chunks; c += per) {
+    double w[PER / V][V], sum = 0.0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum += w[e];
+    for (int u = 0; u < PER / V; ++u)
+      entries<V, T>(a, s, d, true, c * CHUNK + V * (u * 256 + static_cast<int>(threadIdx.x)), w[u]);
+#pragma unroll
+    for (int u = 0; u < PER / V; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum += w[u][e];
+    sum = wave_sum(sum);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) ssum[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) a.mass[s * a.chunks + c] = ((ssum[0] + ssum[1]) + ssum[2]) + ssum[3];
   }
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63) == 0) ssum[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) a.mass[s * a.chunks + c] = ((ssum[0] + ssum[1]) + ssum[2]) + ssum[3];
 }
 
 // Sum of the earlier threads' values; `all` the whole.
@@ -341,25 +342,28 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(Args a) {
     if (left) return a.mass[s * a.chunks + c];
     return st[c].sum * exp2_64((static_cast<double>(st[c].max) - static_cast<double>(d.top)) * a.scale);
   };
+  const double u = a.u[s * (a.D + 1) + a.D];
+  double own = 0.0;  // this thread's chunk, where there are no more chunks than threads
   auto whole = [&]() {
     double v = 0.0, all;
-    for (int64_t c = threadIdx.x; c < a.chunks; c += 256) v += mass(c);
+    for (int64_t c = threadIdx.x; c < a.chunks; c += 256) v += own = mass(c);
     sum_before(v, ds, all);
     return all;
   };
   double total = whole();
   if (left && !(total > 0.0)) {  // nothing of p is above q
     left = false;
+    own = 0.0;
     total = whole();
   }
-  const double goal = static_cast<double>(a.u[s * (a.D + 1) + a.D]) * total;
+  const double goal = u * total;
   // the first chunk whose running sum passes the goal; failing that (a number
   // of 1 or more, or a rounding), the last one that holds anything
   int64_t chunk = INT64_MAX, last = -1;
   double base = 0.0;
   for (int64_t c0 = 0; c0 < a.chunks; c0 += 256) {
     const int64_t c = c0 + threadIdx.x;
-    const double v = mass(c);
+    const double v = a.chunks <= 256 ? own : mass(c);
     double all;
     const double before = base + sum_before(v, ds, all);
     const int64_t hit = group_min(v > 0.0 && before + v > goal ? c : INT64_MAX, is);
@@ -434,12 +438,14 @@ hipError_t launch_verify(const VerifyArgs& v) {
   a.mass = reinterpret_cast<double*>(base);
   base += align256(v.S * a.chunks * sizeof(double));
   a.decision = reinterpret_cast<Decision*>(base);
+  // every workgroup takes the decision: about as many as run at once
+  const int per = a.greedy ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.chunks, 1024 / v.S)));
   with_type(v.type, [&](auto t) {
     using T = decltype(t);
     hipLaunchKernelGGL(verify_stats_kernel<T>, dim3(static_cast<unsigned>(v.S * (v.D + 1) * a.chunks)),
                        dim3(256), 0, v.stream, a);
-    hipLaunchKernelGGL(verify_mass_kernel<T>, dim3(static_cast<unsigned>(v.S * (a.greedy ? 1 : a.chunks))),
-                       dim3(256), 0, v.stream, a);
+    hipLaunchKernelGGL(verify_mass_kernel<T>, dim3(static_cast<unsigned>(v.S * per)), dim3(256), 0, v.stream, a,
+                       per);
     if (!a.greedy)
       hipLaunchKernelGGL(verify_draw_kernel<T>, dim3(static_cast<unsigned>(v.S)), dim3(256), 0, v.stream, a);
   });
