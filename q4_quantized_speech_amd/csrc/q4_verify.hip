@@ -29,14 +29,15 @@ constexpr int CHUNK = 4096;         // columns of a workgroup
 constexpr int PER = CHUNK / 256;    // per thread
 constexpr int MAX_ROWS = 64;        // D + 1
 
-// 2^t for t <= 0, 0 below -1000: t = k + f, |f| <= 1/2, 2^f by the polynomial of
-// degree 9 through it at Chebyshev's nodes (computed in 60 digits; within
-// 1.9e-14 of 2^f), k from the last bits of t + 1.5 * 2^52 and added to the
-// exponent: full-rate instructions alone (conversions, ldexp and a Taylor series
-// of 13 terms: 58 us against XX for 384 rows of 131072 float32).
-__device__ __forceinline__ double exp2_64(double t) {
+// 2^t for -1010 < t <= 0: t = k + f, |f| <= 1/2, 2^f by the polynomial of degree 9
+// through it at Chebyshev's nodes (computed in 60 digits; within 1.9e-14 of 2^f),
+// k from the last bits of t + 1.5 * 2^52 and added to the exponent.
+// (Conversions, ldexp and a Taylor series of 13 terms: verify_stats_kernel 58 us
+// against 51 for 384 rows of 131072 float32.)
+__device__ __forceinline__ double exp2_near(double t) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   constexpr double BIG = 0x1.8p52;
-  const double c = fmax(t, -1001.0), sum = c + BIG, f = c - (sum - BIG);
+  const double sum = t + BIG, f = t - (sum - BIG);
   double p = 0x1.b6571de2f2351p-24;
   p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
   p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
@@ -47,10 +48,13 @@ __device__ __forceinline__ double exp2_64(double t) {
   p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
   p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
   p = __builtin_fma(p, f, 0x1.000000000003dp+0);
-  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
-  const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, sum));
-  const uint32_t hi = static_cast<uint32_t>(bits >> 32) + (k << 20);
-  const double r = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | static_cast<uint32_t>(bits));
+  u32x2 bits = __builtin_bit_cast(u32x2, p);
+  bits.y += __builtin_bit_cast(u32x2, sum).x << 20;
+  return __builtin_bit_cast(double, bits);
+}
+// For any t <= 0, 0 below -1000.
+__device__ __forceinline__ double exp2_64(double t) {
+  const double r = exp2_near(fmax(t, -1001.0));
   return t > -1000.0 ? r : 0.0;
 }
 
@@ -88,19 +92,12 @@ __device__ __forceinline__ int length(const Args& a, int64_t s) {
   return a.lens ? max(0, min(a.D, a.lens[s])) : a.D;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
 // The larger, NaN if either is.
 __device__ __forceinline__ float larger(float a, float b) {
   return a != a || b != b ? __builtin_nanf("") : fmaxf(a, b);
 }
 __device__ __forceinline__ float wave_larger(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = larger(v, __shfl_xor(v, d));
-  return v;
+  return __any(v != v) ? __builtin_nanf("") : wave64_max(v);
 }
 
 // Columns n .. n + V - 1 of a row of N (those past it: `fill`).
@@ -120,11 +117,11 @@ __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
   __shared__ double ssum[4];
   __shared__ int32_t sat[4];
   constexpr int V = 16 / sizeof(T);
-  const int64_t item = blockIdx.x, r = item / a.chunks, c = item - r * a.chunks;
-  const int64_t s = r / (a.D + 1);
-  if (static_cast<int>(r - s * (a.D + 1)) > length(a, s)) return;
-  const T* row = static_cast<const T*>(a.logits) + r * a.N;
-  const int64_t n0 = c * CHUNK;
+  const uint32_t chunks = static_cast<uint32_t>(a.chunks), rows = a.D + 1;
+  const uint32_t item = blockIdx.x, r = item / chunks, c = item - r * chunks, s = r / rows;
+  if (static_cast<int>(r - s * rows) > length(a, s)) return;
+  const T* row = static_cast<const T*>(a.logits) + static_cast<int64_t>(r) * a.N;
+  const int64_t n0 = static_cast<int64_t>(c) * CHUNK;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float l[PER];
   float top = -__builtin_inff();
@@ -135,13 +132,16 @@ __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) l[u * V + e] = v[e];
   }
-  bool nan = false;
+  float odd = 0.f;  // NaN once a NaN (or an infinity) is among them
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     top = fmaxf(top, l[e]);
-    nan |= l[e] != l[e];
+    odd = __builtin_fmaf(l[e], 0.f, odd);
   }
-  if (nan) top = __builtin_nanf("");
+  if (odd != odd) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) top = larger(top, l[e]);
+  }
   top = wave_larger(top);
   if (lane == 0) smax[wave] = top;
   __syncthreads();
@@ -164,11 +164,14 @@ __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
     double sum = 0.0;
     // a chunk of masked columns has no sum (nor has one that spoils its row)
     if (top > -__builtin_inff() && top < __builtin_inff()) {
+      // masked columns, and what is below it by 2^-1000 and more, count as 2^-1000
       const double t = -static_cast<double>(top) * a.scale;
+      const float lowest = top - static_cast<float>(1000.0 / a.scale);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) sum += exp2_64(__builtin_fma(static_cast<double>(l[e]), a.scale, t));
+      for (int e = 0; e < PER; ++e)
+        sum += exp2_near(__builtin_fma(static_cast<double>(fmaxf(l[e], lowest)), a.scale, t));
     }
-    sum = wave_sum(sum);
+    sum = wave64_sum(sum);
     if (lane == 0) ssum[wave] = sum;
     __syncthreads();
     out.sum = ((ssum[0] + ssum[1]) + ssum[2]) + ssum[3];
@@ -215,7 +218,7 @@ __device__ __forceinline__ Decision decide(const Args& a, int64_t s) {
         double z = 0.0;
         for (int64_t c = lane; c < a.chunks; c += 64)
           z += st[c].sum * exp2_64((static_cast<double>(st[c].max) - static_cast<double>(top)) * a.scale);
-        d.z = wave_sum(z);
+        d.z = wave64_sum(z);
         et = t < 0 ? 0.0 : exp2_64((static_cast<double>(lt) - static_cast<double>(top)) * a.scale);
       }
     }
@@ -263,8 +266,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void verify_mass_kernel(Args a, int per) {
   __shared__ double ssum[4];
   constexpr int V = 16 / sizeof(T);
-  const int64_t s = blockIdx.x / per;
-  const int first = static_cast<int>(blockIdx.x - s * per);
+  const uint32_t s = blockIdx.x / static_cast<uint32_t>(per), first = blockIdx.x - s * per;
   const Decision d = decide<T>(a, s);
   if (first == 0) {
     publish(a, s, d);
@@ -281,7 +283,7 @@ __global__ __launch_bounds__(256) void verify_mass_kernel(Args a, int per) {
     for (int u = 0; u < PER / V; ++u)
 #pragma unroll
       for (int e = 0; e < V; ++e) sum += w[u][e];
-    sum = wave_sum(sum);
+    sum = wave64_sum(sum);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) ssum[threadIdx.x >> 6] = sum;
     __syncthreads();
