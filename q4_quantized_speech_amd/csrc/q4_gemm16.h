@@ -98,13 +98,14 @@ struct TransposedGemm {
   // the first one's in part
   const f16x8* g2;
   const uint8_t* w2;
+  int rt;  // 16-row tiles of a workgroup, 1 to 4 (0: transposed_rt(M))
 };
 struct TransposedPlan {
   double us;  // estimate
   int splits;
 };
 inline int transposed_rt(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
-TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus);
+TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus, int rt = 0);
 hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s);
 
 // Logits of weight rows n0 .. n0 + cols: l[m][n] = inv[m] sum_b scale[n][b]

@@ -1065,8 +1065,8 @@ double tile_time_us(Tile t, int64_t M, int64_t N, int64_t C, int units, int spli
   return gemm + 2.0 * splits * M * N * 4.0 / 4e6;  // slices written and read at 4 TB/s
 }
 
-TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus) {
-  const int rt = transposed_rt(M);
+TransposedPlan transposed_plan(int64_t M, int64_t N, int64_t K, int units, int cus, int rt) {
+  if (rt == 0) rt = transposed_rt(M);
   const int64_t tiles = (M + 16 * rt - 1) / (16 * rt) * ((K + 127) / 128);
   const int64_t blocks = (N + 31) / 32;
   TransposedPlan best = {1e30, 1};
@@ -1100,7 +1100,7 @@ hipError_t launch_gemm_plain(Tile t, const PlainGemm& p, hipStream_t s) {
 }
 
 hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
-  const int rt = transposed_rt(p.M);
+  const int rt = p.rt ? p.rt : transposed_rt(p.M);
   const int mtiles = static_cast<int>((p.M + 16 * rt - 1) / (16 * rt));
   const int tiles = static_cast<int>(mtiles * ((p.K + 127) / 128));
   const int64_t span = (p.CB + p.splits - 1) / p.splits;
@@ -1127,6 +1127,7 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   };
   if (rt == 1) parts(one);
   else if (rt == 2) parts(two);
+  else if (rt == 3) parts(integral_constant<int, 3>{});
   else parts(integral_constant<int, 4>{});
   return hipGetLastError();
 }

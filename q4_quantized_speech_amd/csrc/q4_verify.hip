@@ -21,6 +21,7 @@
 
 #include "q4_kernels.h"
 #include "q4_types.h"
+#include "q4_wave.h"
 
 namespace q4 {
 namespace {
