@@ -302,33 +302,35 @@ void ffn_few_kernel(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ 
   };
   // blocks B0 .. B0 + NB - 1 of a chunk: step s is block s / TILES against tile
   // s % TILES; a step's scaled sums are taken while the next one's products run.
-  // The empty volatile asm keeps that order: regrouped, all products first,
-  // their results would spill.
-  auto blocks = [&](const Codes& k, auto b0, auto nb, const float (&is)[VR], auto&& acts) {
+  // Operands of x are asked for AD - 1 blocks ahead (acts of a block past the
+  // chunk are the next chunk's).  The empty volatile asm keeps that order:
+  // regrouped, all products first, their results would spill.
+  constexpr int AD = RT == 1 || RT * PA > 6 ? 2 : 4;
+  f16x8 a[AD][RT][PA];
+  auto blocks = [&](const Codes& k, auto b0, auto nb, const float (&is)[VR], auto&& acts) __attribute__((always_inline)) {
     constexpr int B0 = decltype(b0)::value, NB = decltype(nb)::value, STEPS = NB * TILES;
-    f16x8 a[2][RT][PA];
     f32x4 p[2][RT];
     uint32_t d[2][TILES];
     int from = 4 * i;  // of the scale's lane, in bytes
     asm volatile("" : "+v"(from));
-    auto products = [&](int s) {
+    auto products = [&](int s) __attribute__((always_inline)) {
       const int b = B0 + s / TILES, t = s % TILES;
-      if (t == 0 && s + TILES < STEPS) acts(b + 1, a[(b + 1) & 1]);
+      if (t == 0 && (RT > 1 || s + TILES < STEPS)) acts(b + AD - 1, a[(b + AD - 1) % AD]);
       if ((b & 1) == 0)
         d[(b >> 1) & 1][t] = __builtin_amdgcn_ds_bpermute(from + 64 * (b >> 1), k.dd[t]);
       const f16x8 q = codes8(k.q[t][b & 1][b >> 1]);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        p[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b & 1][r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        p[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b % AD][r][0], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
       if constexpr (PA == 2) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          p[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b & 1][r][1], q, p[s & 1][r], 0, 0, 0);
+          p[s & 1][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b % AD][r][1], q, p[s & 1][r], 0, 0, 0);
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) asm volatile("" : "+v"(p[s & 1][r])::"memory");
     };
-    acts(B0, a[B0 & 1]);
+    if constexpr (RT == 1) acts(B0, a[B0 % AD]);
     products(0);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -389,16 +391,23 @@ void ffn_few_kernel(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ 
     const f16x8* A = static_cast<const f16x8*>(X) + lane;
     const int64_t rta = (M + 15) / 16;
     const float none[VR] = {};
-    if (c < chunks) w.load(row, c, g, K);
+    auto acts = [&](int64_t block, f16x8 (&to)[RT][PA]) {
+      const f16x8* at = A + min(block, AB - 1) * 64;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int p = 0; p < PA; ++p) to[r][p] = at[(p * rta + min<int64_t>(r, rta - 1)) * AB * 64];
+    };
+    if (c < chunks) {
+      w.load(row, c, g, K);
+#pragma unroll
+      for (int b = 0; b < AD - 1; ++b) acts(8 * c + b, a[b]);
+    }
     for (; c < chunks; c += waves) {
       const Codes k = decode(w, c);
       if (c + waves < chunks) w.load(row, c + waves, g, K);
-      blocks(k, Int<0>{}, Int<8>{}, none, [&](int b, f16x8 (&a)[RT][PA]) {
-        const f16x8* at = A + min(8 * c + b, AB - 1) * 64;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int p = 0; p < PA; ++p) a[r][p] = at[(p * rta + min<int64_t>(r, rta - 1)) * AB * 64];
+      blocks(k, Int<0>{}, Int<8>{}, none, [&](int b, f16x8 (&to)[RT][PA]) {
+        acts(b < 8 ? 8 * c + b : 8 * (c + waves) + b - 8, to);
       });
     }
   }
@@ -791,14 +800,14 @@ FfnPlan ffn_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
     return p;
   }
   if (p.few) {
-    // short matrices: the wider tile once a CU has more than one of the narrow
-    // (x is read per workgroup)
-    p.nt = (N + 15) / 16 > cus ? 2 : 1;
-    // a wave per chunk while a workgroup has no more than eight of them; else
-    // eight waves for up to 16 rows and four above, whose registers let two
-    // workgroups share a CU (9216 x 3072, 38 rows: 33.6 us against 42.9 with six)
+    // Up to 16 rows here have long rows (more than STREAM_K columns): eight waves,
+    // and the wider tile once a CU has more than one of the narrow.  Above, four
+    // waves of one tile, whose registers let two workgroups share a CU with four
+    // blocks of x in flight (38 rows of 9216 x 3072: 32.4 us; six waves 41.7, two
+    // tiles 39.8, two blocks in flight 38.5 and 34.6).
     const int64_t chunks = (K + 255) / 256;
-    p.waves = static_cast<int>(chunks <= FW ? chunks : p.rt == 1 ? FW : 4);
+    p.nt = p.rt == 1 && (N + 15) / 16 > cus ? 2 : 1;
+    p.waves = static_cast<int>(std::min<int64_t>(chunks, p.rt == 1 ? FW : 4));
     if (p.rt == 1) return p;
   }
   p.x = c.take(static_cast<size_t>(frag_elems(M, K)) * 16 * p.pa);
@@ -901,8 +910,8 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
                            RT == 1 ? a.x : static_cast<const void*>(xa), inv, a.K, o);
       };
       auto cols = [&](auto rt, auto vr) {
-        if (p.nt == 1) launch(rt, Int<1>{}, vr);
-        else launch(rt, Int<2>{}, vr);
+        if (decltype(rt)::value > 1 || p.nt == 1) launch(rt, Int<1>{}, vr);
+        else launch(Int<1>{}, Int<2>{}, vr);
       };
       if (a.M <= 4) cols(Int<1>{}, Int<1>{});
       else if (a.M <= 8) cols(Int<1>{}, Int<2>{});
