@@ -165,12 +165,20 @@ __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
     double sum = 0.0;
     // a chunk of masked columns has no sum (nor has one that spoils its row)
     if (top > -__builtin_inff() && top < __builtin_inff()) {
-      // masked columns, and what is below it by 2^-1000 and more, count as 2^-1000
-      const double t = -static_cast<double>(top) * a.scale;
-      const float lowest = top - static_cast<float>(1000.0 / a.scale);
+      const double t = top;
+      // a bound of 2^-900 of the largest, where float32 tells it from the largest
+      // (not at temperatures near 0): masked columns, and what is below, count as
+      // that much
+      const float span = static_cast<float>(900.0 / a.scale);
+      if (span > fabsf(top) * 0x1p-20f) {
+        const float lowest = top - span;
 #pragma unroll
-      for (int e = 0; e < PER; ++e)
-        sum += exp2_near(__builtin_fma(static_cast<double>(fmaxf(l[e], lowest)), a.scale, t));
+        for (int e = 0; e < PER; ++e)
+          sum += exp2_near((static_cast<double>(fmaxf(l[e], lowest)) - t) * a.scale);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < PER; ++e) sum += exp2_64((static_cast<double>(l[e]) - t) * a.scale);
+      }
     }
     sum = wave64_sum(sum);
     if (lane == 0) ssum[wave] = sum;
@@ -253,10 +261,9 @@ __device__ __forceinline__ void entries(const Args& a, int64_t s, const Decision
   const bool probs = left && a.probs;
   if (probs) load_columns<V>(static_cast<const T*>(a.probs) + (s * a.D + d.row) * a.N, n, a.N, 0.f, q);
   const int64_t t = left && !probs ? a.draft[s * a.D + d.row] : -1;
-  const double top = -static_cast<double>(d.top) * a.scale;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    w[e] = exp2_64(__builtin_fma(static_cast<double>(l[e]), a.scale, top));
+    w[e] = exp2_64((static_cast<double>(l[e]) - static_cast<double>(d.top)) * a.scale);
     if (probs) w[e] = fmax(__builtin_fma(-static_cast<double>(q[e]), d.z, w[e]), 0.0);
     if (t == n + e) w[e] = 0.0;
   }
