@@ -474,12 +474,13 @@ q4_status q4_gated_ffn(const void* w_gate, const void* w_up, const void* x, cons
  *        the projections (q4_lora_grad's dy).  At least one of dx, dz is
  *        given.  dz may be z.
  *   Ranges as for q4_gated_ffn.
- *   workspace : q4_gated_ffn_grad_workspace_bytes(type, M, N, K) bytes; as
- *           above.  Without dx none is needed.
+ *   workspace : q4_gated_ffn_grad_workspace_bytes(type, M, N, K) bytes (dz as
+ *           operands and two or more float32 copies of dx); as above.  Without
+ *           dx none is needed.
  * dx: exact weights, float32 sums, dg and du before their rounding to dz's
  * type, scaled per row by a power of two into binary16: to 2^-22 in float32
- * (two parts), 2^-12 in the 16-bit types (one, half of a binary16 step), or
- * 2^-33 of max|dh| max|z| of the row.  Deterministic; a row that holds an
+ * and float16 (two parts), 2^-12 in bfloat16 (one), or 2^-33 of
+ * max|dh| max|z| of the row.  Deterministic; a row that holds an
  * infinity or NaN gives non-finite values in that row only.
  */
 size_t q4_gated_ffn_grad_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);

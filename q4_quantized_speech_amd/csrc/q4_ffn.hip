@@ -792,7 +792,9 @@ FfnPlan ffn_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   p.pa = type == TYPE_F32 ? 2 : 1;
   p.few = M <= FEW_ROWS;
   p.rt = static_cast<int>((M + 15) / 16);
-  if (p.rt == 1 && K <= STREAM_K) {
+  // (five to eight rows of float32: the staged rows of sixteen waves are past the
+  // LDS)
+  if (p.rt == 1 && K <= (p.pa == 2 && M > 4 && M <= 8 ? STREAM_K - 256 : STREAM_K)) {
     p.stream = true;
     p.waves = static_cast<int>((K + 255) / 256);
     // a workgroup per CU, more of fewer waves
@@ -838,7 +840,9 @@ struct GradPlan {
 GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   GradPlan p = {};
   Carver c;
-  p.pa = type == TYPE_F32 ? 2 : 1;
+  // one binary16 part of dg and du (2^-12) is an eighth of bfloat16's own half
+  // step; float16's result would be 1.4 times as far off as its rounding alone
+  p.pa = type == TYPE_BF16 ? 1 : 2;
   p.rows = (N + 63) / 64 * 64;
   // tiles of as many rows as leave the fewest products, and of equals the tallest
   // (76 rows: two of 48, not of 64)
@@ -959,7 +963,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus) {
   const int64_t CB = p.rows / 32;
   with_type(a.type, [&](auto type) {
     using T = decltype(type);
-    constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+    constexpr int PARTS = __is_same(T, __bf16) ? 1 : 2;
     const T *z = static_cast<const T*>(a.z), *dh = static_cast<const T*>(a.dh);
     if (a.dx)
       hipLaunchKernelGGL(ffn_bound_kernel<T>, dim3(static_cast<unsigned>(a.M)), dim3(64 * BOUND_WAVES), 0, a.stream, z,

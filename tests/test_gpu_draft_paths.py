@@ -184,6 +184,52 @@ def test_verify_offsets_past_32_bits():
     assert (accepted < d).any() and (accepted >= 0).all()
 
 
+@pytest.mark.parametrize("m", [1, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("k", [3840, 3872, 4064, 4096])
+def test_forward_longest_rows_of_the_persistent_kernel(m, k):
+    """Fifteen and sixteen waves, with as much LDS as their rows of x take."""
+    n = 40
+    qg, wg = G.weights(n, k, 95)
+    qu, wu = G.weights(n, k, 96)
+    for dtype in (F32, BF16, F16):
+        x, _ = G.inputs(m, n, k, dtype, m, False)
+        announce(f"gated_ffn {m}x{n}x{k} {dtype}")
+        h, z = q4.gated_ffn(qg, qu, x, keep=True)
+        want, tol, wz, tz = G.forward(wg, wu, x, None, "silu", dtype)
+        G.assert_close(z, wz, tz, "z")
+        G.assert_close(h, want, tol, "h")
+
+
+@pytest.mark.parametrize("temp", [2.0 ** -60, 1e-9, 1e-6, 1e-3, 50.0, 2.0 ** 60])
+def test_verify_any_temperature(temp):
+    """From one token of each row to all of them alike; logits near and far from 0."""
+    import test_gpu_verify as V
+    l, draft, u, q = V.case(6, 3, 9000, F32, 17)
+    l[1] += 3000.0
+    l[2] *= 1e-6
+    l[3] -= 1e6
+    l[4, :, 100:] = -INF
+    draft[4] %= 100
+    l[5] *= 1e20
+    best = l[:, :3].argmax(2).to(torch.int32)
+    draft[::2] = best[::2]
+    V.check(l, draft, u, q, temp=temp)
+    V.check(l, draft, u, None, temp=temp)
+
+
+def test_verify_more_chunks_than_threads():
+    """A table of 2.6 million tokens: 640 chunks of a row."""
+    import test_gpu_verify as V
+    for dtype in (F32, BF16):
+        l, draft, u, q = V.case(2, 1, 2621441, dtype, 18, sharp=1.0)
+        l[1, 0, 2621440] = 30.0
+        draft[1, 0] = 2621440
+        V.check(l, draft, u, q)
+        V.check(l, draft, u, None)
+        u[:, 1] = 1 - 2.0 ** -24
+        V.check(l, draft, u, q, temp=1.3)
+
+
 # ------------------------------------------------------------------ graphs and streams
 
 def calls(gen):
