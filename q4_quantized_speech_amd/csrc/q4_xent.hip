@@ -435,19 +435,18 @@ __device__ __forceinline__ void weights8(const uint8_t* blk, int i, float (&w)[8
 }
 
 // Compacts a row's entries (token >= 0) into LDS, in order, and returns their
-// number.  All 256 threads; ends with a barrier.
+// number.  All threads, at least 256; ends with a barrier.
 __device__ __forceinline__ int row_entries(const Teacher& t, int64_t m, int (&slot)[TOP_MAX],
-                                           int (&base)[5]) {
+                                           int (&base)[4]) {
   const int j = threadIdx.x, lane = j & 63, wave = j >> 6;
   const bool here = j < t.top && t.at[m * t.top + j] >= 0;
   const uint64_t mask = __ballot(here);
-  if (lane == 0) base[wave + 1] = __popcll(mask);
-  if (j == 0) base[0] = 0;
+  if (lane == 0 && wave < 4) base[wave] = __popcll(mask);  // (the others hold none)
   __syncthreads();
   int from = 0, all = 0;
   for (int w = 0; w < 4; ++w) {
-    if (w < wave) from += base[w + 1];
-    all += base[w + 1];
+    if (w < wave) from += base[w];
+    all += base[w];
   }
   if (here) slot[from + __popcll(mask & ((uint64_t(1) << lane) - 1))] = j;
   __syncthreads();
@@ -463,7 +462,7 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
     float* __restrict__ loss, float* __restrict__ lse, T* __restrict__ dx, int64_t M, int64_t K,
     Teacher t) {
   __shared__ float red[4], c[TOP_MAX];
-  __shared__ int slot[TOP_MAX], base[5];
+  __shared__ int slot[TOP_MAX], base[4];
   __shared__ int64_t row[TOP_MAX];
   const int64_t m = blockIdx.x;
   const int count = row_entries(t, m, slot, base), j = threadIdx.x;
@@ -524,22 +523,46 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
   }
 }
 
-// The loss alone, from lse: the student's logits at the teacher's tokens, a wave
-// per entry.
+// The loss alone: the student's logits at the teacher's tokens, a wave per entry.
+// tmax, tsum (nullable): the maxima and sums of a table in one piece, folded here
+// into lse; else lse is read.
+// Measured: 8 rows of 16 entries, 1280 columns, with the fold 6.9 us (the fold
+// apart 4.7, and 8.3 with four waves).
+constexpr int LOSS_WAVES = 16;
 template <typename T>
-__global__ __launch_bounds__(256) void distill_loss_kernel(const T* __restrict__ x,
-                                                           const uint8_t* __restrict__ W,
-                                                           const float* __restrict__ lse,
-                                                           float* __restrict__ loss, int64_t K,
-                                                           Teacher t) {
-  __shared__ float red[4];
-  __shared__ int slot[TOP_MAX], base[5];
+__global__ __launch_bounds__(64 * LOSS_WAVES) void distill_loss_kernel(
+    const T* __restrict__ x, const uint8_t* __restrict__ W, const float* __restrict__ tmax,
+    const float* __restrict__ tsum, int64_t entries, int64_t tld, float* __restrict__ lse,
+    float* __restrict__ loss, int64_t K, Teacher t) {
+  __shared__ float red[LOSS_WAVES];
+  __shared__ int slot[TOP_MAX], base[4];
   const int64_t m = blockIdx.x;
   const int count = row_entries(t, m, slot, base);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const float over = lse[m];
+  auto all = [&](float v, auto fold) {  // over the waves, in all threads, in a fixed order
+    __syncthreads();
+    if (lane == 0) red[wave] = v;
+    __syncthreads();
+    v = red[0];
+    for (int w = 1; w < LOSS_WAVES; ++w) v = fold(v, red[w]);
+    return v;
+  };
+  float over;
+  if (tmax) {
+    float top = -__builtin_inff(), s = 0.f;
+    for (int64_t e = threadIdx.x; e < entries; e += 64 * LOSS_WAVES) top = fmaxf(top, tmax[m * tld + e]);
+    top = all(wave_max(top), [](float a, float b) { return fmaxf(a, b); });
+    for (int64_t e = threadIdx.x; e < entries; e += 64 * LOSS_WAVES) {
+      const float v = tsum[m * tld + e];
+      if (v != 0.f) s += v * exp_below(tmax[m * tld + e], top);
+    }
+    over = top + logf(all(wave_sum(s), [](float a, float b) { return a + b; }));
+    if (threadIdx.x == 0) lse[m] = over;
+  } else {
+    over = lse[m];
+  }
   float sum = 0.f;
-  for (int n = wave; n < count; n += 4) {
+  for (int n = wave; n < count; n += LOSS_WAVES) {
     const int64_t at = m * t.top + slot[n];
     const uint8_t* row = W + static_cast<int64_t>(t.at[at]) * (K / 32) * BLOCK_BYTES;
     float s = 0.f;
@@ -556,10 +579,8 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(const T* __restrict__
     const float q = t.q[at];
     if (q != 0.f) sum += q * (t.logq[at] + (over - s / t.temperature));
   }
-  if (lane == 0) red[wave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    loss[m] = count ? t.temperature * t.temperature * (((red[0] + red[1]) + red[2]) + red[3]) : 0.f;
+  sum = all(sum, [](float a, float b) { return a + b; });
+  if (threadIdx.x == 0) loss[m] = count ? t.temperature * t.temperature * sum : 0.f;
 }
 
 template <typename T>
@@ -775,6 +796,7 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
     const int64_t entries = cols / 64;
     if (!grad) {
       const bool last = n0 + p.piece >= N;
+      if (teacher && first && last) break;  // folded with the loss
       hipLaunchKernelGGL(xent_rows_kernel<false>, rows, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
                          entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, first, tlogit,
                          targets, N, last ? loss : nullptr, lse);
@@ -837,8 +859,10 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
     if (teacher)
       with_type(type, [&](auto v) {
         using T = decltype(v);
-        hipLaunchKernelGGL(distill_loss_kernel<T>, rows, dim3(256), 0, s, static_cast<const T*>(x), w, lse,
-                           loss, K, t);
+        const bool one = p.piece >= N;
+        hipLaunchKernelGGL(distill_loss_kernel<T>, rows, dim3(64 * LOSS_WAVES), 0, s,
+                           static_cast<const T*>(x), w, one ? f32(p.tmax) : nullptr, f32(p.tsum),
+                           (N + 63) / 64, p.entries, lse, loss, K, t);
       });
     return hipGetLastError();
   }
