@@ -607,8 +607,8 @@ __device__ __forceinline__ void logits_out(const f32x4 (&acc)[FM][4], int64_t m0
   }
 }
 
-// Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 179 us, 1500 in
-// one 354 us (845 and 853 TFLOP/s of binary16).  The block scale's FMAs keep the
+// Measured, 256 x 256 tiles: 375 x 32768 over 3072 in two parts 179 us (845
+// TFLOP/s of binary16), 1500 in one 330 (915).  The block scale's FMAs keep the
 // vector unit busy 48 % of the time beside the matrix cores' 33 %.
 template <typename S, int PA, bool STATS>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
@@ -833,7 +833,10 @@ constexpr int TW = 8;  // waves
 // (three: 620), 16 x 3072 x 4096 float32 8.2 us.
 // Waves wait 41 to 44 % of their cycles, mostly for a block's bytes: two per SIMD
 // do not cover them.
-template <int RT, int PA, int PB, typename T, bool ODD>
+// TWO: a second matrix's slices follow the first's (chosen at run time by every
+// call, the pointers cost one matrix 0.4 to 1.4 us: 64.0 us against 62.6 for the
+// gradient of 1500 x 5120 x 1280 bfloat16 with its other launches).
+template <int RT, int PA, int PB, typename T, bool ODD, bool TWO>
 __global__ __launch_bounds__(64 * TW) __attribute__((amdgpu_waves_per_eu(2, RT <= 1 ? 4 : 2)))
 void gemm_transposed_kernel(const f16x8* __restrict__ G1, const f16x8* __restrict__ G2,
                             const uint8_t* __restrict__ W1, const uint8_t* __restrict__ W2,
@@ -851,7 +854,7 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G1, const f16x8* __restric
   const unsigned item = xcd_order(blockIdx.x, gridDim.x);
   const int slice = item / tiles, tile = item % tiles;
   // slices from `splits` on are the second matrix's
-  const bool second = slice >= splits;
+  const bool second = TWO && slice >= splits;
   const f16x8* G = second ? G2 : G1;
   const uint8_t* W = second ? W2 : W1;
   const int split = second ? slice - splits : slice;
@@ -1107,8 +1110,11 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   auto go = [&](auto rtc, auto pa, auto pb, auto type) {
     using T = decltype(type);
     constexpr int RT = decltype(rtc)::value, PA = decltype(pa)::value, PB = decltype(pb)::value;
-    auto* kernel = p.K % 64 == 0 ? gemm_transposed_kernel<RT, PA, PB, T, false>
-                                 : gemm_transposed_kernel<RT, PA, PB, T, true>;
+    const bool odd = p.K % 64 != 0;
+    auto* kernel = p.w2 ? (odd ? gemm_transposed_kernel<RT, PA, PB, T, true, true>
+                               : gemm_transposed_kernel<RT, PA, PB, T, false, true>)
+                        : (odd ? gemm_transposed_kernel<RT, PA, PB, T, true, false>
+                               : gemm_transposed_kernel<RT, PA, PB, T, false, false>);
     const int64_t slices = static_cast<int64_t>(p.splits) * (p.w2 ? 2 : 1);
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * slices)), dim3(64 * TW), 0, s, p.g,
                        p.g2, p.w, p.w2, p.splits, p.n0, p.N, p.M, p.K, p.CB, mtiles, tiles, span,
