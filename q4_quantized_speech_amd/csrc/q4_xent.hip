@@ -324,7 +324,7 @@ struct Teacher {
 
 // A workgroup per row: q in float64 (the loss is a difference of logarithms),
 // and inv /= temperature, so that the products come out as l.
-// Measured: 1500 rows of 64 entries 6 us.
+// Measured: 8 rows of 16 entries 4.3 us (latency), 1500 of 64 14.4.
 __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ logits,
                                                                   double temperature, int64_t N,
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t*
 // Takes the teacher's tokens of a piece out of a row's logits (they become
 // -inf, their values are kept in t.logit) and of the 64-column maxima, then
 // moves the running maximum and sum as xent_rows_kernel does.
-// Measured per piece of 32768 columns, 1500 rows of 64 entries: 14 us.
+// Measured per piece of 32768 columns, 1500 rows of 64 entries: 10.5 us.
 __global__ __launch_bounds__(256) void distill_rows_kernel(
     float* __restrict__ logits, float* __restrict__ tmax, int64_t cols, int64_t ld, int64_t tld,
     int64_t n0, const float* __restrict__ psum, int chunks, float* __restrict__ run_max,
@@ -453,7 +453,10 @@ __device__ __forceinline__ int row_entries(const Teacher& t, int64_t m, int (&sl
   return all;
 }
 
-// loss, lse and the gradient: one workgroup per row.
+// loss, lse and the gradient: one workgroup per row.  Per teacher entry a row of
+// the table is decoded, eight weights of a dword at a time.
+// Measured: 375 rows of 32 entries, 1280 columns, float32 22 us; 1500 of 64, 3072
+// columns, bfloat16 75 (166 MB of table rows: 2.2 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void distill_final_kernel(
     const float* __restrict__ run_max, const float* __restrict__ run_sum,
