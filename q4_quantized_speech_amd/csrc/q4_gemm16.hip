@@ -843,7 +843,8 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G1, const f16x8* __restric
                             int splits, int64_t n0, int64_t N, int64_t M, int64_t K, int64_t CB, int mtiles, int tiles,
                             int64_t span, float* __restrict__ part, const float* __restrict__ alpha,
                             const float* __restrict__ inv, T* __restrict__ out) {
-  constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time
+  constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time (of three the last one alone)
+  static_assert(RT <= TW / 2, "two waves finish a row block");
   __shared__ f32x4 red[4][RP * 8][64];
   // two arrays: reading one does not have to wait for loads into the other
   using R = Raw<ODD>;
@@ -943,16 +944,16 @@ void gemm_transposed_kernel(const f16x8* __restrict__ G1, const f16x8* __restric
     if (t0) __syncthreads();
 #pragma unroll
     for (int e = 0; e < RP * 8; ++e)
-      if (wave >= 4) red[wave - 4][e][lane] = acc[t0 + e / 8][e % 8];
+      if (t0 + e / 8 < RT && wave >= 4) red[wave - 4][e][lane] = acc[t0 + e / 8][e % 8];
     __syncthreads();
     if (wave < 4) {
 #pragma unroll
       for (int e = 0; e < RP * 8; ++e)
-        red[wave][e][lane] = acc[t0 + e / 8][e % 8] + red[wave][e][lane];
+        if (t0 + e / 8 < RT) red[wave][e][lane] = acc[t0 + e / 8][e % 8] + red[wave][e][lane];
     }
     __syncthreads();
     const int t = wave >> 1;
-    if (t >= t0 && t < t0 + RP) {
+    if (t >= t0 && t < min(t0 + RP, RT)) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         s[c] = red[0][(t - t0) * 8 + 4 * h + c][lane];
