@@ -478,9 +478,8 @@ q4_status q4_gated_ffn(const void* w_gate, const void* w_up, const void* x, cons
  *           operands and two or more float32 copies of dx); as above.  Without
  *           dx none is needed.
  * dx: exact weights, float32 sums, dg and du before their rounding to dz's
- * type, scaled per row by a power of two into binary16: to 2^-22 in float32
- * and float16 (two parts), 2^-12 in bfloat16 (one), or 2^-33 of
- * max|dh| max|z| of the row.  Deterministic; a row that holds an
+ * type, scaled per row by a power of two into two binary16 parts whatever the
+ * type: to 2^-22 of them, or 2^-33 of max|dh| max|z| of the row.  Deterministic; a row that holds an
  * infinity or NaN gives non-finite values in that row only.
  */
 size_t q4_gated_ffn_grad_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);

@@ -66,7 +66,7 @@ q4_status q4_gated_ffn(const void* w_gate, const void* w_up, const void* x, cons
 
 size_t q4_gated_ffn_grad_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K) {
   if (!type_ok(type) || !ffn_shape_ok(M, N, K)) return 0;
-  return ffn_grad_workspace_bytes(type, M, N, K, device_info().cu_count);
+  return ffn_grad_workspace_bytes(M, N, K, device_info().cu_count);
 }
 
 q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z, const void* dh,
@@ -79,7 +79,7 @@ q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z,
       !aligned16(dz) || !aligned16(workspace))
     return Q4_ERR_ALIGN;
   const int cus = device_info().cu_count;
-  if (dx && (!workspace || ws_bytes < ffn_grad_workspace_bytes(type, M, N, K, cus)))
+  if (dx && (!workspace || ws_bytes < ffn_grad_workspace_bytes(M, N, K, cus)))
     return Q4_ERR_WORKSPACE;
   const FfnGradArgs a = {static_cast<const uint8_t*>(w_gate), static_cast<const uint8_t*>(w_up), z, dh,
                          dx, dz, act, type, M, N, K, workspace, static_cast<hipStream_t>(stream)};

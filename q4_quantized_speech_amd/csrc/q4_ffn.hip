@@ -725,10 +725,13 @@ __global__ __launch_bounds__(64 * BOUND_WAVES) void ffn_bound_kernel(const T* __
   inv[m] = is;
 }
 
-// dg and du as operand fragments (NATURAL over the columns), and where the
-// caller wants them in dz.  A wave takes 16 rows of 32 columns.
+// dg and du as operand fragments (NATURAL over the columns) of two parts whatever
+// the type, and where the caller wants them in dz: one part, 11 bits, would be
+// below bfloat16's own rounding for a term but not for a sum whose terms cancel
+// (random terms: dx 8.6e-4 from the exact one rounded, two parts 6e-5).  A wave
+// takes 16 rows of 32 columns.
 // Measured: 76 x 9216 float32 7.3 us, 1500 x 5120 bfloat16 14 (77 MB: 5.5 TB/s).
-template <int ACT, int PARTS, typename T>
+template <int ACT, typename T>
 __global__ __launch_bounds__(256) void ffn_dz_kernel(const T* z, const T* __restrict__ dh, T* dz,
                                                      const float* __restrict__ inv,
                                                      f16x8* __restrict__ fg, f16x8* __restrict__ fu,
@@ -787,10 +790,10 @@ __global__ __launch_bounds__(256) void ffn_dz_kernel(const T* z, const T* __rest
     for (int e = 0; e < 8; ++e) {
       const float x = v[e] * s;
       hi[e] = static_cast<_Float16>(x);
-      if constexpr (PARTS == 2) lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
+      lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
     }
     f[at] = hi;
-    if constexpr (PARTS == 2) f[part + at] = lo;
+    f[part + at] = lo;
   };
   put(fg, zg);
   put(fu, zu);
@@ -849,33 +852,31 @@ FfnPlan ffn_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
   return p;
 }
 
+constexpr int GRAD_UNITS = 3;  // products of a pair of fragments: two parts of each
 struct GradPlan {
-  int pa, rt, splits;  // splits of each projection
+  int rt, splits;  // splits of each projection
   int64_t rows;    // of a projection, padded
   size_t inv, fg, fu, part, total;
 };
 
-GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int cus) {
   GradPlan p = {};
   Carver c;
-  // one binary16 part of dg and du (2^-12) is an eighth of bfloat16's own half
-  // step; float16's result would be 1.4 times as far off as its rounding alone
-  p.pa = type == TYPE_BF16 ? 1 : 2;
   p.rows = (N + 63) / 64 * 64;
   // tiles of as many rows as leave the fewest products, and of equals the tallest
   // (76 rows: two of 48, not of 64)
   int64_t least = INT64_MAX;
   for (int rt = 4; rt >= 1; --rt) {
-    const int64_t clk = (M + 16 * rt - 1) / (16 * rt) * std::max(8 * rt * (p.pa + 1) * 16, 800);
+    const int64_t clk = (M + 16 * rt - 1) / (16 * rt) * std::max(8 * rt * GRAD_UNITS * 16, 800);
     if (clk < least) {
       least = clk;
       p.rt = rt;
     }
   }
-  p.splits = (transposed_plan(M, 2 * p.rows, K, p.pa + 1, cus, p.rt).splits + 1) / 2;
+  p.splits = (transposed_plan(M, 2 * p.rows, K, GRAD_UNITS, cus, p.rt).splits + 1) / 2;
   p.inv = c.take(static_cast<size_t>(M) * 4);
-  p.fg = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * p.pa);
-  p.fu = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * p.pa);
+  p.fg = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * 2);
+  p.fu = c.take(static_cast<size_t>(frag_elems(M, p.rows)) * 16 * 2);
   p.part = c.take(static_cast<size_t>(2 * p.splits) * M * K * 4);
   p.total = c.at;
   return p;
@@ -968,12 +969,12 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
   return hipGetLastError();
 }
 
-size_t ffn_grad_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus) {
-  return grad_plan(type, M, N, K, cus).total;
+size_t ffn_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus) {
+  return grad_plan(M, N, K, cus).total;
 }
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus) {
-  const GradPlan p = grad_plan(a.type, a.M, a.N, a.K, cus);
+  const GradPlan p = grad_plan(a.M, a.N, a.K, cus);
   char* base = static_cast<char*>(a.ws);
   f16x8* fg = a.dx ? reinterpret_cast<f16x8*>(base + p.fg) : nullptr;
   f16x8* fu = a.dx ? reinterpret_cast<f16x8*>(base + p.fu) : nullptr;
@@ -981,13 +982,12 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus) {
   const int64_t CB = p.rows / 32;
   with_type(a.type, [&](auto type) {
     using T = decltype(type);
-    constexpr int PARTS = __is_same(T, __bf16) ? 1 : 2;
     const T *z = static_cast<const T*>(a.z), *dh = static_cast<const T*>(a.dh);
     if (a.dx)
       hipLaunchKernelGGL(ffn_bound_kernel<T>, dim3(static_cast<unsigned>(a.M)), dim3(64 * BOUND_WAVES), 0, a.stream, z,
                          dh, inv, a.N);
     const dim3 grid(static_cast<unsigned>((a.M + 15) / 16), static_cast<unsigned>((CB + 3) / 4));
-    auto* kernel = a.act == ACT_SILU ? ffn_dz_kernel<ACT_SILU, PARTS, T> : ffn_dz_kernel<ACT_GELU, PARTS, T>;
+    auto* kernel = a.act == ACT_SILU ? ffn_dz_kernel<ACT_SILU, T> : ffn_dz_kernel<ACT_GELU, T>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, a.stream, z, dh,
                        static_cast<T*>(a.dz), inv, fg, fu, a.M, a.N, CB);
   });
@@ -996,7 +996,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus) {
   TransposedGemm g = {};
   g.g = fg;
   g.g2 = fu;
-  g.pa = p.pa;
+  g.pa = 2;
   g.pb = 2;
   g.type = a.type;
   g.w = a.gate;

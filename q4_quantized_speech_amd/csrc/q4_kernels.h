@@ -107,7 +107,7 @@ struct FfnGradArgs {
   void* ws;
   hipStream_t stream;
 };
-size_t ffn_grad_workspace_bytes(int type, int64_t M, int64_t N, int64_t K, int cus);
+size_t ffn_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_ffn_grad(const FfnGradArgs& a, int cus);
 
 // Cross entropy of the head against targets, or (teacher not null, targets
