@@ -116,13 +116,13 @@ __device__ __forceinline__ void load_columns(const T* row, int64_t n, int64_t N,
 // sequences with 0 to 7 drafts 26 us: bound by the float64 instructions of the
 // exponentials (17 a column, at half the rate of float32's), not by the bytes.
 template <typename T>
-__global__ __launch_bounds__(256) void verify_stats_kernel(Args a) {
+__global__ __launch_bounds__(256) void verify_stats_kernel(Args a, uint32_t first) {
   __shared__ float smax[4];
   __shared__ double ssum[4];
   __shared__ int32_t sat[4];
   constexpr int V = 16 / sizeof(T);
   const uint32_t chunks = static_cast<uint32_t>(a.chunks), rows = a.D + 1;
-  const uint32_t item = blockIdx.x, r = item / chunks, c = item - r * chunks, s = r / rows;
+  const uint32_t item = first + blockIdx.x, r = item / chunks, c = item - r * chunks, s = r / rows;
   if (static_cast<int>(r - s * rows) > length(a, s)) return;
   const T* row = static_cast<const T*>(a.logits) + static_cast<int64_t>(r) * a.N;
   const int64_t n0 = static_cast<int64_t>(c) * CHUNK;
@@ -454,18 +454,28 @@ hipError_t launch_verify(const VerifyArgs& v) {
   a.mass = reinterpret_cast<double*>(base);
   base += align256(v.S * a.chunks * sizeof(double));
   a.decision = reinterpret_cast<Decision*>(base);
+  // a dimension takes fewer than 2^32 threads: S (D + 1) ceil(N / CHUNK), which is below
+  // 2^29, in launches of at most 2^23 workgroups
+  const int64_t items = v.S * (v.D + 1) * a.chunks;
+  constexpr int64_t MOST = int64_t(1) << 23;
   // every workgroup takes the decision: about as many as run at once
   const int per = a.greedy ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.chunks, 1024 / v.S)));
+  hipError_t status = hipSuccess;
+  // after a launch that fails there is none: it would read what was not written
   with_type(v.type, [&](auto t) {
     using T = decltype(t);
-    hipLaunchKernelGGL(verify_stats_kernel<T>, dim3(static_cast<unsigned>(v.S * (v.D + 1) * a.chunks)),
-                       dim3(256), 0, v.stream, a);
+    for (int64_t first = 0; first < items; first += MOST) {
+      hipLaunchKernelGGL(verify_stats_kernel<T>, dim3(static_cast<unsigned>(std::min(MOST, items - first))),
+                         dim3(256), 0, v.stream, a, static_cast<uint32_t>(first));
+      if ((status = hipGetLastError()) != hipSuccess) return;
+    }
     hipLaunchKernelGGL(verify_mass_kernel<T>, dim3(static_cast<unsigned>(v.S * per)), dim3(256), 0, v.stream, a,
                        per);
-    if (!a.greedy)
-      hipLaunchKernelGGL(verify_draw_kernel<T>, dim3(static_cast<unsigned>(v.S)), dim3(256), 0, v.stream, a);
+    if ((status = hipGetLastError()) != hipSuccess || a.greedy) return;
+    hipLaunchKernelGGL(verify_draw_kernel<T>, dim3(static_cast<unsigned>(v.S)), dim3(256), 0, v.stream, a);
+    status = hipGetLastError();
   });
-  return hipGetLastError();
+  return status;
 }
 
 }  // namespace q4
