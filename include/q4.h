@@ -509,10 +509,12 @@ q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z,
  *           top) bytes of device scratch; its contents do not matter.  Calls
  *           that share it must be ordered.
  * Logits, maxima and sums are float32 over exact weights.  In the gradient the
- * teacher's tokens are taken out of the sum over the vocabulary and p - q is
- * formed for each of them in float32, so a student near its teacher keeps the
- * precision of the difference; the other probabilities are kept relative to
- * their largest and rounded as in q4_lmhead_xent.  |deq(T)| must stay below
+ * teacher's tokens are taken out of the sum over the vocabulary, and the loss
+ * and p - q of each of them are formed in float64 from the float32 logits, 1 - p
+ * and 1 - q of a token with q above one half from the sums of the others: a
+ * student near its teacher, or as sure as it, keeps the precision of the
+ * difference.  The other probabilities are kept relative to their largest and
+ * rounded as in q4_lmhead_xent.  |deq(T)| must stay below
  * 65504 for dx.  Deterministic; a row of x that holds an infinity or NaN, or
  * one of top_logits that holds NaN or +inf in a present entry, gives
  * non-finite values in that row only.

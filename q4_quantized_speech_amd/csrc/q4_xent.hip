@@ -29,12 +29,13 @@
 //
 // The teacher's tokens are taken out of each piece's logits, as the target is
 // above, and their part of the gradient, where p and q nearly cancel once the
-// student is trained, is formed in float32 at the end.
+// student is trained, is formed in float64 at the end.
 
 #include <algorithm>
 
 #include "q4_gemm16.h"
 #include "q4_kernels.h"
+#include "q4_wave.h"
 
 namespace q4 {
 namespace {
@@ -311,18 +312,18 @@ __global__ __launch_bounds__(256) void xent_chunk_kernel(const float* __restrict
 // ---------------------------------------------------------------------------
 constexpr int TOP_MAX = 256;  // teacher entries of a row: one thread each
 
-// What the other kernels take of the teacher, [M][top]: q and log q, the entry's
-// token or -1 (absent, or a repetition of an earlier entry, which has its sum).
+// What the other kernels take of the teacher, [M][top]: q, the entry's token or -1
+// (absent, or a repetition of an earlier entry, which has its sum).
 struct Teacher {
-  float *q, *logq;
+  double* q;
   int32_t* at;
   float* logit;   // the student's at those tokens
   int32_t* none;  // M targets outside the table
   int top;
-  float temperature;
+  double temperature;
 };
 
-// A workgroup per row: q in float64 (the loss is a difference of logarithms),
+// A workgroup per row: q in float64 (loss and gradient are differences from it),
 // and inv /= temperature, so that the products come out as l.
 // Measured: 8 rows of 16 entries 4.3 us (latency), 1500 of 64 14.4.
 __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t* __restrict__ ids,
@@ -363,8 +364,7 @@ __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t*
   }
   if (j < t.top) {
     const double q = first ? own / sum : 0.0;
-    t.q[m * t.top + j] = static_cast<float>(q);
-    t.logq[m * t.top + j] = q == 0.0 ? 0.f : static_cast<float>(log(q));
+    t.q[m * t.top + j] = q;
     t.at[m * t.top + j] = first ? mine : -1;
   }
   if (j == 0) {
@@ -453,6 +453,41 @@ __device__ __forceinline__ int row_entries(const Teacher& t, int64_t m, int (&sl
   return all;
 }
 
+// Over the first four waves of a workgroup, in all threads (the others bring 0).
+__device__ __forceinline__ double group_sum64(double v, double (&red)[4]) {
+  v = wave64_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0 && threadIdx.x < TOP_MAX) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return ((red[0] + red[1]) + red[2]) + red[3];
+}
+
+// A row's softmax and divergence in float64, thread j its j-th entry.  A student that
+// is sure of its teacher's likeliest token has a loss and a gradient far below 1: its
+// 1 - p and the teacher's 1 - q are sums over the others, log p and log q those of 1
+// less them, so that nothing is left to the rounding of a number next to 1.
+struct Divergence {
+  double over;  // log z, z = sum_n exp(l_n - base)
+  double z, sum;
+  double diff;  // p_j - q_j
+  // entry j: q and the student's logit less base (q = 0 past the entries); rest: what
+  // the tokens that are not the teacher's add to z
+  __device__ __forceinline__ Divergence(bool mine, double q, double d, double rest, double (&red)[4]) {
+    const bool likely = q > 0.5;  // one entry at most
+    const double e = mine ? exp(d) : 0.0;
+    const double own = group_sum64(likely ? e : 0.0, red);
+    const double left = group_sum64(likely ? 0.0 : q, red);  // 1 - q of the likely one
+    const double others = group_sum64(likely ? 0.0 : e, red) + rest;
+    const double top = group_sum64(likely ? d : 0.0, red);
+    z = own + others;
+    // log z = d + log(1 + others / own) where own is the most of z
+    over = own > others ? top + log1p(others / own) : log(z);
+    const double logq = likely ? log1p(-left) : log(q);
+    sum = group_sum64(mine && q != 0.0 ? q * (logq - d + over) : 0.0, red);
+    diff = likely ? left - others / z : e / z - q;
+  }
+};
+
 // loss, lse and the gradient: one workgroup per row.  Per teacher entry a row of
 // the table is decoded, eight weights of a dword at a time.
 // Measured: 375 rows of 32 entries, 1280 columns, float32 22 us; 1500 of 64, 3072
@@ -465,34 +500,32 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
     float* __restrict__ loss, float* __restrict__ lse, T* __restrict__ dx, int64_t M, int64_t K,
     Teacher t) {
   __shared__ float red[4], c[TOP_MAX];
+  __shared__ double red64[4];
   __shared__ int slot[TOP_MAX], base[4];
   __shared__ int64_t row[TOP_MAX];
   const int64_t m = blockIdx.x;
   const int count = row_entries(t, m, slot, base), j = threadIdx.x;
   const bool mine = j < count;
   const int64_t at = mine ? m * t.top + slot[j] : 0;
-  const float l = mine ? t.logit[at] : -__builtin_inff(), q = mine ? t.q[at] : 0.f;
+  const float l = mine ? t.logit[at] : -__builtin_inff();
+  const double q = mine ? t.q[at] : 0.0;
   float rest = run_sum[m];
   for (int i = 0; i < chunks; ++i) rest += psum[static_cast<int64_t>(i) * M + m];
   const float most = run_max[m], top = group_max(fmaxf(l, most), red);
-  const float el = mine ? exp_below(l, top) : 0.f, er = exp_below(most, top);
-  const float z = group_sum(el, red) + rest * er;
-  const float over = logf(z);
-  // q_j (log q_j - log p_j); an entry without probability adds nothing
-  const float term = mine && q != 0.f ? q * (t.logq[at] + (top - l) + over) : 0.f;
-  const float sum = group_sum(term, red);
-  const float tt = t.temperature;
+  const double er = exp(static_cast<double>(most) - top);
+  const Divergence v(mine, q, static_cast<double>(l) - top, rest * er, red64);
+  const double tt = t.temperature;
   if (j == 0) {
-    lse[m] = top + over;
-    loss[m] = count ? tt * tt * sum : 0.f;
+    lse[m] = static_cast<float>(top + v.over);
+    loss[m] = count ? static_cast<float>(tt * tt * v.sum) : 0.f;
   }
-  const float g = count ? (dloss ? dloss[m] : 1.f) * tt : 0.f;
+  const float g = count ? (dloss ? dloss[m] : 1.f) * static_cast<float>(tt) : 0.f;
   if (mine) {
-    c[j] = el / z - q;
+    c[j] = static_cast<float>(v.diff);
     row[j] = t.at[at] * (K / 32);
   }
   __syncthreads();
-  const float f = er / z * (1.f / P_SCALE);
+  const float f = static_cast<float>(er / v.z * (1.0 / P_SCALE));
   for (int64_t u = threadIdx.x; u < K / 8; u += 256) {
     const int64_t b = u >> 2;
     const int i = static_cast<int>(u & 3);
@@ -579,11 +612,11 @@ __global__ __launch_bounds__(64 * LOSS_WAVES) void distill_loss_kernel(
       for (int e = 0; e < 4; ++e) s = __builtin_fmaf(w[4 + e], b[e], __builtin_fmaf(w[e], a[e], s));
     }
     s = wave_sum(s);
-    const float q = t.q[at];
-    if (q != 0.f) sum += q * (t.logq[at] + (over - s / t.temperature));
+    const double q = t.q[at];
+    if (q != 0.0) sum += static_cast<float>(q * (log(q) + (over - s / t.temperature)));
   }
   sum = all(sum, [](float a, float b) { return a + b; });
-  if (threadIdx.x == 0) loss[m] = count ? t.temperature * t.temperature * sum : 0.f;
+  if (threadIdx.x == 0) loss[m] = count ? static_cast<float>(t.temperature * t.temperature * sum) : 0.f;
 }
 
 template <typename T>
@@ -621,7 +654,7 @@ struct XentPlan {
   Tile t1, t2;
   int64_t piece, entries, chunks;
   size_t x, inv, run_max, run_sum, tlogit, alpha, tmax, tsum, psum, logits, codes, scale, wt, prob,
-      part, q, logq, at, student, none, total;
+      part, q, at, student, none, total;
 };
 
 // top: teacher entries of a row (0: a loss against targets).
@@ -699,8 +732,7 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int64_t
     p.tsum = c.take(static_cast<size_t>(M) * p.entries * 4);
   }
   if (top) {
-    p.q = c.take(static_cast<size_t>(M) * top * 4);
-    p.logq = c.take(static_cast<size_t>(M) * top * 4);
+    p.q = c.take(static_cast<size_t>(M) * top * 8);
     p.at = c.take(static_cast<size_t>(M) * top * 4);
     p.student = c.take(static_cast<size_t>(M) * top * 4);
     p.none = c.take(static_cast<size_t>(M) * 4);
@@ -764,9 +796,8 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
   Q4_TRY(prep_rows(x, type, Order::NIBBLE, xa, f32(p.inv), M, K, s));
   Teacher t = {};
   if (teacher) {
-    t = {f32(p.q), f32(p.logq), reinterpret_cast<int32_t*>(base + p.at), f32(p.student),
-         reinterpret_cast<int32_t*>(base + p.none), static_cast<int>(teacher->top),
-         static_cast<float>(teacher->temperature)};
+    t = {reinterpret_cast<double*>(base + p.q), reinterpret_cast<int32_t*>(base + p.at), f32(p.student),
+         reinterpret_cast<int32_t*>(base + p.none), static_cast<int>(teacher->top), teacher->temperature};
     targets = t.none;
     hipLaunchKernelGGL(distill_teacher_kernel, rows, dim3(TOP_MAX), 0, s, teacher->ids, teacher->logits,
                        teacher->temperature, N, f32(p.inv), t);
