@@ -33,7 +33,7 @@
 
 #include <algorithm>
 
-#include "q4_gemm16.h"
+#include "q4_gemm16_tiles.h"
 #include "q4_kernels.h"
 #include "q4_wave.h"
 
@@ -318,19 +318,21 @@ struct Teacher {
   double* q;
   int32_t* at;
   float* logit;   // the student's at those tokens
-  int32_t* none;  // M targets outside the table
+  // M targets for the logits' kernels: the token with q above one half where the loss
+  // alone is computed, -1 (none) else
+  int32_t* target;
   int top;
   double temperature;
 };
 
 // A workgroup per row: q in float64 (loss and gradient are differences from it),
 // and inv /= temperature, so that the products come out as l.
-// Measured: 8 rows of 16 entries 4.3 us (latency), 1500 of 64 14.4.
+// Measured: 8 rows of 16 entries 4.2 us (latency), 1500 of 64 14.7.
 __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ logits,
-                                                                  double temperature, int64_t N,
+                                                                  double temperature, int64_t N, bool alone,
                                                                   float* __restrict__ inv, Teacher t) {
-  __shared__ int32_t id[TOP_MAX];
+  __shared__ int32_t id[TOP_MAX], target;
   __shared__ double e[TOP_MAX];
   const int64_t m = blockIdx.x;
   const int j = threadIdx.x;
@@ -344,6 +346,7 @@ __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t*
   }
   id[j] = mine;
   e[j] = b;
+  if (j == 0) target = -1;
   __syncthreads();
   double top = none;
   for (int i = 0; i < t.top; ++i) top = e[i] > top || e[i] != e[i] ? e[i] : top;
@@ -366,9 +369,11 @@ __global__ __launch_bounds__(TOP_MAX) void distill_teacher_kernel(const int32_t*
     const double q = first ? own / sum : 0.0;
     t.q[m * t.top + j] = q;
     t.at[m * t.top + j] = first ? mine : -1;
+    if (alone && q > 0.5) target = mine;
   }
+  __syncthreads();
   if (j == 0) {
-    t.none[m] = -1;
+    t.target[m] = target;
     inv[m] = static_cast<float>(inv[m] / temperature);
   }
 }
@@ -434,12 +439,13 @@ __device__ __forceinline__ void weights8(const uint8_t* blk, int i, float (&w)[8
   for (int e = 0; e < 8; ++e) w[e] = (w[e] - 8.f) * d;
 }
 
-// Compacts a row's entries (token >= 0) into LDS, in order, and returns their
-// number.  All threads, at least 256; ends with a barrier.
+// Compacts a row's entries (token >= 0) into LDS, their places and tokens in order,
+// and returns their number.  All threads, at least 256; ends with a barrier.
 __device__ __forceinline__ int row_entries(const Teacher& t, int64_t m, int (&slot)[TOP_MAX],
-                                           int (&base)[4]) {
+                                           int (&token)[TOP_MAX], int (&base)[4]) {
   const int j = threadIdx.x, lane = j & 63, wave = j >> 6;
-  const bool here = j < t.top && t.at[m * t.top + j] >= 0;
+  const int at = j < t.top ? t.at[m * t.top + j] : -1;
+  const bool here = at >= 0;
   const uint64_t mask = __ballot(here);
   if (lane == 0 && wave < 4) base[wave] = __popcll(mask);  // (the others hold none)
   __syncthreads();
@@ -448,7 +454,11 @@ __device__ __forceinline__ int row_entries(const Teacher& t, int64_t m, int (&sl
     if (w < wave) from += base[w];
     all += base[w];
   }
-  if (here) slot[from + __popcll(mask & ((uint64_t(1) << lane) - 1))] = j;
+  if (here) {
+    const int n = from + __popcll(mask & ((uint64_t(1) << lane) - 1));
+    slot[n] = j;
+    token[n] = at;
+  }
   __syncthreads();
   return all;
 }
@@ -471,13 +481,15 @@ struct Divergence {
   double z, sum;
   double diff;  // p_j - q_j
   // entry j: q and the student's logit less base (q = 0 past the entries); rest: what
-  // the tokens that are not the teacher's add to z
-  __device__ __forceinline__ Divergence(bool mine, double q, double d, double rest, double (&red)[4]) {
+  // the tokens that are not the teacher's add to z, with ALL all but the likely one
+  template <bool ALL>
+  __device__ __forceinline__ Divergence(std::bool_constant<ALL>, bool mine, double q, double d, double rest,
+                                        double (&red)[4]) {
     const bool likely = q > 0.5;  // one entry at most
     const double e = mine ? exp(d) : 0.0;
     const double own = group_sum64(likely ? e : 0.0, red);
     const double left = group_sum64(likely ? 0.0 : q, red);  // 1 - q of the likely one
-    const double others = group_sum64(likely ? 0.0 : e, red) + rest;
+    const double others = ALL ? rest : group_sum64(likely ? 0.0 : e, red) + rest;
     const double top = group_sum64(likely ? d : 0.0, red);
     z = own + others;
     // log z = d + log(1 + others / own) where own is the most of z
@@ -491,7 +503,7 @@ struct Divergence {
 // loss, lse and the gradient: one workgroup per row.  Per teacher entry a row of
 // the table is decoded, eight weights of a dword at a time.
 // Measured: 375 rows of 32 entries, 1280 columns, float32 22 us; 1500 of 64, 3072
-// columns, bfloat16 75 (166 MB of table rows: 2.2 TB/s).
+// columns, bfloat16 77 (166 MB of table rows: 2.2 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void distill_final_kernel(
     const float* __restrict__ run_max, const float* __restrict__ run_sum,
@@ -501,10 +513,10 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
     Teacher t) {
   __shared__ float red[4], c[TOP_MAX];
   __shared__ double red64[4];
-  __shared__ int slot[TOP_MAX], base[4];
+  __shared__ int slot[TOP_MAX], token[TOP_MAX], base[4];
   __shared__ int64_t row[TOP_MAX];
   const int64_t m = blockIdx.x;
-  const int count = row_entries(t, m, slot, base), j = threadIdx.x;
+  const int count = row_entries(t, m, slot, token, base), j = threadIdx.x;
   const bool mine = j < count;
   const int64_t at = mine ? m * t.top + slot[j] : 0;
   const float l = mine ? t.logit[at] : -__builtin_inff();
@@ -513,7 +525,7 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
   for (int i = 0; i < chunks; ++i) rest += psum[static_cast<int64_t>(i) * M + m];
   const float most = run_max[m], top = group_max(fmaxf(l, most), red);
   const double er = exp(static_cast<double>(most) - top);
-  const Divergence v(mine, q, static_cast<double>(l) - top, rest * er, red64);
+  const Divergence v(std::false_type{}, mine, q, static_cast<double>(l) - top, rest * er, red64);
   const double tt = t.temperature;
   if (j == 0) {
     lse[m] = static_cast<float>(top + v.over);
@@ -522,7 +534,7 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
   const float g = count ? (dloss ? dloss[m] : 1.f) * static_cast<float>(tt) : 0.f;
   if (mine) {
     c[j] = static_cast<float>(v.diff);
-    row[j] = t.at[at] * (K / 32);
+    row[j] = token[j] * (K / 32);
   }
   __syncthreads();
   const float f = static_cast<float>(er / v.z * (1.0 / P_SCALE));
@@ -559,22 +571,68 @@ __global__ __launch_bounds__(256) void distill_final_kernel(
   }
 }
 
-// The loss alone: the student's logits at the teacher's tokens, a wave per entry.
-// tmax, tsum (nullable): the maxima and sums of a table in one piece, folded here
-// into lse; else lse is read.
-// Measured: 8 rows of 16 entries, 1280 columns, with the fold 6.9 us (the fold
-// apart 4.7, and 8.3 with four waves).
+// The loss alone.  The student's logits at the teacher's tokens come from the products,
+// scales and order of the logits' kernels on the same operands: the same bits as in the
+// sums, so a student at its teacher has no loss (a dot product of its own differed by
+// up to 1e-6 of either sign).  The waves take the products of 16 tokens and one block
+// each (of a tile's 16 rows one counts), then a thread per token adds them in order.
+// A: prep_rows' operands.  tmax, tsum (nullable): the maxima and sums of a table in one
+// piece, folded here; else run_max and run_sum are.
+// Measured: 8 rows of 16 entries, 1280 columns float32, with the fold 10.3 us; latency (dot
+// products took 7.1; products and sums by one wave per 16 tokens 22).
 constexpr int LOSS_WAVES = 16;
-template <typename T>
+constexpr int LOSS_ITEMS = 512;  // products kept at a time
+template <int PA>
 __global__ __launch_bounds__(64 * LOSS_WAVES) void distill_loss_kernel(
-    const T* __restrict__ x, const uint8_t* __restrict__ W, const float* __restrict__ tmax,
-    const float* __restrict__ tsum, int64_t entries, int64_t tld, float* __restrict__ lse,
-    float* __restrict__ loss, int64_t K, Teacher t) {
-  __shared__ float red[LOSS_WAVES];
-  __shared__ int slot[TOP_MAX], base[4];
+    const f16x8* __restrict__ A, const float* __restrict__ inv, const uint8_t* __restrict__ W,
+    const float* __restrict__ tmax, const float* __restrict__ tsum, int64_t entries, int64_t tld,
+    const float* __restrict__ run_max, const float* __restrict__ run_sum, float* __restrict__ lse,
+    float* __restrict__ loss, int64_t M, int64_t K, int64_t CB, Teacher t) {
+  __shared__ float red[LOSS_WAVES], product[LOSS_ITEMS][16], scale[LOSS_ITEMS][16];
+  __shared__ double red64[4];
+  __shared__ int slot[TOP_MAX], token[TOP_MAX], base[4];
   const int64_t m = blockIdx.x;
-  const int count = row_entries(t, m, slot, base);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int j = threadIdx.x;
+  // asked for first: two entries a thread are 131072 columns
+  float em[2], es[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t e = j + u * 64 * LOSS_WAVES;
+    em[u] = tmax && e < entries ? tmax[m * tld + e] : -__builtin_inff();
+    es[u] = tmax && e < entries ? tsum[m * tld + e] : 0.f;
+  }
+  const int count = row_entries(t, m, slot, token, base);
+  const int lane = j & 63, wave = j >> 6, i = lane & 15, g = lane >> 4;
+  const bool mine = j < count;
+  const int tiles = (count + 15) / 16, r = static_cast<int>(m & 15);
+  const int64_t KB = K / 32, part = (M + 15) / 16 * CB * 64;
+  const f16x8* a = A + (m >> 4) * CB * 64 + lane;
+  float l = 0.f;  // entry j's logit
+  for (int64_t b0 = 0; tiles && b0 < KB; b0 += LOSS_ITEMS / tiles) {
+    const int blocks = static_cast<int>(min<int64_t>(LOSS_ITEMS / tiles, KB - b0));
+#pragma unroll 4
+    for (int item = wave; item < blocks * tiles; item += LOSS_WAVES) {
+      const int64_t b = b0 + item / tiles;
+      const int64_t row = token[min(item % tiles * 16 + i, count - 1)] * KB;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(W + (row + b) * BLOCK_BYTES);
+      const f16x8 q = codes8(p[1 + 2 * g] | static_cast<uint32_t>(p[2 + 2 * g]) << 16);
+      f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b * 64], q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      if constexpr (PA == 2) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[part + b * 64], q, s, 0, 0, 0);
+      if (g == r >> 2) {  // row 4 g + v of the tile
+        product[item][i] = r & 2 ? (r & 1 ? s.w : s.z) : (r & 1 ? s.y : s.x);
+        scale[item][i] = half_bits_to_float(p[0]);
+      }
+    }
+    __syncthreads();
+    if (mine) {
+#pragma unroll 8
+      for (int b = 0; b < blocks; ++b) {
+        const int item = b * tiles + (j >> 4);
+        l = __builtin_fmaf(scale[item][j & 15], product[item][j & 15], l);
+      }
+    }
+    __syncthreads();
+  }
   auto all = [&](float v, auto fold) {  // over the waves, in all threads, in a fixed order
     __syncthreads();
     if (lane == 0) red[wave] = v;
@@ -583,40 +641,31 @@ __global__ __launch_bounds__(64 * LOSS_WAVES) void distill_loss_kernel(
     for (int w = 1; w < LOSS_WAVES; ++w) v = fold(v, red[w]);
     return v;
   };
-  float over;
+  float top, s = 0.f;
   if (tmax) {
-    float top = -__builtin_inff(), s = 0.f;
-    for (int64_t e = threadIdx.x; e < entries; e += 64 * LOSS_WAVES) top = fmaxf(top, tmax[m * tld + e]);
-    top = all(wave_max(top), [](float a, float b) { return fmaxf(a, b); });
-    for (int64_t e = threadIdx.x; e < entries; e += 64 * LOSS_WAVES) {
-      const float v = tsum[m * tld + e];
-      if (v != 0.f) s += v * exp_below(tmax[m * tld + e], top);
-    }
-    over = top + logf(all(wave_sum(s), [](float a, float b) { return a + b; }));
-    if (threadIdx.x == 0) lse[m] = over;
-  } else {
-    over = lse[m];
-  }
-  float sum = 0.f;
-  for (int n = wave; n < count; n += LOSS_WAVES) {
-    const int64_t at = m * t.top + slot[n];
-    const uint8_t* row = W + static_cast<int64_t>(t.at[at]) * (K / 32) * BLOCK_BYTES;
-    float s = 0.f;
-    for (int64_t u = lane; u < K / 8; u += 64) {
-      float w[8], a[4], b[4];
-      weights8(row + (u >> 2) * BLOCK_BYTES, static_cast<int>(u & 3), w);
-      const T* p = x + m * K + 32 * (u >> 2) + 4 * (u & 3);
-      load_f32<4>(p, a);
-      load_f32<4>(p + 16, b);
+    float own = fmaxf(em[0], em[1]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = __builtin_fmaf(w[4 + e], b[e], __builtin_fmaf(w[e], a[e], s));
+    for (int u = 0; u < 2; ++u)
+      if (es[u] != 0.f) s += es[u] * exp_below(em[u], own);
+    for (int64_t e = j + 2 * 64 * LOSS_WAVES; e < entries; e += 64 * LOSS_WAVES) {
+      const float v = tsum[m * tld + e], up = fmaxf(own, tmax[m * tld + e]);
+      s *= exp_below(own, up);
+      if (v != 0.f) s += v * exp_below(tmax[m * tld + e], up);
+      own = up;
     }
-    s = wave_sum(s);
-    const double q = t.q[at];
-    if (q != 0.0) sum += static_cast<float>(q * (log(q) + (over - s / t.temperature)));
+    top = all(wave_max(own), [](float a, float b) { return fmaxf(a, b); });
+    if (s != 0.f) s *= exp_below(own, top);
+    s = all(wave_sum(s), [](float a, float b) { return a + b; });
+  } else {
+    top = run_max[m];
+    s = run_sum[m];
   }
-  sum = all(sum, [](float a, float b) { return a + b; });
-  if (threadIdx.x == 0) loss[m] = count ? static_cast<float>(t.temperature * t.temperature * sum) : 0.f;
+  const Divergence v(std::true_type{}, mine, mine ? t.q[m * t.top + slot[j]] : 0.0,
+                     mine ? static_cast<double>(l * inv[m]) - top : 0.0, s, red64);
+  if (j == 0) {
+    lse[m] = static_cast<float>(top + v.over);
+    loss[m] = count ? static_cast<float>(t.temperature * t.temperature * v.sum) : 0.f;
+  }
 }
 
 template <typename T>
@@ -654,7 +703,7 @@ struct XentPlan {
   Tile t1, t2;
   int64_t piece, entries, chunks;
   size_t x, inv, run_max, run_sum, tlogit, alpha, tmax, tsum, psum, logits, codes, scale, wt, prob,
-      part, q, at, student, none, total;
+      part, q, at, student, target, total;
 };
 
 // top: teacher entries of a row (0: a loss against targets).
@@ -735,7 +784,7 @@ XentPlan xent_plan(int type, bool grad, int64_t M, int64_t N, int64_t K, int64_t
     p.q = c.take(static_cast<size_t>(M) * top * 8);
     p.at = c.take(static_cast<size_t>(M) * top * 4);
     p.student = c.take(static_cast<size_t>(M) * top * 4);
-    p.none = c.take(static_cast<size_t>(M) * 4);
+    p.target = c.take(static_cast<size_t>(M) * 4);
   }
   p.total = c.at;
   return p;
@@ -797,10 +846,10 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
   Teacher t = {};
   if (teacher) {
     t = {reinterpret_cast<double*>(base + p.q), reinterpret_cast<int32_t*>(base + p.at), f32(p.student),
-         reinterpret_cast<int32_t*>(base + p.none), static_cast<int>(teacher->top), teacher->temperature};
-    targets = t.none;
+         reinterpret_cast<int32_t*>(base + p.target), static_cast<int>(teacher->top), teacher->temperature};
+    targets = t.target;
     hipLaunchKernelGGL(distill_teacher_kernel, rows, dim3(TOP_MAX), 0, s, teacher->ids, teacher->logits,
-                       teacher->temperature, N, f32(p.inv), t);
+                       teacher->temperature, N, !grad, f32(p.inv), t);
     Q4_TRY(hipGetLastError());
   }
   for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
@@ -833,7 +882,7 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
       if (teacher && first && last) break;  // folded with the loss
       hipLaunchKernelGGL(xent_rows_kernel<false>, rows, dim3(256), 0, s, f32(p.tmax), f32(p.tsum),
                          entries, p.entries, nullptr, 0, run_max, run_sum, nullptr, M, first, tlogit,
-                         targets, N, last ? loss : nullptr, lse);
+                         targets, N, last && !teacher ? loss : nullptr, lse);
       Q4_TRY(hipGetLastError());
       continue;
     }
@@ -890,14 +939,12 @@ hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
     Q4_TRY(launch_gemm_plain(p.t2, g, s));
   }
   if (!grad) {
-    if (teacher)
-      with_type(type, [&](auto v) {
-        using T = decltype(v);
-        const bool one = p.piece >= N;
-        hipLaunchKernelGGL(distill_loss_kernel<T>, rows, dim3(64 * LOSS_WAVES), 0, s,
-                           static_cast<const T*>(x), w, one ? f32(p.tmax) : nullptr, f32(p.tsum),
-                           (N + 63) / 64, p.entries, lse, loss, K, t);
-      });
+    if (teacher) {
+      const bool one = p.piece >= N;
+      auto* kernel = p.pa == 2 ? distill_loss_kernel<2> : distill_loss_kernel<1>;
+      hipLaunchKernelGGL(kernel, rows, dim3(64 * LOSS_WAVES), 0, s, xa, f32(p.inv), w, one ? f32(p.tmax) : nullptr,
+                         f32(p.tsum), (N + 63) / 64, p.entries, run_max, run_sum, lse, loss, M, K, blocks32(K), t);
+    }
     return hipGetLastError();
   }
   if (teacher) {

@@ -104,6 +104,24 @@ def test_student_sure_of_its_teachers_token(m, n, k, top, dtype):
         assert torch.allclose(lse, lse2, rtol=2 ** -20, atol=0)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("m,n,k,top", SHAPES)
+def test_sure_students_loss_alone(m, n, k, top, dtype):
+    wq, w = D.table(n, k, 500 + m)
+    gen = torch.Generator(device="cuda").manual_seed(m + top)
+    ids = torch.stack([torch.randperm(n, device="cuda", generator=gen)[:top] for _ in range(m)]).to(torch.int32)
+    margin = torch.linspace(12.0, 50.0, m, device="cuda", dtype=torch.float64)
+    x = lean(w, ids[:, 0].long(), margin, gen).to(dtype)
+    logits = torch.randn((m, top), device="cuda", generator=gen)
+    logits[:, 0] = margin.float() + 1.0
+    for temp in (1.0, 1.5):
+        announce(f"lmhead_distill sure, loss alone {m}x{n}x{k} top {top} {dtype} temperature {temp}")
+        loss, lse, _ = q4.lmhead_distill(wq, x, ids, logits, temperature=temp)
+        torch.cuda.synchronize()
+        want, tl, _, _, _ = reference(w, x, ids, logits, temp)
+        D.assert_close(loss, want, tl, "loss alone")
+
+
 def at_teacher(m, n, k, top, temp, dtype, seed):
     """A student at its teacher: the teacher's logits are the student's best, all that matter."""
     wq, w = D.table(n, k, seed)
@@ -113,7 +131,7 @@ def at_teacher(m, n, k, top, temp, dtype, seed):
     return wq, w, x, best.indices.to(torch.int32), best.values.float().contiguous()
 
 
-@pytest.mark.parametrize("grad", [True])
+@pytest.mark.parametrize("grad", [True, False])
 @pytest.mark.parametrize("m,n,k,top,temp,dtype", [(24, 256, 256, 256, 1.0, F32), (24, 200, 256, 200, 4.0, F32),
                                                   (90, 256, 512, 256, 2.0, F32), (70, 180, 96, 180, 16.0, BF16),
                                                   (7, 250, 1280, 250, 8.0, F16)])
