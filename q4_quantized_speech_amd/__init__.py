@@ -695,14 +695,17 @@ def gated_ffn(w_gate: torch.Tensor, w_up: torch.Tensor, x: torch.Tensor, act: st
 def gated_ffn_grad(w_gate: torch.Tensor, w_up: torch.Tensor, z: torch.Tensor, dh: torch.Tensor,
                    act: str = "silu", keep: bool = False, dx: torch.Tensor | None = None,
                    dz: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                   stream=None):
+                   stream=None, need_dx: bool = True):
     """(dx, dz): the gradient of ``gated_ffn`` for dh [M, N], the gradient of its h, from the z
     it kept.  dx is [M, K]; dz [M, 2 N], with ``keep`` (or a ``dz`` to write, which may be z),
     the gradient of r and the dy of ``lora_grad`` for adapters beside the projections, else
-    None."""
+    None.  Without ``need_dx`` (the model's first block) dx is None, and dz alone is computed,
+    without its products and without a workspace."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return gated_ffn_grad(w_gate, w_up, z, dh, act, keep, dx, dz, workspace)
+            return gated_ffn_grad(w_gate, w_up, z, dh, act, keep, dx, dz, workspace, None, need_dx)
+    if not need_dx and (dx is not None or not (keep or dz is not None)):
+        raise ValueError("without need_dx there is no dx to write, and dz is needed (keep, or a dz to write)")
     code, n, k = _gated(w_gate, w_up, act)
     t = _activations(z, "z")
     m, n2 = z.shape
@@ -712,14 +715,16 @@ def gated_ffn_grad(w_gate: torch.Tensor, w_up: torch.Tensor, z: torch.Tensor, dh
         if v is not None:
             _matrix(v, name, (m, width), z.dtype)
     dev = _gpu(w_gate, w_up, z, dh, dx, dz)
-    if dx is None:
-        dx = torch.empty((m, k), dtype=z.dtype, device=z.device)
+    ws = None
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((m, k), dtype=z.dtype, device=z.device)
+        ws = _scratch(workspace, "q4_gated_ffn_grad_workspace_bytes", dev, t, m, n, k)
     if keep and dz is None:
         dz = torch.empty((m, 2 * n), dtype=z.dtype, device=z.device)
-    ws = _scratch(workspace, "q4_gated_ffn_grad_workspace_bytes", dev, t, m, n, k)
     _check(lib().q4_gated_ffn_grad(w_gate.data_ptr(), w_up.data_ptr(), z.data_ptr(), dh.data_ptr(),
-                                   dx.data_ptr(), _addr(dz), code, t, m, n, k, ws.data_ptr(),
-                                   ws.numel(), _raw_stream(dev)), "q4_gated_ffn_grad")
+                                   _addr(dx), _addr(dz), code, t, m, n, k, _addr(ws),
+                                   ws.numel() if need_dx else 0, _raw_stream(dev)), "q4_gated_ffn_grad")
     return dx, dz
 
 
