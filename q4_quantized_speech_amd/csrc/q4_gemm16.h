@@ -94,11 +94,11 @@ struct TransposedGemm {
   float* part;
   const float *alpha, *inv;
   void* out;
-  // w2 (nullable): a second matrix of N rows with its own G; its slices follow
-  // the first one's in part
+  // w2 (nullable): a second matrix of N rows with its own G, two parts of both; its
+  // slices follow the first one's in part
   const f16x8* g2;
   const uint8_t* w2;
-  int rt;  // 16-row tiles of a workgroup, 1 to 4 (0: transposed_rt(M))
+  int rt;  // with w2: 16-row tiles of a workgroup, 1 to 4 (else 0: transposed_rt(M))
 };
 struct TransposedPlan {
   double us;  // estimate

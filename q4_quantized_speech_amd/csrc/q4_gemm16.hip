@@ -1108,15 +1108,13 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   const int mtiles = static_cast<int>((p.M + 16 * rt - 1) / (16 * rt));
   const int tiles = static_cast<int>(mtiles * ((p.K + 127) / 128));
   const int64_t span = (p.CB + p.splits - 1) / p.splits;
-  auto go = [&](auto rtc, auto pa, auto pb, auto type) {
+  auto go = [&](auto rtc, auto pa, auto pb, auto type, auto two) {
     using T = decltype(type);
     constexpr int RT = decltype(rtc)::value, PA = decltype(pa)::value, PB = decltype(pb)::value;
-    const bool odd = p.K % 64 != 0;
-    auto* kernel = p.w2 ? (odd ? gemm_transposed_kernel<RT, PA, PB, T, true, true>
-                               : gemm_transposed_kernel<RT, PA, PB, T, false, true>)
-                        : (odd ? gemm_transposed_kernel<RT, PA, PB, T, true, false>
-                               : gemm_transposed_kernel<RT, PA, PB, T, false, false>);
-    const int64_t slices = static_cast<int64_t>(p.splits) * (p.w2 ? 2 : 1);
+    constexpr bool TWO = decltype(two)::value;
+    auto* kernel = p.K % 64 != 0 ? gemm_transposed_kernel<RT, PA, PB, T, true, TWO>
+                                 : gemm_transposed_kernel<RT, PA, PB, T, false, TWO>;
+    const int64_t slices = static_cast<int64_t>(p.splits) * (TWO ? 2 : 1);
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * slices)), dim3(64 * TW), 0, s, p.g,
                        p.g2, p.w, p.w2, p.splits, p.n0, p.N, p.M, p.K, p.CB, mtiles, tiles, span,
                        p.part, p.alpha, p.inv, static_cast<T*>(p.out));
@@ -1124,18 +1122,27 @@ hipError_t launch_gemm_transposed(const TransposedGemm& p, hipStream_t s) {
   using std::integral_constant;
   const integral_constant<int, 1> one;
   const integral_constant<int, 2> two;
+  const integral_constant<int, 4> four;
+  if (p.w2) {  // the gated block's gradient: two parts of both, slices
+    auto pair = [&](auto rtc) { go(rtc, two, two, float{}, std::true_type{}); };
+    if (rt == 1) pair(one);
+    else if (rt == 2) pair(two);
+    else if (rt == 3) pair(integral_constant<int, 3>{});
+    else pair(four);
+    return hipGetLastError();
+  }
   auto parts = [&](auto rtc) {
+    const std::false_type single;
     // float32 has two parts of both, float16 and bfloat16 one of G; the head's
     // gradient, which writes slices whatever its type, one of both there
-    if (p.pa == 2) go(rtc, two, two, float{});
-    else if (p.pb == 1) go(rtc, one, one, float{});
-    else if (p.type == TYPE_F16) go(rtc, one, two, _Float16{});
-    else go(rtc, one, two, __bf16{});
+    if (p.pa == 2) go(rtc, two, two, float{}, single);
+    else if (p.pb == 1) go(rtc, one, one, float{}, single);
+    else if (p.type == TYPE_F16) go(rtc, one, two, _Float16{}, single);
+    else go(rtc, one, two, __bf16{}, single);
   };
   if (rt == 1) parts(one);
   else if (rt == 2) parts(two);
-  else if (rt == 3) parts(integral_constant<int, 3>{});
-  else parts(integral_constant<int, 4>{});
+  else parts(four);
   return hipGetLastError();
 }
 
