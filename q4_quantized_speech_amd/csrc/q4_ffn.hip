@@ -95,8 +95,14 @@ __device__ __forceinline__ void finish(const Out& o, int64_t m, int64_t n, float
 // 4 x 4 transpositions over the lane groups give it dword g of each of the
 // eight blocks, the operand of the exact codes q - 8.
 // ---------------------------------------------------------------------------
-constexpr int FW = 8;            // waves at most
-constexpr int64_t FEW_ROWS = 64; // rows of x this route takes
+constexpr int FW = 8;  // waves at most
+// Rows of x this route takes: four tiles of 16, whose sums fill the registers.  Above,
+// unpacking the codes of both projections costs 35 us (2 x 9216 x 3072) whatever the
+// number of rows.  This route and the unpacked one, weights from memory, us:
+// 2 x 9216 x 3072 float32 32 rows 31.4 and 91.0, 64 41.3 and 95.1; bfloat16 64 33.8
+// and 84.0; 2 x 5120 x 1280 float32 64 18.9 and 50.3.  So 65 rows (94.7, 83.0 and 49.8)
+// take more than two calls of half of them would, up to about 128.
+constexpr int64_t FEW_ROWS = 64;
 
 // Row g (lanes 16 g .. 16 g + 15) of r[t] holds X[g][t]; afterwards row g of
 // r[p] holds X[p][g].
@@ -823,13 +829,16 @@ FfnPlan ffn_plan(int type, int64_t M, int64_t N, int64_t K, int cus) {
     return p;
   }
   if (p.few) {
-    // Up to 16 rows here have long rows (more than STREAM_K columns): eight waves,
-    // and the wider tile once a CU has more than one of the narrow.  Above, four
-    // waves of one tile, whose registers let two workgroups share a CU with four
-    // blocks of x in flight (38 rows of 9216 x 3072: 32.4 us; six waves 41.7, two
-    // tiles 39.8, two blocks in flight 38.5 and 34.6).
+    // Up to 16 rows here have long rows (more than STREAM_K columns): eight waves.
+    // Nine to sixteen take the wider tile once a CU has more than one of the narrow,
+    // which then read x again (16 float32 rows, narrow and wide, us: 9216 x 5120 54.3
+    // and 46.2, 4112 x 8192 57.2 and 38.6, but 4096 x 8192 32.0 and 38.4; 8 rows 30.9
+    // and 35.8, 31.5 and 29.3, 21.4 and 29.3; one row 19.4 and 27.4, 19.5 and 22.0).
+    // Above, four waves of one tile, whose registers let two workgroups share a CU
+    // with four blocks of x in flight (38 rows of 9216 x 3072: 32.4 us; six waves
+    // 41.7, two tiles 39.8, two blocks in flight 38.5 and 34.6).
     const int64_t chunks = (K + 255) / 256;
-    p.nt = p.rt == 1 && (N + 15) / 16 > cus ? 2 : 1;
+    p.nt = p.rt == 1 && M > 8 && (N + 15) / 16 > cus ? 2 : 1;
     p.waves = static_cast<int>(std::min<int64_t>(chunks, p.rt == 1 ? FW : 4));
     if (p.rt == 1) return p;
   }
@@ -932,16 +941,15 @@ hipError_t launch_ffn(const FfnArgs& a, int cus) {
         hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * p.waves), lds, a.stream, a.gate, a.up,
                            RT == 1 ? a.x : static_cast<const void*>(xa), inv, a.K, o);
       };
-      auto cols = [&](auto rt, auto vr) {
-        if (decltype(rt)::value > 1 || p.nt == 1) launch(rt, Int<1>{}, vr);
-        else launch(Int<1>{}, Int<2>{}, vr);
-      };
-      if (a.M <= 4) cols(Int<1>{}, Int<1>{});
-      else if (a.M <= 8) cols(Int<1>{}, Int<2>{});
-      else if (a.M <= 16) cols(Int<1>{}, Int<4>{});
-      else if (a.M <= 32) cols(Int<2>{}, Int<4>{});
-      else if (a.M <= 48) cols(Int<3>{}, Int<4>{});
-      else cols(Int<4>{}, Int<4>{});
+      const Int<1> one;
+      const Int<4> four;
+      if (a.M <= 4) launch(one, one, one);
+      else if (a.M <= 8) launch(one, one, Int<2>{});
+      else if (a.M <= 16 && p.nt == 1) launch(one, one, four);
+      else if (a.M <= 16) launch(one, Int<2>{}, four);
+      else if (a.M <= 32) launch(Int<2>{}, one, four);
+      else if (a.M <= 48) launch(Int<3>{}, one, four);
+      else launch(four, one, four);
     });
     return hipGetLastError();
   }
