@@ -451,12 +451,13 @@ enum { Q4_ACT_SILU = 0, Q4_ACT_GELU = 1 };  /* g * sigmoid(g); gelu in its tanh 
  *   1 <= M <= 2^20, 1 <= N <= 2097152, K a positive multiple of 32 up to
  *   4194304, M*N and M*K below 2^33, N*K below 2^33.
  *   workspace : q4_gated_ffn_workspace_bytes(type, M, N, K) bytes of device
- *           scratch (0 for few rows: NULL allowed); its contents do not
+ *           scratch (0 up to 16 rows: NULL allowed); its contents do not
  *           matter.  Calls that share it must be ordered.
  * Exact codes on the matrix cores, each block's scale applied in float32,
- * float32 sums.  x enters exactly (float32 as bfloat16 parts), or above 64 rows
- * scaled per row by a power of two into binary16 (float32 rows as two parts):
- * to 2^-22 of an element or 2^-39 of its row's largest.  Deterministic; an
+ * float32 sums.  x enters in binary16, float16 as it is, float32 as two parts
+ * and bfloat16 as one, both scaled by a power of two per 128 or 256 columns of a
+ * row up to 16 rows and per row above: to 2^-22 of a float32 element, bfloat16
+ * exactly, or to 2^-39 of the largest that shares its scale.  Deterministic; an
  * infinity or NaN in a row of x gives non-finite values in that row only.
  */
 size_t q4_gated_ffn_workspace_bytes(int32_t type, int64_t M, int64_t N, int64_t K);

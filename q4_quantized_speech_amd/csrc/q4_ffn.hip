@@ -645,8 +645,8 @@ __global__ __launch_bounds__(256) void ffn_codes_kernel(const uint8_t* __restric
   scale[f * 16 + i] = half_bits_to_float(d);
 }
 
-// Measured: 1500 x 2 x 9216 x 3072 bfloat16, with g and u kept, 237 to 247 us in a
-// trace from a cold start; the call with prep_rows and ffn_codes 252.  A block's
+// Measured: 1500 x 2 x 9216 x 3072 bfloat16, with g and u kept, 237 to 248 us in a
+// trace from a cold start; the call with prep_rows and ffn_codes 253.  A block's
 // scale costs as many vector cycles (four FMAs) as its product costs the matrix
 // cores, and the two hardly overlap: that call without three of the four FMAs took
 // 210 us, with the loads always of one block 244, against 253.  432 tiles on 256
@@ -684,7 +684,7 @@ void ffn_gemm_kernel(const f16x8* __restrict__ A, const f16x8* __restrict__ Q,
 // magnitudes are below 1.13 max|dh| max|z| (act' of either activation is below
 // 1.13, |act(g)| at most |g|).  A bound that is too high by 2^b only costs values
 // 2^-(39 - b) times it.
-// Measured: 76 rows of 9216 float32 4.7 us, 1500 of 5120 bfloat16 8.4.
+// Measured: 76 rows of 9216 float32 4.9 us, 1500 of 5120 bfloat16 9.7.
 constexpr int BOUND_WAVES = 16;
 template <typename T>
 __global__ __launch_bounds__(64 * BOUND_WAVES) void ffn_bound_kernel(const T* __restrict__ z,
@@ -734,9 +734,9 @@ __global__ __launch_bounds__(64 * BOUND_WAVES) void ffn_bound_kernel(const T* __
 // dg and du as operand fragments (NATURAL over the columns) of two parts whatever
 // the type, and where the caller wants them in dz: one part, 11 bits, would be
 // below bfloat16's own rounding for a term but not for a sum whose terms cancel
-// (random terms: dx 8.6e-4 from the exact one rounded, two parts 6e-5).  A wave
+// (random terms: dx 8.6e-4 from the exact one rounded, two parts 3e-5).  A wave
 // takes 16 rows of 32 columns.
-// Measured: 76 x 9216 float32 7.3 us, 1500 x 5120 bfloat16 14 (77 MB: 5.5 TB/s).
+// Measured: 76 x 9216 float32 7.3 us, 1500 x 5120 bfloat16 18 (107 MB: 5.8 TB/s).
 template <int ACT, typename T>
 __global__ __launch_bounds__(256) void ffn_dz_kernel(const T* z, const T* __restrict__ dh, T* dz,
                                                      const float* __restrict__ inv,

@@ -840,8 +840,9 @@ template <int RT, int PA, int PB, typename T, bool ODD, bool TWO>
 __global__ __launch_bounds__(64 * TW) __attribute__((amdgpu_waves_per_eu(2, RT <= 1 ? 4 : 2)))
 void gemm_transposed_kernel(const f16x8* __restrict__ G1, const f16x8* __restrict__ G2,
                             const uint8_t* __restrict__ W1, const uint8_t* __restrict__ W2,
-                            int splits, int64_t n0, int64_t N, int64_t M, int64_t K, int64_t CB, int mtiles, int tiles,
-                            int64_t span, float* __restrict__ part, const float* __restrict__ alpha,
+                            int splits, int64_t n0, int64_t N, int64_t M, int64_t K, int64_t CB,
+                            int mtiles, int tiles, int64_t span, float* __restrict__ part,
+                            const float* __restrict__ alpha,
                             const float* __restrict__ inv, T* __restrict__ out) {
   constexpr int RP = RT > 2 ? 2 : RT;  // row blocks added at a time (of three the last one alone)
   static_assert(RT <= TW / 2, "two waves finish a row block");

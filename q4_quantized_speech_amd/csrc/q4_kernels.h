@@ -121,8 +121,8 @@ struct TeacherArgs {
 };
 size_t xent_workspace_bytes(int type, bool grad, int64_t M, int64_t N, int64_t K, int64_t top, int cus);
 hipError_t launch_xent(const uint8_t* w, const void* x, const int32_t* targets,
-                       const TeacherArgs* teacher, const float* dloss, float* loss, float* lse, void* dx, int type, int64_t M, int64_t N, int64_t K,
-                       void* ws, int cus, hipStream_t s);
+                       const TeacherArgs* teacher, const float* dloss, float* loss, float* lse, void* dx,
+                       int type, int64_t M, int64_t N, int64_t K, void* ws, int cus, hipStream_t s);
 
 // Verification of drafted tokens (arguments as in q4_verify_draft).
 struct VerifyArgs {
