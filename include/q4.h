@@ -514,8 +514,9 @@ q4_status q4_gated_ffn_grad(const void* w_gate, const void* w_up, const void* z,
  * and p - q of each of them are formed in float64 from the float32 logits, 1 - p
  * and 1 - q of a token with q above one half from the sums of the others: a
  * student near its teacher, or as sure as it, keeps the precision of the
- * difference.  The other probabilities are kept relative to their largest and
- * rounded as in q4_lmhead_xent.  |deq(T)| must stay below
+ * difference (the loss to some 2^-48 temperature^2 beside the logits' errors).
+ * The other probabilities are kept relative to their largest and rounded as in
+ * q4_lmhead_xent.  |deq(T)| must stay below
  * 65504 for dx.  Deterministic; a row of x that holds an infinity or NaN, or
  * one of top_logits that holds NaN or +inf in a present entry, gives
  * non-finite values in that row only.

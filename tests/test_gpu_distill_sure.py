@@ -73,7 +73,7 @@ def lean(w, at, margins, gen, noise=0.3):
 
 # (rows, table, columns, entries): to 64 rows straight from the table, above through unpacked codes
 SHAPES = [(12, 700, 256, 1), (40, 3000, 320, 1), (90, 1200, 256, 1), (5, 131072, 512, 1), (12, 700, 256, 9),
-          (64, 5000, 352, 33), (120, 2000, 256, 64)]
+          (64, 5000, 352, 33), (120, 2000, 256, 64), (3, 200, 20032, 5), (70, 300, 1280, 256)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
@@ -148,3 +148,15 @@ def test_student_at_its_teacher_has_no_loss(m, n, k, top, temp, dtype, grad):
     # hundred float32 exponentials, each within a few u, make up 1 - p
     below = temp ** 2 * (2.0 ** -45 if grad else 8 * U * (1 - likely))
     assert (loss.double() >= -below).all(), float((loss.double() / below).min())
+
+
+@pytest.mark.parametrize("temp", [2.0 ** -60, 2.0 ** -20, 1e-3, 64.0, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("m", [6, 70])
+def test_any_temperature(m, temp):
+    """The ends of the range, with and without the gradient (the checks of test_gpu_distill)."""
+    n, k, top = 900, 96, 17
+    wq, w = D.table(n, k, 700)
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn((m, k), device="cuda", generator=gen) * 4
+    ids, logits = D.teacher(m, n, top, 12)
+    D.check(wq, w, x, ids, logits, temp)
